@@ -8,8 +8,9 @@ Formats (both with one E8M0 scale 2**e per 32 elements along K):
 
 Slab layouts, R = rows rounded up to 256, rows past the last are zero:
   MXFP8  codes uint8 [K/64, R, 64], scales uint8 [K/64, R, 2]
-  MXFP4  codes uint8 [ceil(K/128), R, 64] (element 2b of a 128-K slab in the
-         low half of byte b, 2b + 1 in the high half), scales uint8
+  MXFP4  codes uint8 [ceil(K/128), R/16, 4, 16, 16]: slab, block of 16 rows,
+         group of 32 elements, row, byte (element 2b of the group in the low
+         half of byte b, 2b + 1 in the high half); scales uint8
          [ceil(K/128), R, 4]; groups past K are zero
 
 `own = False` computes each operator in elementary torch operations; `own =
@@ -176,14 +177,15 @@ def _pack4(v, e):
     byte = (code[..., 0::2] | (code[..., 1::2] << 4)).view(rows, groups * 16)
     q = torch.zeros((R, S * 64), dtype=torch.uint8, device=v.device)
     q[:rows, : groups * 16] = byte
+    q = q.view(R // 16, 16, S, 4, 16).permute(2, 0, 3, 1, 4).contiguous()
     s = torch.zeros((R, S * 4), dtype=torch.uint8, device=v.device)
     s[:rows, :groups] = (e + 127).to(torch.uint8)
-    return (q.view(R, S, 64).transpose(0, 1).contiguous(), s.view(R, S, 4).transpose(0, 1).contiguous())
+    return q, s.view(R, S, 4).transpose(0, 1).contiguous()
 
 
 def _unpack4(q, s, rows, K):
     """Values of an MXFP4 slab, float32 [rows, K]."""
-    b = q[:, :rows].transpose(0, 1).reshape(rows, -1)[:, : K // 2]
+    b = q.permute(1, 3, 0, 2, 4).reshape(q.shape[1] * 16, -1)[:rows, : K // 2]
     code = torch.stack((b & 15, b >> 4), dim=-1).view(rows, K)
     m = (code & 7).to(torch.float32)
     a = torch.where(m < 4, m / 2, torch.where(m < 6, m - 2, 2 * m - 8))
@@ -311,7 +313,7 @@ def _exact_weights(st, N, K):
     q, s = st["wq"], st["ws"]
     for k0 in range(0, K, 128):
         n = min(128, K - k0)
-        b = q[k0 // 128, :N, : n // 2].to(torch.int64)
+        b = torch.cat([q[k0 // 128, :, c].reshape(-1, 16) for c in range(n // 32)], dim=1)[:N].to(torch.int64)
         sc = _exact_pow2(s[k0 // 128, :N, : n // 32].to(torch.int64) - 127).repeat_interleave(GROUP, dim=1)
         out[:, k0 : k0 + n : 2] = table[b & 15]
         out[:, k0 + 1 : k0 + n : 2] = table[b >> 4]
