@@ -53,6 +53,8 @@
 extern "C" {
 #endif
 
+/* Changes with the signature or meaning of a declared call; entry points
+ * added beside the others (the MXFP4 and norm calls) leave it. */
 #define MX_ABI_VERSION 12
 
 typedef enum {
@@ -502,6 +504,111 @@ int mx_pc_quantize_weight_slab(const void* w, int wdtype, int64_t N, int64_t K, 
 int mx_pc_linear_slab(const uint8_t* xq, const float* xs, int64_t M, int64_t K,
                       const uint8_t* wq, const float* ws, int64_t N,
                       const void* bias, int epilogue, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4: 4-bit microscaled elements. As the MXFP8 rule above with E2M1
+ * elements (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6; bit 3 the sign):
+ *   e      = clamp(floor(log2 amax) - 2, -127, 127)   (amax = 0 gives -127)
+ *   code_i = E2M1(x_i * 2^-e), round to nearest even after saturating to +-6;
+ *            the sign of zero is kept
+ *   A group holding NaN or Inf gets scale 0xFF and every code 7; its elements
+ *   are NaN (E2M1 has none of its own, the scale alone marks them).
+ * The slab layout of an operand of `rows` rows, with R = mx_slab_rows(rows)
+ * and S = ceil(K / 128):
+ *   codes   q  uint8 [S][R/16][4][16][16]   slab, block of 16 rows, group of 32
+ *              elements, row, byte: element 2b of the group in the low half of
+ *              byte b, element 2b + 1 in the high half
+ *   scales  s  uint8 [S][R][4]
+ * K is any multiple of 32; groups past K and rows past the last are zero
+ * (codes and scales). A 1 KB block of a slab is what a wave's lanes take as
+ * one MFMA operand, in lane order.
+ * ------------------------------------------------------------------------ */
+
+/* Format of a linear's activations (its slab operand, or what bf16 rows are
+ * quantized to): MXFP8 (slab of mx_quantize_act_slab, K % 64 == 0) or MXFP4
+ * (slab of mx_fp4_quantize_act_slab, K % 32 == 0). */
+typedef enum { MX_ACT_FP8 = 0, MX_ACT_FP4 = 1 } mx_act_format;
+
+/* MXFP4 quantization of bf16 activations x [M][ldx] (ldx >= K, ldx % 8 == 0,
+ * K % 32 == 0) and of f32 or bf16 weights w [N][ldw] (ldw * sizeof(element) %
+ * 16 == 0) into slabs. Rows and codes 16-byte aligned, scales 4-byte aligned;
+ * outputs must not overlap an input or each other. */
+int mx_fp4_quantize_act_slab(const void* x, int64_t M, int64_t K, int64_t ldx,
+                             uint8_t* q, uint8_t* s, void* stream);
+int mx_fp4_quantize_weight_slab(const void* w, int wdtype, int64_t N, int64_t K, int64_t ldw,
+                                uint8_t* q, uint8_t* s, void* stream);
+
+/* The values of an MXFP4 slab, row-major: y [rows][ldy] of type ydtype
+ * (MX_DT_BF16 or MX_DT_F32; ldy * sizeof(element) % 16 == 0). Exact wherever
+ * the value is finite in that type (scales from 2^125 on can overflow to
+ * infinity); NaN groups give NaN. Columns K .. ldy-1 are left as they are. */
+int mx_fp4_dequantize_slab(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K,
+                           void* y, int ydtype, int64_t ldy, void* stream);
+
+/* Row-major packed codes q [rows][K/2] (element 2b of a row in the low half
+ * of byte b) and scales s [rows][K/32], e.g. weights stored quantized, to the
+ * slab layout. Codes 16-byte aligned, slab scales 4-byte aligned; outputs
+ * must not overlap inputs. */
+int mx_fp4_slab_pack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K,
+                     uint8_t* qslab, uint8_t* sslab, void* stream);
+
+/* An MXFP4 slab as the MXFP8 slab of the same values: every E2M1 value is an
+ * E4M3 one, so the codes change and the scales stay; a NaN group gets codes
+ * 0x7F. K % 64 == 0. */
+int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K,
+                       uint8_t* q8, uint8_t* s8, void* stream);
+
+/* The linear on MXFP4 weights:
+ *   y[m][n] = bf16_rne( epi( sum_k xhat[m][k] * what[n][k] + f32(bias[n]) ) )
+ * with xhat the values of an MXFP4 or MXFP8 activation slab (act), what those
+ * of the MXFP4 weight slab wq, ws (R = mx_slab_rows(N)). Products are exact,
+ * sums FP32. bias f16 [N] or NULL; y bf16 [M][N]; N % 16 == 0 (else
+ * MX_ERR_UNSUPPORTED). Codes and y 16-byte aligned, scales 4-byte aligned; y
+ * must not overlap an input. The kernel is chosen by the shape and the format
+ * alone, so results are deterministic. workspace: mx_fp4_linear_slab_ws_bytes
+ * bytes, 256-byte aligned, overlapping no operand or output (NULL when that
+ * is 0); its contents are overwritten and need no initial value. Nothing is
+ * allocated. */
+int64_t mx_fp4_linear_slab_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
+int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+                       const uint8_t* wq, const uint8_t* ws, int64_t N,
+                       const void* bias, int epilogue, void* y,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same in one call: bf16 activations x [M][ldx] (ldx >= K, ldx % 8 == 0)
+ * quantized to MXFP4 or MXFP8 (act) at run time, then the product. Up to 16
+ * tokens are quantized inside the product's kernel (one launch, no
+ * workspace); more go through a slab in the workspace
+ * (mx_fp4_linear_ws_bytes bytes, 256-byte aligned, overlapping no argument). */
+int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
+int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx,
+                  const uint8_t* wq, const uint8_t* ws, int64_t N,
+                  const void* bias, int epilogue, int act, void* y,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * RMS norm with the residual's addition, written as the next quantized
+ * linear's activation slab:
+ *   h    = x + residual, rounded to the residual's type (h = x without one)
+ *   y    = bf16_rne( h * weight / sqrt(mean_k h^2 + eps) )
+ *   q, s = the MX quantization of y (act: MXFP8 or MXFP4), bit-identical to
+ *          mx_quantize_act_slab / mx_fp4_quantize_act_slab of y
+ * The mean and the product are computed in f64 and rounded once (through f32)
+ * to bf16. A row holding NaN or Inf, or an all-zero row with eps = 0, gives
+ * what the formula gives in floating point (NaN groups).
+ * x: bf16 [M][ldx]; residual: bf16 or f32 (rdtype) [M][ldr], or NULL; weight:
+ * bf16 or f32 (wdtype) [K], or NULL for ones; eps >= 0 and finite;
+ * residual_out (h): of the residual's type [M][ldo], or NULL to drop it; it may
+ * be the residual itself with the same pitch, and must otherwise overlap
+ * nothing; y: bf16 [M][ldy], or NULL to drop it; q, s: the slab. rdtype and
+ * wdtype are ignored for NULL pointers. Every buffer 16-byte aligned, rows a
+ * multiple of 16 bytes apart. K as the format requires, at most 65536, M at
+ * most 2^22 (else MX_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr,
+                    const void* weight, int wdtype, double eps, int64_t M, int64_t K,
+                    void* residual_out, int64_t ldo, void* y, int64_t ldy,
+                    int act, uint8_t* q, uint8_t* s, void* stream);
 
 #ifdef __cplusplus
 }

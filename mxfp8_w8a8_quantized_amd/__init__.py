@@ -23,6 +23,9 @@ MX_EPI_NONE = 0
 MX_EPI_GELU_TANH = 1
 MX_DT_BF16 = 0
 MX_DT_F32 = 1
+MX_ACT_FP8 = 0
+MX_ACT_FP4 = 1
+ACT_FORMATS = {"fp8": MX_ACT_FP8, "fp4": MX_ACT_FP4}
 MX_PLAN_SLAB = 0
 MX_PLAN_SPLITK = 1
 MX_PLAN_SMALL = 2
@@ -76,6 +79,17 @@ SIGNATURES = {
     "mx_pc_quantize_act_slab": ([_P, _I64, _I64, _I64, _P, _P, _P], _INT),
     "mx_pc_quantize_weight_slab": ([_P, _INT, _I64, _I64, _I64, _P, _P, _P], _INT),
     "mx_pc_linear_slab": ([_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P], _INT),
+    "mx_fp4_quantize_act_slab": ([_P, _I64, _I64, _I64, _P, _P, _P], _INT),
+    "mx_fp4_quantize_weight_slab": ([_P, _INT, _I64, _I64, _I64, _P, _P, _P], _INT),
+    "mx_fp4_dequantize_slab": ([_P, _P, _I64, _I64, _P, _INT, _I64, _P], _INT),
+    "mx_fp4_slab_pack": ([_P, _P, _I64, _I64, _P, _P, _P], _INT),
+    "mx_fp4_slab_unpack": ([_P, _P, _I64, _I64, _P, _P, _P], _INT),
+    "mx_fp4_linear_slab_ws_bytes": ([_I64, _I64, _I64, _INT], _I64),
+    "mx_fp4_linear_slab": ([_INT, _P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P, _I64, _P], _INT),
+    "mx_fp4_linear_ws_bytes": ([_I64, _I64, _I64, _INT], _I64),
+    "mx_fp4_linear": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _P], _INT),
+    "mx_rmsnorm_slab": ([_P, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P,
+                         _P, _P], _INT),
 }
 
 
@@ -749,3 +763,258 @@ def mx_linear_noalloc(x, w, bias=None, gelu=False, y=None):
         _check(lib().mx_linear_noalloc(_ptr(x), M, K, ld, _ptr(w.q), _ptr(w.s), N, _ptr(bias), epi, _ptr(y),
                                        _stream(dev)))
     return y
+
+
+class FP4Slab(NamedTuple):
+    """An MXFP4 operand in the slab layout: codes q uint8 [S, R/16, 4, 16, 16]
+    and scales s uint8 [S, R, 4], S = ceil(K/128), R = mx_slab_rows(rows);
+    rows past `rows` and groups past K are zero."""
+
+    q: torch.Tensor
+    s: torch.Tensor
+    rows: int
+    K: int
+
+
+def _fp4_shapes(rows, K):
+    S, R = (K + 127) // 128, (rows + 255) // 256 * 256
+    return (S, R // 16, 4, 16, 16), (S, R, 4)
+
+
+def _fp4_out(rows, K, dev, out):
+    sq, ss = _fp4_shapes(rows, K)
+    if out is None:
+        return FP4Slab(torch.empty(sq, dtype=torch.uint8, device=dev), torch.empty(ss, dtype=torch.uint8, device=dev),
+                       rows, K)
+    _need_fp4(out, "out", dev)
+    if out.rows != rows or out.K != K:
+        raise ValueError(f"out must hold {rows} rows of K = {K}")
+    return out
+
+
+def _need_fp4(t, name, dev):
+    if not isinstance(t, FP4Slab):
+        raise TypeError(f"{name} must be an FP4Slab")
+    _need(t.q, name + ".q", torch.uint8, dev)
+    _need(t.s, name + ".s", torch.uint8, dev)
+    if (t.q.shape, t.s.shape) != _fp4_shapes(t.rows, t.K):
+        raise ValueError(f"{name} is not an MXFP4 slab of {t.rows} rows and K = {t.K}")
+
+
+def _act_format(act):
+    if act not in ACT_FORMATS:
+        raise ValueError(f"act must be 'fp8' or 'fp4', got {act!r}")
+    return ACT_FORMATS[act]
+
+
+def _need_rows(x, name, dtypes):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in dtypes:
+        raise TypeError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+
+
+def _pitch(x):
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+_DTYPES = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
+
+
+def _run(fn, dev, *args):
+    """Calls fn(*args, stream) with `dev` the current device."""
+    if torch.cuda.current_device() == dev.index:  # the usual case: no switch
+        _check(fn(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)))
+
+
+def _fp4_quantize(x, name, dtypes, out):
+    _need_rows(x, name, dtypes)
+    rows, K = x.shape
+    if K == 0 or K % 32 != 0:
+        raise ValueError("MXFP4 needs K to be a positive multiple of 32")
+    return _fp4_out(rows, K, x.device, out)
+
+
+def mx_fp4_quantize_act_slab(x, out=None):
+    """bf16 [M, K] (rows may be strided, K % 32 == 0) -> FP4Slab of its MXFP4 codes and scales."""
+    out = _fp4_quantize(x, "x", (torch.bfloat16,), out)
+    _run(lib().mx_fp4_quantize_act_slab, x.device, _ptr(x), x.shape[0], x.shape[1], _pitch(x), _ptr(out.q), _ptr(out.s))
+    return out
+
+
+def mx_fp4_quantize_weight_slab(w, out=None):
+    """fp32 or bf16 [N, K] (K % 32 == 0) -> FP4Slab of its MXFP4 codes and scales."""
+    out = _fp4_quantize(w, "w", (torch.float32, torch.bfloat16), out)
+    _run(lib().mx_fp4_quantize_weight_slab, w.device, _ptr(w), _DTYPES[w.dtype], w.shape[0], w.shape[1], _pitch(w),
+         _ptr(out.q), _ptr(out.s))
+    return out
+
+
+def mx_fp4_dequantize_slab(slab, y=None, dtype=torch.bfloat16):
+    """The values of an FP4Slab as y [rows, K] (bf16 or fp32; rows may be
+    strided; allocated with `dtype` when None)."""
+    dev = slab.q.device
+    _need_fp4(slab, "slab", dev)
+    if y is None:
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be bfloat16 or float32")
+        y = torch.empty((slab.rows, slab.K), dtype=dtype, device=dev)
+    _need_rows(y, "y", (torch.bfloat16, torch.float32))
+    if y.device != dev or tuple(y.shape) != (slab.rows, slab.K):
+        raise ValueError(f"y must be [{slab.rows}, {slab.K}] on {dev}")
+    _run(lib().mx_fp4_dequantize_slab, dev, _ptr(slab.q), _ptr(slab.s), slab.rows, slab.K, _ptr(y), _DTYPES[y.dtype],
+         _pitch(y))
+    return y
+
+
+def mx_fp4_slab_pack(q, s, out=None):
+    """Row-major packed codes uint8 [rows, K/2] (element 2b of a row in the
+    low half of byte b) and scales uint8 [rows, K/32] -> FP4Slab."""
+    dev = q.device
+    _need(q, "q", torch.uint8, dev)
+    _need(s, "s", torch.uint8, dev)
+    if q.dim() != 2 or q.shape[1] == 0 or q.shape[1] % 16 != 0:
+        raise ValueError("q must be [rows, K/2] with K a positive multiple of 32")
+    rows, K = q.shape[0], 2 * q.shape[1]
+    if s.shape != (rows, K // 32):
+        raise ValueError("s must be [rows, K/32]")
+    out = _fp4_out(rows, K, dev, out)
+    _run(lib().mx_fp4_slab_pack, dev, _ptr(q), _ptr(s), rows, K, _ptr(out.q), _ptr(out.s))
+    return out
+
+
+def mx_fp4_slab_unpack(slab, out=None):
+    """An FP4Slab as the MXFP8 Slab of the same values (K % 64 == 0)."""
+    dev = slab.q.device
+    _need_fp4(slab, "slab", dev)
+    if slab.K % 64 != 0:
+        raise ValueError("the MXFP8 slab layout needs K % 64 == 0")
+    out = _slab_out(slab.rows, slab.K, dev, out)
+    _run(lib().mx_fp4_slab_unpack, dev, _ptr(slab.q), _ptr(slab.s), slab.rows, slab.K, _ptr(out.q), _ptr(out.s))
+    return out
+
+
+def _fp4_linear_out(M, w, bias, y, dev):
+    _need_fp4(w, "w", dev)
+    if bias is not None:
+        _need(bias, "bias", torch.float16, dev)
+        if bias.shape != (w.rows,):
+            raise ValueError("bias must be f16 [N]")
+    if y is None:
+        return torch.empty((M, w.rows), dtype=torch.bfloat16, device=dev)
+    _need(y, "y", torch.bfloat16, dev)
+    if tuple(y.shape) != (M, w.rows):
+        raise ValueError("y must be bf16 [M, N]")
+    return y
+
+
+def _fp4_workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty((need,), dtype=torch.uint8, device=dev) if need > 0 else None
+    _need(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def mx_fp4_linear_slab_ws_bytes(M, K, N, act="fp4"):
+    return lib().mx_fp4_linear_slab_ws_bytes(M, K, N, _act_format(act))
+
+
+def mx_fp4_linear_slab(x, w, bias=None, gelu=False, y=None, workspace=None):
+    """y = bf16(epi(xhat @ what^T + bias)) on an activation slab x (FP4Slab,
+    or Slab for MXFP8 activations) and MXFP4 weights w (FP4Slab). workspace:
+    uint8 of at least mx_fp4_linear_slab_ws_bytes bytes (allocated here when
+    None and needed)."""
+    if not isinstance(x, (FP4Slab, Slab)):
+        raise TypeError("x must be an FP4Slab or a Slab")
+    dev = x.q.device
+    if isinstance(x, FP4Slab):
+        act = "fp4"
+        _need_fp4(x, "x", dev)
+    else:
+        act = "fp8"
+        _need(x.q, "x.q", torch.uint8, dev)
+        _need(x.s, "x.s", torch.uint8, dev)
+        R = (x.rows + 255) // 256 * 256
+        if x.q.shape != (x.K // 64, R, 64) or x.s.shape != (x.K // 64, R, 2):
+            raise ValueError(f"x is not a slab of {x.rows} rows and K = {x.K}")
+    M, K = x.rows, x.K
+    y = _fp4_linear_out(M, w, bias, y, dev)
+    if w.K != K:
+        raise ValueError(f"x has K = {K}, w has K = {w.K}")
+    workspace = _fp4_workspace(workspace, lib().mx_fp4_linear_slab_ws_bytes(M, K, w.rows, ACT_FORMATS[act]), dev)
+    _run(lib().mx_fp4_linear_slab, dev, ACT_FORMATS[act], _ptr(x.q), _ptr(x.s), M, K, _ptr(w.q), _ptr(w.s), w.rows,
+         _ptr(bias), MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, _ptr(y), _ptr(workspace),
+         0 if workspace is None else workspace.numel())
+    return y
+
+
+def mx_fp4_linear_ws_bytes(M, K, N, act="fp4"):
+    return lib().mx_fp4_linear_ws_bytes(M, K, N, _act_format(act))
+
+
+def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None):
+    """The linear on MXFP4 weights in one call (mx.h mx_fp4_linear): bf16 x
+    [M, K] (rows may be strided) is quantized to MXFP4 (act="fp4") or MXFP8
+    (act="fp8") and multiplied by the FP4Slab w. workspace: uint8 of at least
+    mx_fp4_linear_ws_bytes(M, K, N, act) bytes (allocated here when None and
+    needed; none up to 16 tokens)."""
+    fmt = _act_format(act)
+    _need_rows(x, "x", (torch.bfloat16,))
+    dev = x.device
+    M, K = x.shape
+    y = _fp4_linear_out(M, w, bias, y, dev)
+    if w.K != K:
+        raise ValueError(f"x has K = {K}, w has K = {w.K}")
+    workspace = _fp4_workspace(workspace, lib().mx_fp4_linear_ws_bytes(M, K, w.rows, fmt), dev)
+    _run(lib().mx_fp4_linear, dev, _ptr(x), M, K, _pitch(x), _ptr(w.q), _ptr(w.s), w.rows, _ptr(bias),
+         MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, fmt, _ptr(y), _ptr(workspace),
+         0 if workspace is None else workspace.numel())
+    return y
+
+
+def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None, residual_out=None, y=None):
+    """h = x + residual, then the RMS norm of h as the activation slab of a
+    quantized linear (mx.h mx_rmsnorm_slab): returns (slab, h).
+
+    x: bf16 [M, K]; residual: bf16 or fp32 [M, K] or None; weight: bf16 or
+    fp32 [K] or None (ones); rows of x, residual, residual_out and y may be
+    strided. act: "fp8" gives a Slab (mx_linear_slab and its kin, and
+    mx_fp4_linear_slab), "fp4" an FP4Slab. residual_out: h goes here
+    (allocated when None and there is a residual; may be `residual` itself); h
+    is None without a residual. y: bf16 [M, K] that also receives the norm, if
+    given."""
+    fmt = _act_format(act)
+    _need_rows(x, "x", (torch.bfloat16,))
+    dev = x.device
+    M, K = x.shape
+    if K == 0 or K % (32 if act == "fp4" else 64) != 0:
+        raise ValueError("K must be a positive multiple of 32 (fp4) or 64 (fp8)")
+    rdt = wdt = 0
+    if residual is not None:
+        _need_rows(residual, "residual", (torch.bfloat16, torch.float32))
+        rdt = _DTYPES[residual.dtype]
+        if residual_out is None:
+            residual_out = torch.empty((M, K), dtype=residual.dtype, device=dev)
+        _need_rows(residual_out, "residual_out", (residual.dtype,))
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        if weight.dtype not in _DTYPES:
+            raise TypeError("weight must be bfloat16 or float32")
+        _need(weight, "weight", weight.dtype, dev)
+        if tuple(weight.shape) != (K,):
+            raise ValueError(f"weight must be [{K}]")
+        wdt = _DTYPES[weight.dtype]
+    if y is not None:
+        _need_rows(y, "y", (torch.bfloat16,))
+    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
+        if t is not None and (t.device != dev or t.shape != x.shape):
+            raise ValueError(f"{name} must be [{M}, {K}] on {dev}")
+    out = _fp4_out(M, K, dev, out) if act == "fp4" else _slab_out(M, K, dev, out)
+    _run(lib().mx_rmsnorm_slab, dev, _ptr(x), _pitch(x), _ptr(residual), rdt, 0 if residual is None else _pitch(residual),
+         _ptr(weight), wdt, float(eps), M, K, _ptr(residual_out), 0 if residual_out is None else _pitch(residual_out),
+         _ptr(y), 0 if y is None else _pitch(y), fmt, _ptr(out.q), _ptr(out.s))
+    return out, residual_out

@@ -935,3 +935,302 @@ int mx_linear_noalloc(const void* x, int64_t M, int64_t K, int64_t ldx, const ui
 }
 
 }  // extern "C"
+
+/* ---- MXFP4: quantizers and linears; RMS norm into a slab ---- */
+
+namespace {
+
+// Bytes of an MXFP4 slab of R (padded) rows.
+uint64_t fp4_code_bytes(int64_t R, int64_t K) { return (uint64_t)R * ((K + 127) / 128) * 64; }
+uint64_t fp4_scale_bytes(int64_t R, int64_t K) { return (uint64_t)R * ((K + 127) / 128) * 4; }
+
+// A slab operand of the given activation format.
+uint64_t act_code_bytes(int act, int64_t R, int64_t K) {
+  return act == MX_ACT_FP4 ? fp4_code_bytes(R, K) : (uint64_t)R * K;
+}
+uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
+  return act == MX_ACT_FP4 ? fp4_scale_bytes(R, K) : (uint64_t)R * (K / 32);
+}
+
+// Most tokens of the few-token kernel; more go through the tiled GEMMs.
+constexpr int64_t kFp4FewTokens = int64_t(1) << 30;
+
+int check_act_k(int act, int64_t K) {
+  if (act != MX_ACT_FP8 && act != MX_ACT_FP4) return fail(MX_ERR_INVALID_ARGUMENT, "unknown activation format %d", act);
+  const int st = check_k(K);
+  if (st != MX_OK) return st;
+  if (act == MX_ACT_FP8 && K % 64 != 0)
+    return fail(MX_ERR_INVALID_ARGUMENT, "K = %lld must be a multiple of 64 for MXFP8 activations", (long long)K);
+  return MX_OK;
+}
+
+bool bad_fp4_shape(int64_t M, int64_t K, int64_t N, int act) {
+  return M < 0 || N < 0 || K < 32 || K % 32 != 0 || M > kMaxRows || N > kMaxKN || K > kMaxKN ||
+         (act != MX_ACT_FP8 && act != MX_ACT_FP4) || (act == MX_ACT_FP8 && K % 64 != 0);
+}
+
+// Everything of an MXFP4-weight linear but its token operand.
+int check_fp4_linear(int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias,
+                     int epilogue, int act, const void* y) {
+  int st;
+  if ((st = check_rows("M", M)) != MX_OK) return st;
+  if ((st = check_act_k(act, K)) != MX_OK) return st;
+  if (N < 0) return fail(MX_ERR_INVALID_ARGUMENT, "N = %lld is negative", (long long)N);
+  if (N > kMaxKN) return fail(MX_ERR_UNSUPPORTED, "N = %lld exceeds the supported 2^20", (long long)N);
+  if (epilogue != MX_EPI_NONE && epilogue != MX_EPI_GELU_TANH)
+    return fail(MX_ERR_INVALID_ARGUMENT, "unknown epilogue %d", epilogue);
+  if (M == 0 || N == 0) return MX_OK;
+  if (N % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "N = %lld must be a multiple of 16", (long long)N);
+  if (wq == nullptr || ws == nullptr || y == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL weight or output pointer");
+  if (!aligned(wq, 16) || !aligned(y, 16) || !aligned(ws, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "codes and y must be 16-byte aligned, scales 4-byte aligned");
+  if (bias != nullptr && !aligned(bias, 2)) return fail(MX_ERR_INVALID_ARGUMENT, "bias must be 2-byte aligned");
+  return MX_OK;
+}
+
+// [out, out + bytes) meets a weight operand or the bias.
+bool overlaps_fp4_weights(const void* out, uint64_t bytes, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
+                          const void* bias) {
+  const int64_t RN = mx::slab_rows(N);
+  return overlap(out, bytes, wq, fp4_code_bytes(RN, K)) || overlap(out, bytes, ws, fp4_scale_bytes(RN, K)) ||
+         overlap(out, bytes, bias, (uint64_t)N * 2);
+}
+
+int check_fp4_quantize(const void* x, int dt, int64_t rows, int64_t K, int64_t ld, const uint8_t* q,
+                       const uint8_t* s) {
+  int st;
+  if (dt != MX_DT_BF16 && dt != MX_DT_F32) return fail(MX_ERR_INVALID_ARGUMENT, "unknown dtype %d", dt);
+  if ((st = check_rows("rows", rows)) != MX_OK) return st;
+  if ((st = check_k(K)) != MX_OK) return st;
+  const int64_t es = dt == MX_DT_F32 ? 4 : 2;
+  if (ld < K || (ld * es) % 16 != 0)
+    return fail(MX_ERR_INVALID_ARGUMENT, "pitch %lld must be >= K with 16-byte aligned rows", (long long)ld);
+  if (rows == 0) return MX_OK;
+  if (x == nullptr || q == nullptr || s == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "rows and codes must be 16-byte aligned, scales 4-byte aligned");
+  const int64_t R = mx::slab_rows(rows);
+  const uint64_t xbytes = ((uint64_t)(rows - 1) * ld + K) * es;
+  const uint64_t nq = fp4_code_bytes(R, K), ns = fp4_scale_bytes(R, K);
+  if (overlap(q, nq, x, xbytes) || overlap(s, ns, x, xbytes) || overlap(q, nq, s, ns))
+    return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap an input or each other");
+  return check_device();
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_fp4_quantize_act_slab(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, uint8_t* s, void* stream) {
+  const int st = check_fp4_quantize(x, MX_DT_BF16, M, K, ldx, q, s);
+  if (st != MX_OK || M == 0) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_quantize_slab(0, x, M, K, ldx, q, s, (hipStream_t)stream), "MXFP4 quantize launch");
+}
+
+int mx_fp4_quantize_weight_slab(const void* w, int wdtype, int64_t N, int64_t K, int64_t ldw, uint8_t* q, uint8_t* s,
+                                void* stream) {
+  const int st = check_fp4_quantize(w, wdtype, N, K, ldw, q, s);
+  if (st != MX_OK || N == 0) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_quantize_slab(wdtype == MX_DT_F32 ? 1 : 0, w, N, K, ldw, q, s, (hipStream_t)stream),
+                "MXFP4 quantize launch");
+}
+
+int mx_fp4_dequantize_slab(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, void* y, int ydtype,
+                           int64_t ldy, void* stream) {
+  const int st = check_fp4_quantize(y, ydtype, rows, K, ldy, q, s);  // the same operands, the other way
+  if (st != MX_OK || rows == 0) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_dequantize_slab(q, s, rows, K, ydtype == MX_DT_F32 ? 1 : 0, y, ldy, (hipStream_t)stream),
+                "MXFP4 dequantize launch");
+}
+
+int mx_fp4_slab_pack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, uint8_t* qslab, uint8_t* sslab,
+                     void* stream) {
+  int st;
+  if ((st = check_rows("rows", rows)) != MX_OK) return st;
+  if ((st = check_k(K)) != MX_OK) return st;
+  if (rows == 0) return MX_OK;
+  if (q == nullptr || s == nullptr || qslab == nullptr || sslab == nullptr)
+    return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(qslab, 16) || !aligned(sslab, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned, slab scales 4-byte aligned");
+  const int64_t R = mx::slab_rows(rows);
+  const uint64_t nq = (uint64_t)rows * (K / 2), ns = (uint64_t)rows * (K / 32);
+  const uint64_t oq = fp4_code_bytes(R, K), os = fp4_scale_bytes(R, K);
+  if (overlap(qslab, oq, q, nq) || overlap(qslab, oq, s, ns) || overlap(sslab, os, q, nq) ||
+      overlap(sslab, os, s, ns) || overlap(qslab, oq, sslab, os))
+    return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap an input or each other");
+  if ((st = check_device()) != MX_OK) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_slab_pack(q, s, rows, K, qslab, sslab, (hipStream_t)stream), "MXFP4 slab pack launch");
+}
+
+int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, uint8_t* q8, uint8_t* s8,
+                       void* stream) {
+  int st;
+  if ((st = check_rows("rows", rows)) != MX_OK) return st;
+  if ((st = check_act_k(MX_ACT_FP8, K)) != MX_OK) return st;
+  if (rows == 0) return MX_OK;
+  if (q == nullptr || s == nullptr || q8 == nullptr || s8 == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  if (!aligned(q, 16) || !aligned(q8, 16) || !aligned(s, 4) || !aligned(s8, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
+  const int64_t R = mx::slab_rows(rows);
+  const uint64_t nq = fp4_code_bytes(R, K), ns = fp4_scale_bytes(R, K);
+  const uint64_t oq = (uint64_t)R * K, os = (uint64_t)R * (K / 32);
+  if (overlap(q8, oq, q, nq) || overlap(q8, oq, s, ns) || overlap(s8, os, q, nq) || overlap(s8, os, s, ns) ||
+      overlap(q8, oq, s8, os))
+    return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap an input or each other");
+  if ((st = check_device()) != MX_OK) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_slab_unpack(q, s, rows, K, q8, s8, (hipStream_t)stream), "MXFP4 slab unpack launch");
+}
+
+int64_t mx_fp4_linear_slab_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
+  if (bad_fp4_shape(M, K, N, act)) return -1;
+  return 0;
+}
+
+int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* wq,
+                       const uint8_t* ws, int64_t N, const void* bias, int epilogue, void* y, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  int st = check_fp4_linear(M, K, wq, ws, N, bias, epilogue, act, y);
+  if (st != MX_OK || M == 0 || N == 0) return st;
+  if (xq == nullptr || xs == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL xq or xs");
+  if (!aligned(xq, 16) || !aligned(xs, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned, scales 4-byte aligned");
+  const int64_t RM = mx::slab_rows(M);
+  const uint64_t yb = (uint64_t)M * N * 2, xb = act_code_bytes(act, RM, K), sb = act_scale_bytes(act, RM, K);
+  if (overlap(y, yb, xq, xb) || overlap(y, yb, xs, sb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
+    return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
+  (void)workspace;
+  (void)workspace_bytes;
+  if ((st = check_device()) != MX_OK) return st;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y,
+                                          (hipStream_t)stream),
+                "MXFP4 linear launch");
+}
+
+int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
+  const int64_t slab = mx_fp4_linear_slab_ws_bytes(M, K, N, act);
+  if (slab < 0) return -1;
+  if (M == 0 || N == 0 || M <= mx::kFp4RowsMaxTokens) return 0;
+  const int64_t RM = mx::slab_rows(M);
+  return round256((int64_t)(act_code_bytes(act, RM, K) + act_scale_bytes(act, RM, K))) + slab;
+}
+
+int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq, const uint8_t* ws, int64_t N,
+                  const void* bias, int epilogue, int act, void* y, void* workspace, int64_t workspace_bytes,
+                  void* stream) {
+  int st = check_fp4_linear(M, K, wq, ws, N, bias, epilogue, act, y);
+  if (st != MX_OK || M == 0 || N == 0) return st;
+  if (x == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL x");
+  if (ldx < K || ldx % 8 != 0) return fail(MX_ERR_INVALID_ARGUMENT, "ldx = %lld must be >= K and a multiple of 8", (long long)ldx);
+  if (!aligned(x, 16)) return fail(MX_ERR_INVALID_ARGUMENT, "x must be 16-byte aligned");
+  const uint64_t xb = ((uint64_t)(M - 1) * ldx + K) * 2, yb = (uint64_t)M * N * 2;
+  if (overlap(y, yb, x, xb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
+    return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
+  const int64_t need = mx_fp4_linear_ws_bytes(M, K, N, act);
+  if (need > 0) {
+    if (workspace == nullptr || !aligned(workspace, 256))
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned and not NULL");
+    if (workspace_bytes < need)
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
+                  (long long)need);
+    if (overlap(workspace, need, x, xb) || overlap(workspace, need, y, yb) ||
+        overlaps_fp4_weights(workspace, need, K, wq, ws, N, bias))
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace overlaps an argument");
+  }
+  if ((st = check_device()) != MX_OK) return st;
+  (void)hipGetLastError();
+  const hipStream_t hs = (hipStream_t)stream;
+  if (M <= mx::kFp4RowsMaxTokens)
+    return finish(mx::launch_fp4_linear_rows(act == MX_ACT_FP8, x, M, K, ldx, wq, ws, N, bias, epilogue, y, hs),
+                  "MXFP4 linear launch");
+  const int64_t RM = mx::slab_rows(M);
+  uint8_t* xq = (uint8_t*)workspace;
+  uint8_t* xs = xq + act_code_bytes(act, RM, K);
+  const hipError_t e = act == MX_ACT_FP4 ? mx::launch_fp4_quantize_slab(0, x, M, K, ldx, xq, xs, hs)
+                                         : mx::launch_quantize_slab(0, x, M, K, ldx, xq, xs, hs);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  const int64_t used = round256((int64_t)(act_code_bytes(act, RM, K) + act_scale_bytes(act, RM, K)));
+  return mx_fp4_linear_slab(act, xq, xs, M, K, wq, ws, N, bias, epilogue, y, xq + used, workspace_bytes - used, stream);
+}
+
+int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr, const void* weight,
+                    int wdtype, double eps, int64_t M, int64_t K, void* residual_out, int64_t ldo, void* y, int64_t ldy,
+                    int act, uint8_t* q, uint8_t* s, void* stream) {
+  int st;
+  if ((st = check_rows("M", M)) != MX_OK) return st;
+  if ((st = check_act_k(act, K)) != MX_OK) return st;
+  if (K > mx::kNormMaxK) return fail(MX_ERR_UNSUPPORTED, "K = %lld exceeds the norm's 65536", (long long)K);
+  if (M > mx::kNormMaxRows) return fail(MX_ERR_UNSUPPORTED, "M = %lld exceeds the norm's 2^22", (long long)M);
+  if (!(eps >= 0.0 && eps <= 1e30)) return fail(MX_ERR_INVALID_ARGUMENT, "eps = %g must be finite and >= 0", eps);
+  if (residual != nullptr && rdtype != MX_DT_BF16 && rdtype != MX_DT_F32)
+    return fail(MX_ERR_INVALID_ARGUMENT, "unknown residual dtype %d", rdtype);
+  if (weight != nullptr && wdtype != MX_DT_BF16 && wdtype != MX_DT_F32)
+    return fail(MX_ERR_INVALID_ARGUMENT, "unknown weight dtype %d", wdtype);
+  if (residual == nullptr && residual_out != nullptr)
+    return fail(MX_ERR_INVALID_ARGUMENT, "residual_out without a residual");
+  const int64_t es = rdtype == MX_DT_F32 ? 4 : 2;
+  if (ldx < K || ldx % 8 != 0) return fail(MX_ERR_INVALID_ARGUMENT, "ldx = %lld must be >= K and a multiple of 8", (long long)ldx);
+  if (residual != nullptr && (ldr < K || (ldr * es) % 16 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldr = %lld must be >= K with 16-byte aligned rows", (long long)ldr);
+  if (residual_out != nullptr && (ldo < K || (ldo * es) % 16 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldo = %lld must be >= K with 16-byte aligned rows", (long long)ldo);
+  if (y != nullptr && (ldy < K || ldy % 8 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldy = %lld must be >= K and a multiple of 8", (long long)ldy);
+  if (M == 0) return MX_OK;
+  if (x == nullptr || q == nullptr || s == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+      !aligned(y, 16) || !aligned(q, 16) || !aligned(s, 16))
+    return fail(MX_ERR_INVALID_ARGUMENT, "every buffer must be 16-byte aligned");
+  const int64_t R = mx::slab_rows(M);
+  auto span = [&](int64_t ld, int64_t e) { return ((uint64_t)(M - 1) * ld + K) * e; };
+  struct Range {
+    const void* p;
+    uint64_t n;
+  };
+  const Range in[3] = {{x, span(ldx, 2)},
+                       {residual, residual != nullptr ? span(ldr, es) : 0},
+                       {weight, weight != nullptr ? (uint64_t)K * (wdtype == MX_DT_F32 ? 4 : 2) : 0}};
+  const Range out[4] = {{q, act_code_bytes(act, R, K)},
+                        {s, act_scale_bytes(act, R, K)},
+                        {residual_out, residual_out != nullptr ? span(ldo, es) : 0},
+                        {y, y != nullptr ? span(ldy, 2) : 0}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // The new residual may take the old one's place, row by row.
+      if (o == 2 && i == 1 && residual_out == residual && ldo == ldr) continue;
+      if (overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+        return fail(MX_ERR_INVALID_ARGUMENT, "an output overlaps an input");
+    }
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap");
+  }
+  if ((st = check_device()) != MX_OK) return st;
+  mx::RmsNormArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.residual_f32 = rdtype == MX_DT_F32;
+  a.weight = weight;
+  a.weight_f32 = wdtype == MX_DT_F32;
+  a.eps = eps;
+  a.M = M;
+  a.K = K;
+  a.residual_out = residual_out;
+  a.ldo = ldo;
+  a.y = y;
+  a.ldy = ldy;
+  a.fp4 = act == MX_ACT_FP4;
+  a.q = q;
+  a.s = s;
+  (void)hipGetLastError();
+  return finish(mx::launch_rmsnorm_slab(a, (hipStream_t)stream), "RMS norm launch");
+}
+
+}  // extern "C"

@@ -99,6 +99,55 @@ hipError_t launch_pc_quantize_slab(int kind, const void* x, int64_t rows, int64_
 hipError_t launch_pc_linear_slab(const uint8_t* xq, const float* xs, int64_t M, int64_t K, const uint8_t* wq,
                                  const float* ws, int64_t N, const void* bias, int epi, void* y, hipStream_t stream);
 
+// MXFP4 (mx_fp4_device.h has the slab layout). Rows of bf16 (kind 0) or f32
+// (kind 1) to a slab; a slab to row-major bf16 (kind 0) or f32 (kind 1) y;
+// row-major packed codes to a slab; a slab to the MXFP8 slab of the same
+// values (K % 64 == 0). Pitches in elements, K % 32 == 0.
+hipError_t launch_fp4_quantize_slab(int kind, const void* x, int64_t rows, int64_t K, int64_t ld, uint8_t* q,
+                                    uint8_t* s, hipStream_t stream);
+hipError_t launch_fp4_dequantize_slab(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, int kind, void* y,
+                                      int64_t ld, hipStream_t stream);
+hipError_t launch_fp4_slab_pack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, uint8_t* qo, uint8_t* so,
+                                hipStream_t stream);
+hipError_t launch_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t K, uint8_t* qo,
+                                  uint8_t* so, hipStream_t stream);
+
+// Few-token MXFP4-weight linear (mx_fp4_small.hip) on a token slab (fp8: an
+// MXFP8 slab, else an MXFP4 one), or on bf16 rows (M <= kFp4RowsMaxTokens)
+// quantized in the kernel.
+constexpr int64_t kFp4RowsMaxTokens = 16;
+hipError_t launch_fp4_linear_few(int fp8, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+                                 const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
+                                 hipStream_t stream);
+hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
+                                  const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
+                                  hipStream_t stream);
+
+// Residual add, RMS norm and quantization into a slab (mx_norm.hip). K up to
+// kNormMaxK (a row stays in one block's registers); residual, residual_out,
+// weight and y may be null.
+constexpr int64_t kNormMaxK = 65536;
+constexpr int64_t kNormMaxRows = int64_t(1) << 22;  // blocks x threads stay below 2^32
+struct RmsNormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  int residual_f32;
+  const void* weight;
+  int weight_f32;
+  double eps;
+  int64_t M, K;
+  void* residual_out;
+  int64_t ldo;
+  void* y;
+  int64_t ldy;
+  int fp4;
+  uint8_t* q;
+  uint8_t* s;
+};
+hipError_t launch_rmsnorm_slab(const RmsNormArgs& a, hipStream_t stream);
+
 // Bytes of the library-owned scratch array of mx_linear_noalloc (per GPU).
 constexpr int64_t kScratchBytes = int64_t(64) << 20;
 

@@ -8,6 +8,7 @@ here imports the product package.
 Everything is plain numpy in float64 (float32 where the pages fix FP32
 scales). ``oracle/mx_oracle.py`` is the MXFP8 scheme, ``oracle/pc_oracle.py``
 the per-output-channel FP8 scheme; each function cites the passage it follows.
+``oracle/fp4_oracle.py`` is the MXFP4 scheme and the RMS norm.
 """
 
 from .mx_oracle import (  # noqa: F401
@@ -29,3 +30,15 @@ from .mx_oracle import (  # noqa: F401
     tolerance,
 )
 from .pc_oracle import QMAX, dequantize_pc, linear_pc_ref, quantize_pc  # noqa: F401
+from .fp4_oracle import (  # noqa: F401
+    E2M1_MAGNITUDES,
+    dequantize_fp4,
+    e2m1_decode,
+    e2m1_encode,
+    fp4_scale_code,
+    fp4_slab,
+    linear_values_ref,
+    pack_rows,
+    quantize_fp4,
+    rmsnorm_ref,
+)

@@ -1,0 +1,222 @@
+"""GPU parity of the MXFP4-weight linears against the oracle in float64, on
+every route of the calls (bf16 rows quantized in the kernel, slab operands,
+few and many tokens), with MXFP4 and MXFP8 activations.
+
+Tolerance: the library's for every linear, 1e-3 g S + one bf16 ulp with
+S = sum |xhat| |what| and g the epilogue's largest slope (oracle.tolerance):
+products are exact, each MFMA adds 128 (or 64) of them with at most 2^-12 of
+their absolute sum lost to alignment (mixed and FP8 operands; E2M1 products
+lose none of it), the at most K / 64 + 8 fp32 additions lose 2^-24 of S each,
+and the output's rounding half an ulp."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from helpers import assert_linear_close, dev, f64, mx
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(x, w, b, act, gelu):
+    xh = oracle.dequantize_fp4(*oracle.quantize_fp4(f64(x))) if act == "fp4" else oracle.dequantize_mx(
+        *oracle.quantize_mx(f64(x)))
+    wh = oracle.dequantize_fp4(*oracle.quantize_fp4(f64(w)))
+    return oracle.linear_values_ref(xh, wh, None if b is None else f64(b), "gelu_tanh" if gelu else "none")
+
+
+def quantized(x, act):
+    return mx().mx_fp4_quantize_act_slab(x) if act == "fp4" else mx().mx_quantize_act_slab(x)
+
+
+def same(a, b):
+    return torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+CASES = [
+    (1, 32, 16), (1, 5120, 272), (2, 96, 48), (7, 1088, 256), (15, 160, 512), (16, 2048, 16), (17, 1024, 80),
+    (31, 4128, 96), (33, 64, 1040), (64, 608, 304), (65, 256, 256), (100, 3200, 528), (129, 128, 64), (257, 1216, 272),
+    (300, 352, 2064), (513, 544, 528), (1025, 192, 784),
+]
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
+@pytest.mark.parametrize("M,K,N", CASES)
+def test_linear_matches_oracle(M, K, N, act):
+    if act == "fp8":
+        K = (K + 63) // 64 * 64
+    print(f"fp4 linear M={M} K={K} N={N} {act}", flush=True)
+    d = dev()
+    gelu = (M + N // 16) % 2 == 1
+    x = synth.make_activation(M, K, seed=M)
+    w = synth.make_weight(N, K, seed=N) * 4
+    b = None if M % 5 == 0 else synth.make_bias(N, seed=K)
+    ws = mx().mx_fp4_quantize_weight_slab(w.to(d))
+    bd = None if b is None else b.to(d)
+    # Rows of x and y inside larger buffers; every element of y written, none
+    # past its end.
+    xb = torch.full((M, K + 8), float("nan"), dtype=torch.bfloat16, device=d)
+    xb[:, :K] = x.to(d)
+    yb = torch.full((M * N + 4096,), -1, dtype=torch.int16, device=d)
+    y = yb[: M * N].view(torch.bfloat16).view(M, N)
+    mx().mx_fp4_linear(xb[:, :K], ws, bd, gelu=gelu, act=act, y=y)
+    torch.cuda.synchronize()
+    assert bool((yb[M * N :] == -1).all()), "wrote past the end of y"
+    assert not bool((yb[: M * N] == -1).any()), "elements of y left unwritten"
+    ref, S = reference(x, w, b, act, gelu)
+    assert_linear_close(y, ref, S, "gelu_tanh" if gelu else "none", what=f"{M}x{K}x{N} {act}")
+    # The slab call gives the same bits, whatever the workspace held.
+    ys = mx().mx_fp4_linear_slab(quantized(x.to(d), act), ws, bd, gelu=gelu)
+    assert same(ys, y)
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
+@pytest.mark.parametrize("M", [1, 13, 40, 300, 700])
+def test_rows_are_independent_of_their_batch(M, act):
+    """A token's output does not change with the tokens behind it, as long as
+    the call takes the same kernel."""
+    print(f"fp4 rows M={M} {act}", flush=True)
+    d = dev()
+    K, N = 640, 272
+    x = synth.make_activation(M, K, seed=M).to(d)
+    w = mx().mx_fp4_quantize_weight_slab(synth.make_weight(N, K, seed=1).to(d))
+    y = mx().mx_fp4_linear(x, w, act=act)
+    z = x.clone()
+    z[M // 2 :] = float("nan")
+    yz = mx().mx_fp4_linear(z, w, act=act)
+    assert same(yz[: M // 2], y[: M // 2])
+    assert bool(torch.isnan(yz[M // 2 :]).all())
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
+@pytest.mark.parametrize("M", [3, 50, 600])
+def test_nonfinite_groups(M, act):
+    """A NaN or Inf in a token's group makes that token's outputs NaN; one in a
+    weight row's group makes that output column NaN; nothing else changes."""
+    print(f"fp4 nonfinite M={M} {act}", flush=True)
+    d = dev()
+    K, N = 320, 272
+    x = synth.make_activation(M, K, seed=2)
+    w = synth.make_weight(N, K, seed=3)
+    clean = mx().mx_fp4_linear(x.to(d), mx().mx_fp4_quantize_weight_slab(w.to(d)), act=act)
+    x[1, 200] = float("inf")
+    x[M - 1, 0] = float("nan")
+    w[5, 319] = float("nan")
+    w[N - 1, 64] = -float("inf")
+    y = mx().mx_fp4_linear(x.to(d), mx().mx_fp4_quantize_weight_slab(w.to(d)), act=act)
+    want = torch.zeros((M, N), dtype=torch.bool)
+    want[1] = want[M - 1] = True
+    want[:, 5] = want[:, N - 1] = True
+    assert torch.equal(torch.isnan(y).cpu(), want)
+    keep = (~want).to(d)
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
+@pytest.mark.parametrize("M", [4, 90, 1100])
+def test_graph_replays_match_eager(M, act):
+    print(f"fp4 graph M={M} {act}", flush=True)
+    d = dev()
+    K, N = 576, 528
+    w = mx().mx_fp4_quantize_weight_slab(synth.make_weight(N, K, seed=4).to(d))
+    ins = [synth.make_activation(M, K, seed=s).to(d) for s in (1, 2, 3)]
+    x = ins[0].clone()
+    res = torch.randn((M, K), device=d).to(torch.bfloat16)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=d)
+    y2 = torch.empty_like(y)
+    ws = torch.empty((max(mx().mx_fp4_linear_ws_bytes(M, K, N, act), 1),), dtype=torch.uint8, device=d)
+    ws2 = torch.empty((max(mx().mx_fp4_linear_slab_ws_bytes(M, K, N, act), 1),), dtype=torch.uint8, device=d)
+    h = torch.empty_like(res)
+    slab, _ = mx().mx_rmsnorm_slab(x, residual=res, residual_out=h, act=act)
+
+    def step():
+        mx().mx_fp4_linear(x, w, act=act, y=y, workspace=ws)
+        mx().mx_rmsnorm_slab(x, residual=res, residual_out=h, act=act, out=slab)
+        mx().mx_fp4_linear_slab(slab, w, gelu=True, y=y2, workspace=ws2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for xin in ins + ins[:1]:
+        x.copy_(xin)
+        ws.fill_(0xFF)
+        ws2.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        a, b = y.clone(), y2.clone()
+        step()
+        torch.cuda.synchronize()
+        assert same(a, y) and same(b, y2)
+    del g
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
+def test_two_streams_at_once(act):
+    """Calls on two streams with their own workspaces do not meet."""
+    print(f"fp4 two streams {act}", flush=True)
+    d = dev()
+    K, N = 2048, 1024
+    w = mx().mx_fp4_quantize_weight_slab(synth.make_weight(N, K, seed=4).to(d))
+    xs = [synth.make_activation(m, K, seed=m).to(d) for m in (130, 700)]
+    want = [mx().mx_fp4_linear(x, w, act=act) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mx().mx_fp4_linear(xs[i], w, act=act))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(same(y, want[i]) for y in got[i])
+
+
+@pytest.mark.parametrize("M", [2, 200])
+def test_block_of_norm_projection_and_feed_forward(M):
+    """The operators as a serving block runs them: norm (MXFP8) -> W4A8
+    projection -> residual add and norm (MXFP4) -> W4A4 up-projection with GELU
+    -> W4A8 down-projection, each step against the oracle on the values that
+    the step before produced."""
+    print(f"fp4 block M={M}", flush=True)
+    d = dev()
+    H, I = 320, 704
+    x = synth.make_activation(M, H, seed=1)
+    r = (2 * torch.randn((M, H), generator=torch.Generator().manual_seed(2))).to(torch.bfloat16)
+    g1 = 1 + 0.1 * torch.randn((H,), generator=torch.Generator().manual_seed(3))
+    w = [synth.make_weight(n, k, seed=n + k) * 4 for n, k in ((H, H), (I, H), (H, I))]
+    b = [synth.make_bias(n, seed=n) for n in (H, I, H)]
+    wd = [mx().mx_fp4_quantize_weight_slab(t.to(d)) for t in w]
+    wh = [oracle.dequantize_fp4(*oracle.quantize_fp4(f64(t))) for t in w]
+    s1, h1 = mx().mx_rmsnorm_slab(x.to(d), g1.to(d), residual=r.to(d))
+    y1 = mx().mx_fp4_linear_slab(s1, wd[0], b[0].to(d))
+    s2, h2 = mx().mx_rmsnorm_slab(y1, residual=h1, act="fp4")
+    y2 = mx().mx_fp4_linear_slab(s2, wd[1], b[1].to(d), gelu=True)
+    y3 = mx().mx_fp4_linear(y2, wd[2], b[2].to(d), act="fp8")
+    rh1, n1 = oracle.rmsnorm_ref(f64(x), f64(r), f64(g1))
+    assert np.array_equal(f64(h1), rh1)
+    ref, S = oracle.linear_values_ref(oracle.dequantize_mx(*oracle.quantize_mx(n1)), wh[0], f64(b[0]))
+    assert_linear_close(y1, ref, S, what="projection")
+    rh2, n2 = oracle.rmsnorm_ref(f64(y1), f64(h1))
+    assert np.array_equal(f64(h2), rh2)
+    ref, S = oracle.linear_values_ref(oracle.dequantize_fp4(*oracle.quantize_fp4(n2)), wh[1], f64(b[1]), "gelu_tanh")
+    assert_linear_close(y2, ref, S, "gelu_tanh", what="up")
+    ref, S = oracle.linear_values_ref(oracle.dequantize_mx(*oracle.quantize_mx(f64(y2))), wh[2], f64(b[2]))
+    assert_linear_close(y3, ref, S, what="down")
+
+
+def test_empty_calls():
+    d = dev()
+    w = mx().mx_fp4_quantize_weight_slab(synth.make_weight(32, 64, seed=1).to(d))
+    y = mx().mx_fp4_linear(torch.empty((0, 64), dtype=torch.bfloat16, device=d), w)
+    assert y.shape == (0, 32)
+    none = mx().FP4Slab(torch.empty((1, 0, 4, 16, 16), dtype=torch.uint8, device=d),
+                        torch.empty((1, 0, 4), dtype=torch.uint8, device=d), 0, 64)
+    assert mx().mx_fp4_linear(torch.zeros((3, 64), dtype=torch.bfloat16, device=d), none).shape == (3, 0)
