@@ -952,8 +952,21 @@ uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
   return act == MX_ACT_FP4 ? fp4_scale_bytes(R, K) : (uint64_t)R * (K / 32);
 }
 
-// Most tokens of the few-token kernel; more go through the tiled GEMMs.
-constexpr int64_t kFp4FewTokens = int64_t(1) << 30;
+// Most tokens of the few-token kernel, by activation format; more go through
+// the tiled GEMMs.
+constexpr int64_t kFp4FewTokensFp4 = 128;
+constexpr int64_t kFp4FewTokensFp8 = 256;
+// W4A4 on 128-token tiles while the 256 x 256 tiles are at most this many.
+constexpr int64_t kFp4HalfTiles = 128;
+
+bool fp4_few(int64_t M, int act) { return M <= (act == MX_ACT_FP4 ? kFp4FewTokensFp4 : kFp4FewTokensFp8); }
+
+// Workspace of an MXFP8-activation linear past the few-token kernel: the
+// weights as an MXFP8 slab, then the MXFP8 linear's own (its default plan's).
+int64_t unpacked_bytes(int64_t K, int64_t N) {
+  const int64_t RN = mx::slab_rows(N);
+  return round256(RN * K + RN * (K / 32));
+}
 
 int check_act_k(int act, int64_t K) {
   if (act != MX_ACT_FP8 && act != MX_ACT_FP4) return fail(MX_ERR_INVALID_ARGUMENT, "unknown activation format %d", act);
@@ -1089,7 +1102,11 @@ int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t
 
 int64_t mx_fp4_linear_slab_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
   if (bad_fp4_shape(M, K, N, act)) return -1;
-  return 0;
+  if (M == 0 || N == 0 || act == MX_ACT_FP4 || fp4_few(M, act)) return 0;
+  int kind, splits;
+  if (mx_linear_plan_default(M, K, N, &kind, &splits) != MX_OK) return -1;
+  const int64_t plan = mx_linear_plan_ws_bytes(kind, splits, M, K, N);
+  return plan < 0 ? -1 : unpacked_bytes(K, N) + round256(plan);
 }
 
 int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* wq,
@@ -1104,13 +1121,44 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   const uint64_t yb = (uint64_t)M * N * 2, xb = act_code_bytes(act, RM, K), sb = act_scale_bytes(act, RM, K);
   if (overlap(y, yb, xq, xb) || overlap(y, yb, xs, sb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
     return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
-  (void)workspace;
-  (void)workspace_bytes;
+  const int64_t need = mx_fp4_linear_slab_ws_bytes(M, K, N, act);
+  if (need < 0) return fail(MX_ERR_UNSUPPORTED, "no kernel for M = %lld, K = %lld, N = %lld", (long long)M, (long long)K, (long long)N);
+  if (need > 0) {
+    if (workspace == nullptr || !aligned(workspace, 256))
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned and not NULL");
+    if (workspace_bytes < need)
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
+                  (long long)need);
+    if (overlap(workspace, need, xq, xb) || overlap(workspace, need, xs, sb) || overlap(workspace, need, y, yb) ||
+        overlaps_fp4_weights(workspace, need, K, wq, ws, N, bias))
+      return fail(MX_ERR_INVALID_ARGUMENT, "workspace overlaps an argument");
+  }
+  const hipStream_t hs = (hipStream_t)stream;
+  if (fp4_few(M, act)) {
+    if ((st = check_device()) != MX_OK) return st;
+    (void)hipGetLastError();
+    return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y, hs),
+                  "MXFP4 linear launch");
+  }
+  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  if (tiles >= kMaxSplitWorkgroups)
+    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 256 x 256 exceed 2^24", (long long)tiles);
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
-  return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y,
-                                          (hipStream_t)stream),
-                "MXFP4 linear launch");
+  if (act == MX_ACT_FP4)
+    return finish(mx::launch_fp4_linear_tiles(tiles <= kFp4HalfTiles ? 128 : 256, xq, xs, M, K, wq, ws, N, bias,
+                                              epilogue, y, hs),
+                  "MXFP4 linear launch");
+  const int64_t RN = mx::slab_rows(N);
+  uint8_t* w8 = (uint8_t*)workspace;
+  uint8_t* s8 = w8 + RN * K;
+  const hipError_t e = mx::launch_fp4_slab_unpack(wq, ws, N, K, w8, s8, hs);
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 slab unpack launch");
+  int kind, splits;
+  if ((st = mx_linear_plan_default(M, K, N, &kind, &splits)) != MX_OK) return st;
+  const int64_t used = unpacked_bytes(K, N);
+  return mx_linear_slab_plan(kind, splits, xq, xs, M, K, w8, s8, N, bias, epilogue, y, w8 + used, workspace_bytes - used,
+                             stream);
 }
 
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {

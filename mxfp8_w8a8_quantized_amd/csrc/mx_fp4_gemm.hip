@@ -1,0 +1,429 @@
+// MXFP4 W4A4 linear for many tokens, on slab operands (mx_fp4_device.h):
+//
+//   y[m][n] = bf16_rne( epi( sum_k xhat[m][k] * what[n][k] + f32(bias[n]) ) )
+//
+// 256 weight rows x 64 JB tokens per workgroup, four waves of 128 x 32 JB
+// (one per SIMD) on v_mfma_scale_f32_32x32x64_f8f6f4 with the weights as the A
+// operand. K advances in steps of one 128-K slab: 16 KB of codes per 256 rows,
+// the bytes of an MXFP8 step of 64 K, for two MFMAs per fragment pair of half
+// an FP8 MFMA's duration each. So the balance between matrix core, LDS and
+// loads is the one of the MXFP8 slab GEMM at twice the arithmetic, and the
+// same pipeline feeds it: a ring of four LDS regions, each wave issuing a
+// quarter of the refill of step j + 4 during step j; the fragments of step
+// j + 1 read from LDS into a second register set between the MFMAs of step j;
+// one barrier per step, crossed while MFMAs issued ahead of it still run.
+//
+// Operand layout of the MFMA (found on the device): lane l holds 16 bytes, 32
+// consecutive elements of row l % 32, and the scale of those elements. Which
+// 32 is free as long as both operands agree: MFMA s (0, 1) of a step gives lane
+// half h the group 2 h + s, so that a lane's two scales are neighbouring bytes
+// and one 16-bit LDS read fetches both (op_sel takes byte s).
+//
+// A 16-row block of a slab is [group][row][16 bytes]: copied to LDS as it is,
+// the 16 lanes of a ds_read_b128 phase (16 rows of one group) read 256
+// consecutive bytes, without bank conflicts.
+//
+// The accumulators start at the bias. Sums are fp32 in a fixed order.
+#include <type_traits>
+
+#include "mx_fp4_device.h"
+#include "mx_internal.h"
+
+namespace mx {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+constexpr int BN = 256;  // weight rows per tile
+constexpr int NT = 256;
+constexpr int kDropOffset = 1 << 30;  // beyond every resource: the store is dropped
+constexpr int kStoreAux = 2;          // non-temporal
+
+struct GemmParams {
+  const uint8_t* x;
+  const uint8_t* xs;
+  const uint8_t* wq;
+  const uint8_t* ws;
+  const uint16_t* bias;  // f16 bits, or null
+  uint16_t* y;
+  int64_t RM, RN;
+  int M, N, nsteps;
+  int tiles_m, tiles_n;
+};
+
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
+// LDS: four regions (weight codes 16 KB, token codes 16 KB), then the scale
+// ring [weights, tokens][8 steps][256 rows][4], then a 256-byte bias slot per
+// wave.
+constexpr int R_X = 16384;
+constexpr int REGION = 32768;
+constexpr int SR = 4 * REGION;
+constexpr int SR_SLOT = 1024;
+constexpr int SR_OP = 8 * SR_SLOT;
+constexpr int BIAS_TABLE = SR + 2 * SR_OP;
+constexpr int LDS_BYTES = BIAS_TABLE + 4 * 256;
+
+template <int JB>
+struct Shape {
+  static constexpr int MT = 64 * JB;        // tokens per tile
+  static constexpr int CL = 4 + JB;         // 1 KB code DMAs per wave and step
+  static constexpr int NM = 8 * JB;         // MFMAs per wave and step
+  static constexpr int NC = 2 * (4 + JB);   // 16-byte code reads per wave and step
+  static constexpr int NR = NC + 4 + JB;    // and the scale pairs
+  static constexpr int PRE = JB == 4 ? 6 : 4;   // MFMAs issued ahead of the step's barrier
+  static constexpr int SETUP = 6;               // set-up instructions behind each of them
+  static constexpr int RS = JB == 4 ? 20 : 8;   // MFMAs after it that carry reads
+  static constexpr int DS = JB == 4 ? 18 : 10;  // and loads
+  static constexpr int ND = CL + 1;             // loads: the scale DMA, then the codes
+};
+
+struct Src {
+  const uint8_t* w;  // tile origin in slab 0
+  const uint8_t* x;
+  const uint8_t* ws;
+  const uint8_t* xs;
+  uint64_t w_slab, x_slab;  // bytes between code slabs
+  int nsteps;
+};
+
+struct LoadRes {
+  __amdgpu_buffer_rsrc_t w, x;
+  uint8_t* reg;
+};
+
+// Steps past the last load zeros (an empty resource) that nobody reads.
+template <int JB>
+__device__ __forceinline__ LoadRes load_res(const Src& S, uint8_t* smem, int j) {
+  LoadRes L;
+  L.reg = smem + (j & 3) * REGION;
+  const uint32_t n = j < S.nsteps ? 16384u : 0u;
+  L.w = make_rsrc(S.w + (uint64_t)j * S.w_slab, n);
+  L.x = make_rsrc(S.x + (uint64_t)j * S.x_slab, n / 4 * JB);
+  return L;
+}
+
+// Code piece D of a step: one 1 KB block (16 rows), weights and tokens in turn.
+template <int D, int JB>
+__device__ __forceinline__ void load_piece(const LoadRes& L, int wave, int lane) {
+  constexpr bool W = (D & 1) == 0 || D >= 2 * JB;
+  constexpr int u = D < 2 * JB ? D / 2 : D - JB;
+  const int q = wave * (W ? 4 : JB) + u;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(W ? L.w : L.x, (lds_ptr)(L.reg + (W ? 0 : R_X) + q * 1024), 16, lane * 16,
+                                           q * 1024, 0, 0);
+}
+
+// Scales of steps s and s + 1 (s even): 1 KB each for the weights (waves 0, 1)
+// and the tokens (waves 2, 3; with JB = 2 the tile's 512 bytes twice).
+struct ScaleLoad {
+  __amdgpu_buffer_rsrc_t r;
+  uint8_t* dst;
+  int voff;
+};
+
+template <int JB>
+__device__ __forceinline__ ScaleLoad scale_res(const Src& S, uint8_t* smem, int s, int wave, int lane) {
+  const bool w = wave < 2;
+  const int st = s + (wave & 1);
+  ScaleLoad L;
+  const uint64_t slab = (w ? S.w_slab : S.x_slab) >> 4;
+  L.r = make_rsrc((w ? S.ws : S.xs) + (uint64_t)st * slab, st < S.nsteps ? (w ? 1024u : 256u * JB) : 0u);
+  L.dst = smem + SR + (w ? 0 : SR_OP) + (st & 7) * SR_SLOT;
+  L.voff = (JB == 4 || w ? lane : (lane & 31)) * 16;
+  return L;
+}
+
+__device__ __forceinline__ void issue_scales(const ScaleLoad& L) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(L.r, (lds_ptr)L.dst, 16, L.voff, 0, 0, 0);
+}
+
+template <int JB>
+struct Frags {
+  i32x4 a[4][2];   // [fragment][MFMA of the step]
+  i32x4 b[JB][2];
+  int sa[4], sb[JB];  // byte s: the scale for MFMA s
+};
+
+struct FragAddr {
+  const uint8_t* a;
+  const uint8_t* b;
+  const uint8_t* sa;
+  const uint8_t* sb;
+};
+
+template <int JB>
+__device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int wn, int wm, int lane) {
+  const int r32 = lane & 31, hi = lane >> 5;
+  const uint8_t* reg = smem + (j & 3) * REGION;
+  const uint8_t* sc = smem + SR + (j & 7) * SR_SLOT;
+  const int off = (r32 >> 4) * 1024 + (r32 & 15) * 16 + 512 * hi;
+  FragAddr A;
+  A.a = reg + wn * 8192 + off;
+  A.b = reg + R_X + wm * (2048 * JB) + off;
+  A.sa = sc + (wn * 128 + r32) * 4 + 2 * hi;
+  A.sb = sc + SR_OP + (wm * 32 * JB + r32) * 4 + 2 * hi;
+  return A;
+}
+
+// Read piece r: the fragments' 16-byte halves in the order the MFMAs take
+// them (all of MFMA 0, A and B in turn, then all of MFMA 1), then the scales.
+template <int R, int JB>
+__device__ __forceinline__ void read_piece(Frags<JB>& F, const FragAddr& A) {
+  constexpr int NC = Shape<JB>::NC, H = 4 + JB;
+  if constexpr (R < NC) {
+    constexpr int s = R / H, r = R % H;
+    constexpr bool isA = (r % 2 == 0 && r < 2 * JB) || r >= 2 * JB;
+    constexpr int f = r < 2 * JB ? r / 2 : r - JB;
+    const i32x4 v = *(const i32x4*)((isA ? A.a : A.b) + f * 2048 + s * 256);
+    if constexpr (isA)
+      F.a[f][s] = v;
+    else
+      F.b[f][s] = v;
+  } else if constexpr (R < NC + 4) {
+    F.sa[R - NC] = *(const uint16_t*)(A.sa + 32 * 4 * (R - NC));
+  } else {
+    F.sb[R - NC - 4] = *(const uint16_t*)(A.sb + 32 * 4 * (R - NC - 4));
+  }
+}
+
+template <int JB, int B, int E>
+__device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB>& F) {
+  static_for<B, E>([&](auto T) {
+    constexpr int s = decltype(T)::value / (4 * JB), u = decltype(T)::value % (4 * JB), i = u / JB, j = u % JB;
+    const i32x8 a = {F.a[i][s][0], F.a[i][s][1], F.a[i][s][2], F.a[i][s][3], 0, 0, 0, 0};
+    const i32x8 b = {F.b[j][s][0], F.b[j][s][1], F.b[j][s][2], F.b[j][s][3], 0, 0, 0, 0};
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, s, F.sa[i], s, F.sb[j]);
+  });
+}
+
+// Step j: the first MFMAs, which read registers only, cover the wait for this
+// wave's loads of step j + 1, the barrier and the address set-up; the rest run
+// with the LDS reads of step j + 1 and the loads of step j + 4 between them.
+// EVEN: j is even, and the scales of steps j + 4 and j + 5 are fetched too.
+template <bool EVEN, int JB>
+__device__ __forceinline__ void step(f32x16 (&acc)[4][JB], Frags<JB>& cur, Frags<JB>& nxt, const Src& S,
+                                     uint8_t* smem, int j, int wave, int wn, int wm, int lane) {
+  using Sh = Shape<JB>;
+  constexpr int NM = Sh::NM, PRE = Sh::PRE;
+  __builtin_amdgcn_sched_barrier(0);
+  const FragAddr A = frag_addr<JB>(smem, j + 1, wn, wm, lane);
+  const LoadRes L = load_res<JB>(S, smem, j + 4);
+  ScaleLoad SL;
+  if constexpr (EVEN) SL = scale_res<JB>(S, smem, j + 4, wave, lane);
+  mma<JB, 0, PRE>(acc, cur);
+  static_for<0, PRE>([&](auto) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
+    __builtin_amdgcn_sched_group_barrier(0x006, Sh::SETUP, 0);  // set-up VALU / SALU
+  });
+  __builtin_amdgcn_sched_barrier(0);
+  // The lgkmcnt(0) keeps a wave's refill from overtaking another wave's last
+  // reads of the region. Younger loads: those of the two steps after j + 1.
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * Sh::CL + 1) : "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  static_for<0, NM - PRE>([&](auto I) {
+    constexpr int i = decltype(I)::value;
+    constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
+    constexpr int d0 = i < Sh::DS ? Sh::ND * i / Sh::DS : Sh::ND, d1 = i < Sh::DS ? Sh::ND * (i + 1) / Sh::DS : Sh::ND;
+    static_for<r0, r1>([&](auto R) { read_piece<decltype(R)::value, JB>(nxt, A); });
+    static_for<d0, d1>([&](auto D) {
+      constexpr int d = decltype(D)::value;
+      if constexpr (d == 0) {
+        if constexpr (EVEN) issue_scales(SL);
+      } else {
+        load_piece<d - 1, JB>(L, wave, lane);
+      }
+    });
+  });
+  mma<JB, PRE, NM>(acc, cur);
+  static_for<0, NM - PRE>([&](auto I) {
+    constexpr int i = decltype(I)::value;
+    constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
+    constexpr int d0 = i < Sh::DS ? Sh::ND * i / Sh::DS : Sh::ND, d1 = i < Sh::DS ? Sh::ND * (i + 1) / Sh::DS : Sh::ND;
+    constexpr int nd = d1 - d0 - (!EVEN && d0 == 0 && d1 > 0 ? 1 : 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (r1 > r0) __builtin_amdgcn_sched_group_barrier(0x100, r1 - r0, 0);
+    if constexpr (nd > 0) __builtin_amdgcn_sched_group_barrier(0x020, nd, 0);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Workgroup -> (token tile, weight tile): a contiguous range of tiles per XCD,
+// walked in groups of 4 token tiles x all weight tiles (token tile fastest), so
+// that the tiles in flight on an XCD share panels in its L2.
+__device__ inline void tile_coords(uint32_t pid, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int GM = 4;
+  const int lid = (int)xcd_order(pid, (uint32_t)(tiles_m * tiles_n));
+  const int group = lid / (GM * tiles_n);
+  const int gm = min(tiles_m - group * GM, GM);
+  const int in_group = lid - group * GM * tiles_n;
+  tm = group * GM + in_group % gm;
+  tn = in_group / gm;
+}
+
+// The wave's 128 (n) x 32 JB (m) outputs: bf16 through LDS ([m][n], rows of
+// 256 bytes, 8-byte block nb of row m at nb ^ (m & 31): 32 lanes on 32 rows
+// write 32 bank pairs), then whole 256-byte row pieces, 16 bytes a lane.
+template <int EPI, int JB>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][JB], const GemmParams& p, uint8_t* ep, int m0,
+                                           int n0, int rows_m, int rows_n, int wn, int wm, int lane) {
+  const int r32 = lane & 31, hi = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int nb = 8 * i + 2 * q + hi;
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+        const int m = 32 * j + r32;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = epilogue<EPI>(acc[i][j][4 * q + r]);
+        const bf16x2 p0 = {(__bf16)v[0], (__bf16)v[1]};
+        const bf16x2 p1 = {(__bf16)v[2], (__bf16)v[3]};
+        *(i32x2*)(ep + m * 256 + ((nb ^ (m & 31)) << 3)) =
+            i32x2{__builtin_bit_cast(int, p0), __builtin_bit_cast(int, p1)};
+      }
+    }
+  // The staging rows pass data between lanes: no read may move above another
+  // lane's write (LDS order within a wave is kept by the hardware).
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + (size_t)m0 * p.N, (uint32_t)(rows_m * p.N * 2));
+  const int c = lane & 15;
+  const int nl = wn * 128 + 8 * c;
+  const bool n_ok = nl < rows_n;
+#pragma unroll 8
+  for (int it = 0; it < 8 * JB; ++it) {
+    const int m = 4 * it + (lane >> 4);
+    const int sw = m & 31;
+    const i32x4 v = *(const i32x4*)(ep + m * 256 + ((((2 * c) ^ sw) & ~1) << 3));
+    const i32x4 w = (sw & 1) ? i32x4{v[2], v[3], v[0], v[1]} : v;
+    const int off = n_ok ? ((wm * 32 * JB + m) * p.N + n0 + nl) * 2 : kDropOffset;
+    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, kStoreAux);
+  }
+}
+
+template <int EPI, int JB>
+__global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using Sh = Shape<JB>;
+  int tm, tn;
+  tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+  const int m0 = tm * Sh::MT, n0 = tn * BN;
+  const int rows_m = min(p.M - m0, Sh::MT);
+  const int rows_n = min(p.N - n0, BN);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave & 1, wm = wave >> 1;
+
+  Src S;
+  S.w_slab = (uint64_t)p.RN * 64;
+  S.x_slab = (uint64_t)p.RM * 64;
+  S.w = p.wq + (size_t)n0 * 64;
+  S.x = p.x + (size_t)m0 * 64;
+  S.ws = p.ws + (size_t)n0 * 4;
+  S.xs = p.xs + (size_t)m0 * 4;
+  S.nsteps = p.nsteps;
+
+  // Bias: the 128 f16 values of the wave's weight rows into its slot, ahead of
+  // the ring's first loads (columns past N read what the load leaves there;
+  // their outputs are not stored).
+  uint8_t* slot = smem + BIAS_TABLE + wave * 256;
+  if (p.bias != nullptr) {
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.bias + n0, (uint32_t)rows_n * 2u);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 256, 0, 0);
+  } else {
+    *(int*)(slot + lane * 4) = 0;
+  }
+  // The ring's first loads in the order the loop would have issued them (its
+  // waits count on it): scales of steps 0, 1, codes 0, 1, scales 2, 3, codes 2, 3.
+  static_for<0, 4>([&](auto J) {
+    constexpr int j = decltype(J)::value;
+    if constexpr (j % 2 == 0) issue_scales(scale_res<JB>(S, smem, j, wave, lane));
+    const LoadRes L = load_res<JB>(S, smem, j);
+    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, JB>(L, wave, lane); });
+  });
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 * Sh::CL + 2) : "memory");  // the bias
+  f32x16 acc[4][JB];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const i32x2 bq = *(const i32x2*)(slot + (32 * i + 8 * q + 4 * (lane >> 5)) * 2);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t w = (uint32_t)bq[r >> 1];
+        const float b = (float)__builtin_bit_cast(_Float16, (uint16_t)((r & 1) ? (w >> 16) : (w & 0xFFFFu)));
+#pragma unroll
+        for (int j = 0; j < JB; ++j) acc[i][j][4 * q + r] = b;
+      }
+    }
+  // The accumulators are written here, inside the first loads' latency.
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * Sh::CL + 1) : "memory");  // step 0
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  Frags<JB> F0, F1;
+  const FragAddr A0 = frag_addr<JB>(smem, 0, wn, wm, lane);
+  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value, JB>(F0, A0); });
+  int j = 0;
+  for (; j + 1 < p.nsteps; j += 2) {
+    step<true, JB>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
+    step<false, JB>(acc, F1, F0, S, smem, j + 1, wave, wn, wm, lane);
+  }
+  if (j < p.nsteps) step<true, JB>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  store_tile<EPI, JB>(acc, p, smem + wave * 32768, m0, n0, rows_m, rows_n, wn, wm, lane);
+}
+
+template <int EPI, int JB>
+hipError_t launch(const GemmParams& p, hipStream_t st) {
+  static bool configured = false;  // per instantiation; benign race (idempotent)
+  auto kern = fp4_gemm_kernel<EPI, JB>;
+  if (!configured) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+    if (e != hipSuccess) return e;
+    configured = true;
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(NT), LDS_BYTES, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp4_linear_tiles(int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+                                   const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
+                                   hipStream_t stream) {
+  GemmParams p;
+  p.x = xq;
+  p.xs = xs;
+  p.wq = wq;
+  p.ws = ws;
+  p.bias = (const uint16_t*)bias;
+  p.y = (uint16_t*)y;
+  p.RM = slab_rows(M);
+  p.RN = slab_rows(N);
+  p.M = (int)M;
+  p.N = (int)N;
+  p.nsteps = (int)fp4_slabs(K);
+  p.tiles_m = (int)((M + token_tile - 1) / token_tile);
+  p.tiles_n = (int)((N + BN - 1) / BN);
+  if (token_tile == 128) return epi == 1 ? launch<1, 2>(p, stream) : launch<0, 2>(p, stream);
+  return epi == 1 ? launch<1, 4>(p, stream) : launch<0, 4>(p, stream);
+}
+
+}  // namespace mx

@@ -123,6 +123,12 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
                                   const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                   hipStream_t stream);
 
+// W4A4 linear on token_tile (128 or 256) x 256 tiles (mx_fp4_gemm.hip), both
+// operands MXFP4 slabs; N % 16 == 0, tiles below 2^24.
+hipError_t launch_fp4_linear_tiles(int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+                                   const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
+                                   hipStream_t stream);
+
 // Residual add, RMS norm and quantization into a slab (mx_norm.hip). K up to
 // kNormMaxK (a row stays in one block's registers); residual, residual_out,
 // weight and y may be null.
