@@ -564,22 +564,22 @@ int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t
  * of the MXFP4 weight slab wq, ws (R = mx_slab_rows(N)). Products are exact,
  * sums FP32. bias f16 [N] or NULL; y bf16 [M][N]; N % 16 == 0 (else
  * MX_ERR_UNSUPPORTED). Codes and y 16-byte aligned, scales 4-byte aligned; y
- * must not overlap an input. The kernel is chosen by the shape and the format
- * alone, so results are deterministic. workspace: mx_fp4_linear_slab_ws_bytes
- * bytes, 256-byte aligned, overlapping no operand or output (NULL when that
- * is 0); its contents are overwritten and need no initial value. Nothing is
- * allocated. */
-int64_t mx_fp4_linear_slab_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
+ * must not overlap an input. One kernel, chosen by the shape and the format
+ * alone (a few-token kernel up to 2^21 outputs, 128 or 256 token tiles above),
+ * so results are deterministic. Fewer than 2^24 tiles of 256 x 256 (else
+ * MX_ERR_UNSUPPORTED). */
 int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                        const uint8_t* wq, const uint8_t* ws, int64_t N,
-                       const void* bias, int epilogue, void* y,
-                       void* workspace, int64_t workspace_bytes, void* stream);
+                       const void* bias, int epilogue, void* y, void* stream);
 
 /* The same in one call: bf16 activations x [M][ldx] (ldx >= K, ldx % 8 == 0)
- * quantized to MXFP4 or MXFP8 (act) at run time, then the product. Up to 16
- * tokens are quantized inside the product's kernel (one launch, no
- * workspace); more go through a slab in the workspace
- * (mx_fp4_linear_ws_bytes bytes, 256-byte aligned, overlapping no argument). */
+ * quantized to MXFP4 or MXFP8 (act) at run time, then the product,
+ * bit-identical to the quantizer and mx_fp4_linear_slab. A few tokens (up to
+ * 16, at most 98304 elements) are quantized inside the product's kernel: one
+ * launch, no workspace. More go through a slab in the workspace
+ * (mx_fp4_linear_ws_bytes bytes, 256-byte aligned, overlapping no argument; its
+ * contents are overwritten and need no initial value). mx_fp4_linear_ws_bytes
+ * is 0 where none is needed, -1 on a bad shape or format. Nothing is allocated. */
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
 int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx,
                   const uint8_t* wq, const uint8_t* ws, int64_t N,

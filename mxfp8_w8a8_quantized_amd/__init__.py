@@ -7,6 +7,7 @@ If the built library ``libmxfp8.so`` is missing, every call raises.
 """
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -84,8 +85,7 @@ SIGNATURES = {
     "mx_fp4_dequantize_slab": ([_P, _P, _I64, _I64, _P, _INT, _I64, _P], _INT),
     "mx_fp4_slab_pack": ([_P, _P, _I64, _I64, _P, _P, _P], _INT),
     "mx_fp4_slab_unpack": ([_P, _P, _I64, _I64, _P, _P, _P], _INT),
-    "mx_fp4_linear_slab_ws_bytes": ([_I64, _I64, _I64, _INT], _I64),
-    "mx_fp4_linear_slab": ([_INT, _P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P, _I64, _P], _INT),
+    "mx_fp4_linear_slab": ([_INT, _P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P], _INT),
     "mx_fp4_linear_ws_bytes": ([_I64, _I64, _I64, _INT], _I64),
     "mx_fp4_linear": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _P], _INT),
     "mx_rmsnorm_slab": ([_P, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P,
@@ -776,9 +776,10 @@ class FP4Slab(NamedTuple):
     K: int
 
 
+@functools.lru_cache(maxsize=4096)
 def _fp4_shapes(rows, K):
     S, R = (K + 127) // 128, (rows + 255) // 256 * 256
-    return (S, R // 16, 4, 16, 16), (S, R, 4)
+    return torch.Size((S, R // 16, 4, 16, 16)), torch.Size((S, R, 4))
 
 
 def _fp4_out(rows, K, dev, out):
@@ -797,7 +798,8 @@ def _need_fp4(t, name, dev):
         raise TypeError(f"{name} must be an FP4Slab")
     _need(t.q, name + ".q", torch.uint8, dev)
     _need(t.s, name + ".s", torch.uint8, dev)
-    if (t.q.shape, t.s.shape) != _fp4_shapes(t.rows, t.K):
+    sq, ss = _fp4_shapes(t.rows, t.K)
+    if t.q.shape != sq or t.s.shape != ss:
         raise ValueError(f"{name} is not an MXFP4 slab of {t.rows} rows and K = {t.K}")
 
 
@@ -821,13 +823,25 @@ def _pitch(x):
 _DTYPES = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
 
 
+# A call of a few tokens runs for about as long on the GPU as Python needs to
+# make it, so these calls pass addresses as plain integers (None for NULL) and
+# take the stream's handle without building a Stream object.
+
+
+def _adr(t):
+    return t.data_ptr() if t is not None and t.numel() > 0 else None
+
+
 def _run(fn, dev, *args):
-    """Calls fn(*args, stream) with `dev` the current device."""
-    if torch.cuda.current_device() == dev.index:  # the usual case: no switch
-        _check(fn(*args, _stream(dev)))
+    """Calls fn(*args, stream) with `dev` the current device, on its current stream."""
+    i = dev.index
+    if torch.cuda.current_device() == i:  # the usual case: no switch
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status != MX_OK:
+        _check(status)
 
 
 def _fp4_quantize(x, name, dtypes, out):
@@ -841,15 +855,15 @@ def _fp4_quantize(x, name, dtypes, out):
 def mx_fp4_quantize_act_slab(x, out=None):
     """bf16 [M, K] (rows may be strided, K % 32 == 0) -> FP4Slab of its MXFP4 codes and scales."""
     out = _fp4_quantize(x, "x", (torch.bfloat16,), out)
-    _run(lib().mx_fp4_quantize_act_slab, x.device, _ptr(x), x.shape[0], x.shape[1], _pitch(x), _ptr(out.q), _ptr(out.s))
+    _run(lib().mx_fp4_quantize_act_slab, x.device, _adr(x), x.shape[0], x.shape[1], _pitch(x), _adr(out.q), _adr(out.s))
     return out
 
 
 def mx_fp4_quantize_weight_slab(w, out=None):
     """fp32 or bf16 [N, K] (K % 32 == 0) -> FP4Slab of its MXFP4 codes and scales."""
     out = _fp4_quantize(w, "w", (torch.float32, torch.bfloat16), out)
-    _run(lib().mx_fp4_quantize_weight_slab, w.device, _ptr(w), _DTYPES[w.dtype], w.shape[0], w.shape[1], _pitch(w),
-         _ptr(out.q), _ptr(out.s))
+    _run(lib().mx_fp4_quantize_weight_slab, w.device, _adr(w), _DTYPES[w.dtype], w.shape[0], w.shape[1], _pitch(w),
+         _adr(out.q), _adr(out.s))
     return out
 
 
@@ -865,7 +879,7 @@ def mx_fp4_dequantize_slab(slab, y=None, dtype=torch.bfloat16):
     _need_rows(y, "y", (torch.bfloat16, torch.float32))
     if y.device != dev or tuple(y.shape) != (slab.rows, slab.K):
         raise ValueError(f"y must be [{slab.rows}, {slab.K}] on {dev}")
-    _run(lib().mx_fp4_dequantize_slab, dev, _ptr(slab.q), _ptr(slab.s), slab.rows, slab.K, _ptr(y), _DTYPES[y.dtype],
+    _run(lib().mx_fp4_dequantize_slab, dev, _adr(slab.q), _adr(slab.s), slab.rows, slab.K, _adr(y), _DTYPES[y.dtype],
          _pitch(y))
     return y
 
@@ -882,7 +896,7 @@ def mx_fp4_slab_pack(q, s, out=None):
     if s.shape != (rows, K // 32):
         raise ValueError("s must be [rows, K/32]")
     out = _fp4_out(rows, K, dev, out)
-    _run(lib().mx_fp4_slab_pack, dev, _ptr(q), _ptr(s), rows, K, _ptr(out.q), _ptr(out.s))
+    _run(lib().mx_fp4_slab_pack, dev, _adr(q), _adr(s), rows, K, _adr(out.q), _adr(out.s))
     return out
 
 
@@ -893,7 +907,7 @@ def mx_fp4_slab_unpack(slab, out=None):
     if slab.K % 64 != 0:
         raise ValueError("the MXFP8 slab layout needs K % 64 == 0")
     out = _slab_out(slab.rows, slab.K, dev, out)
-    _run(lib().mx_fp4_slab_unpack, dev, _ptr(slab.q), _ptr(slab.s), slab.rows, slab.K, _ptr(out.q), _ptr(out.s))
+    _run(lib().mx_fp4_slab_unpack, dev, _adr(slab.q), _adr(slab.s), slab.rows, slab.K, _adr(out.q), _adr(out.s))
     return out
 
 
@@ -918,15 +932,9 @@ def _fp4_workspace(workspace, need, dev):
     return workspace
 
 
-def mx_fp4_linear_slab_ws_bytes(M, K, N, act="fp4"):
-    return lib().mx_fp4_linear_slab_ws_bytes(M, K, N, _act_format(act))
-
-
-def mx_fp4_linear_slab(x, w, bias=None, gelu=False, y=None, workspace=None):
+def mx_fp4_linear_slab(x, w, bias=None, gelu=False, y=None):
     """y = bf16(epi(xhat @ what^T + bias)) on an activation slab x (FP4Slab,
-    or Slab for MXFP8 activations) and MXFP4 weights w (FP4Slab). workspace:
-    uint8 of at least mx_fp4_linear_slab_ws_bytes bytes (allocated here when
-    None and needed)."""
+    or Slab for MXFP8 activations) and MXFP4 weights w (FP4Slab)."""
     if not isinstance(x, (FP4Slab, Slab)):
         raise TypeError("x must be an FP4Slab or a Slab")
     dev = x.q.device
@@ -944,10 +952,8 @@ def mx_fp4_linear_slab(x, w, bias=None, gelu=False, y=None, workspace=None):
     y = _fp4_linear_out(M, w, bias, y, dev)
     if w.K != K:
         raise ValueError(f"x has K = {K}, w has K = {w.K}")
-    workspace = _fp4_workspace(workspace, lib().mx_fp4_linear_slab_ws_bytes(M, K, w.rows, ACT_FORMATS[act]), dev)
-    _run(lib().mx_fp4_linear_slab, dev, ACT_FORMATS[act], _ptr(x.q), _ptr(x.s), M, K, _ptr(w.q), _ptr(w.s), w.rows,
-         _ptr(bias), MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, _ptr(y), _ptr(workspace),
-         0 if workspace is None else workspace.numel())
+    _run(lib().mx_fp4_linear_slab, dev, ACT_FORMATS[act], _adr(x.q), _adr(x.s), M, K, _adr(w.q), _adr(w.s), w.rows,
+         _adr(bias), MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, _adr(y))
     return y
 
 
@@ -960,7 +966,7 @@ def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None
     [M, K] (rows may be strided) is quantized to MXFP4 (act="fp4") or MXFP8
     (act="fp8") and multiplied by the FP4Slab w. workspace: uint8 of at least
     mx_fp4_linear_ws_bytes(M, K, N, act) bytes (allocated here when None and
-    needed; none up to 16 tokens)."""
+    needed; a few tokens need none)."""
     fmt = _act_format(act)
     _need_rows(x, "x", (torch.bfloat16,))
     dev = x.device
@@ -969,8 +975,8 @@ def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None
     if w.K != K:
         raise ValueError(f"x has K = {K}, w has K = {w.K}")
     workspace = _fp4_workspace(workspace, lib().mx_fp4_linear_ws_bytes(M, K, w.rows, fmt), dev)
-    _run(lib().mx_fp4_linear, dev, _ptr(x), M, K, _pitch(x), _ptr(w.q), _ptr(w.s), w.rows, _ptr(bias),
-         MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, fmt, _ptr(y), _ptr(workspace),
+    _run(lib().mx_fp4_linear, dev, _adr(x), M, K, _pitch(x), _adr(w.q), _adr(w.s), w.rows, _adr(bias),
+         MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, fmt, _adr(y), _adr(workspace),
          0 if workspace is None else workspace.numel())
     return y
 
@@ -1014,7 +1020,7 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
         if t is not None and (t.device != dev or t.shape != x.shape):
             raise ValueError(f"{name} must be [{M}, {K}] on {dev}")
     out = _fp4_out(M, K, dev, out) if act == "fp4" else _slab_out(M, K, dev, out)
-    _run(lib().mx_rmsnorm_slab, dev, _ptr(x), _pitch(x), _ptr(residual), rdt, 0 if residual is None else _pitch(residual),
-         _ptr(weight), wdt, float(eps), M, K, _ptr(residual_out), 0 if residual_out is None else _pitch(residual_out),
-         _ptr(y), 0 if y is None else _pitch(y), fmt, _ptr(out.q), _ptr(out.s))
+    _run(lib().mx_rmsnorm_slab, dev, _adr(x), _pitch(x), _adr(residual), rdt, 0 if residual is None else _pitch(residual),
+         _adr(weight), wdt, float(eps), M, K, _adr(residual_out), 0 if residual_out is None else _pitch(residual_out),
+         _adr(y), 0 if y is None else _pitch(y), fmt, _adr(out.q), _adr(out.s))
     return out, residual_out

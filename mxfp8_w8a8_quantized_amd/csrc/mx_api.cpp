@@ -952,21 +952,27 @@ uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
   return act == MX_ACT_FP4 ? fp4_scale_bytes(R, K) : (uint64_t)R * (K / 32);
 }
 
-// Most tokens of the few-token kernel, by activation format; more go through
-// the tiled GEMMs.
-constexpr int64_t kFp4FewTokensFp4 = 128;
-constexpr int64_t kFp4FewTokensFp8 = 256;
-// W4A4 on 128-token tiles while the 256 x 256 tiles are at most this many.
-constexpr int64_t kFp4HalfTiles = 128;
+// The few-token kernel up to this many outputs (8192 fragments of 16 x 16, at
+// most 32 in each of 256 workgroups), the tiled GEMMs above: 256 x 5120 x 5120
+// takes 13.3 us there against 16.1 (MXFP8 activations 17.8 against 24.1), 512 x
+// 5120 x 5120 20.1 against 16.0 (30.4 against 24.3).
+constexpr int64_t kFp4FewFragments = 8192;
+bool fp4_few(int64_t M, int64_t N) { return ((M + 15) / 16) * (N / 16) <= kFp4FewFragments; }
 
-bool fp4_few(int64_t M, int act) { return M <= (act == MX_ACT_FP4 ? kFp4FewTokensFp4 : kFp4FewTokensFp8); }
-
-// Workspace of an MXFP8-activation linear past the few-token kernel: the
-// weights as an MXFP8 slab, then the MXFP8 linear's own (its default plan's).
-int64_t unpacked_bytes(int64_t K, int64_t N) {
-  const int64_t RN = mx::slab_rows(N);
-  return round256(RN * K + RN * (K / 32));
+// bf16 rows are quantized inside the product's kernel, by every workgroup for
+// itself, up to 16 tokens and this many elements; past that a quantizer
+// launch costs less (16 x 13824 x 5120: 18.1 us against 3 + 8.5; 16 x 5120 x
+// 5120: 8.5 against 3 + 5.0).
+constexpr int64_t kFp4RowsMaxTokens = 16;
+constexpr int64_t kFp4RowsMaxElements = 98304;
+bool fp4_rows(int64_t M, int64_t K, int64_t N) {
+  return M <= kFp4RowsMaxTokens && M * K <= kFp4RowsMaxElements && fp4_few(M, N);
 }
+
+// MXFP4 activations on 128-token tiles while the 256 x 256 tiles are at most
+// this many (half a round of CUs): 1024 x 5120 x 5120 (80 tiles) 18.1 against
+// 26.2 us, 2048 x 5120 x 5120 (160) 37.4 against 31.5.
+constexpr int64_t kFp4HalfTiles = 128;
 
 int check_act_k(int act, int64_t K) {
   if (act != MX_ACT_FP8 && act != MX_ACT_FP4) return fail(MX_ERR_INVALID_ARGUMENT, "unknown activation format %d", act);
@@ -1100,18 +1106,8 @@ int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t
   return finish(mx::launch_fp4_slab_unpack(q, s, rows, K, q8, s8, (hipStream_t)stream), "MXFP4 slab unpack launch");
 }
 
-int64_t mx_fp4_linear_slab_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
-  if (bad_fp4_shape(M, K, N, act)) return -1;
-  if (M == 0 || N == 0 || act == MX_ACT_FP4 || fp4_few(M, act)) return 0;
-  int kind, splits;
-  if (mx_linear_plan_default(M, K, N, &kind, &splits) != MX_OK) return -1;
-  const int64_t plan = mx_linear_plan_ws_bytes(kind, splits, M, K, N);
-  return plan < 0 ? -1 : unpacked_bytes(K, N) + round256(plan);
-}
-
 int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* wq,
-                       const uint8_t* ws, int64_t N, const void* bias, int epilogue, void* y, void* workspace,
-                       int64_t workspace_bytes, void* stream) {
+                       const uint8_t* ws, int64_t N, const void* bias, int epilogue, void* y, void* stream) {
   int st = check_fp4_linear(M, K, wq, ws, N, bias, epilogue, act, y);
   if (st != MX_OK || M == 0 || N == 0) return st;
   if (xq == nullptr || xs == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL xq or xs");
@@ -1121,20 +1117,8 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   const uint64_t yb = (uint64_t)M * N * 2, xb = act_code_bytes(act, RM, K), sb = act_scale_bytes(act, RM, K);
   if (overlap(y, yb, xq, xb) || overlap(y, yb, xs, sb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
     return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
-  const int64_t need = mx_fp4_linear_slab_ws_bytes(M, K, N, act);
-  if (need < 0) return fail(MX_ERR_UNSUPPORTED, "no kernel for M = %lld, K = %lld, N = %lld", (long long)M, (long long)K, (long long)N);
-  if (need > 0) {
-    if (workspace == nullptr || !aligned(workspace, 256))
-      return fail(MX_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned and not NULL");
-    if (workspace_bytes < need)
-      return fail(MX_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
-                  (long long)need);
-    if (overlap(workspace, need, xq, xb) || overlap(workspace, need, xs, sb) || overlap(workspace, need, y, yb) ||
-        overlaps_fp4_weights(workspace, need, K, wq, ws, N, bias))
-      return fail(MX_ERR_INVALID_ARGUMENT, "workspace overlaps an argument");
-  }
   const hipStream_t hs = (hipStream_t)stream;
-  if (fp4_few(M, act)) {
+  if (fp4_few(M, N)) {
     if ((st = check_device()) != MX_OK) return st;
     (void)hipGetLastError();
     return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y, hs),
@@ -1145,28 +1129,16 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
     return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 256 x 256 exceed 2^24", (long long)tiles);
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
-  if (act == MX_ACT_FP4)
-    return finish(mx::launch_fp4_linear_tiles(tiles <= kFp4HalfTiles ? 128 : 256, xq, xs, M, K, wq, ws, N, bias,
-                                              epilogue, y, hs),
-                  "MXFP4 linear launch");
-  const int64_t RN = mx::slab_rows(N);
-  uint8_t* w8 = (uint8_t*)workspace;
-  uint8_t* s8 = w8 + RN * K;
-  const hipError_t e = mx::launch_fp4_slab_unpack(wq, ws, N, K, w8, s8, hs);
-  if (e != hipSuccess) return hip_fail(e, "MXFP4 slab unpack launch");
-  int kind, splits;
-  if ((st = mx_linear_plan_default(M, K, N, &kind, &splits)) != MX_OK) return st;
-  const int64_t used = unpacked_bytes(K, N);
-  return mx_linear_slab_plan(kind, splits, xq, xs, M, K, w8, s8, N, bias, epilogue, y, w8 + used, workspace_bytes - used,
-                             stream);
+  return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, act == MX_ACT_FP8 || tiles <= kFp4HalfTiles ? 128 : 256, xq,
+                                            xs, M, K, wq, ws, N, bias, epilogue, y, hs),
+                "MXFP4 linear launch");
 }
 
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
-  const int64_t slab = mx_fp4_linear_slab_ws_bytes(M, K, N, act);
-  if (slab < 0) return -1;
-  if (M == 0 || N == 0 || M <= mx::kFp4RowsMaxTokens) return 0;
+  if (bad_fp4_shape(M, K, N, act)) return -1;
+  if (M == 0 || N == 0 || fp4_rows(M, K, N)) return 0;
   const int64_t RM = mx::slab_rows(M);
-  return round256((int64_t)(act_code_bytes(act, RM, K) + act_scale_bytes(act, RM, K))) + slab;
+  return round256((int64_t)(act_code_bytes(act, RM, K) + act_scale_bytes(act, RM, K)));
 }
 
 int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq, const uint8_t* ws, int64_t N,
@@ -1194,7 +1166,7 @@ int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
   const hipStream_t hs = (hipStream_t)stream;
-  if (M <= mx::kFp4RowsMaxTokens)
+  if (fp4_rows(M, K, N))
     return finish(mx::launch_fp4_linear_rows(act == MX_ACT_FP8, x, M, K, ldx, wq, ws, N, bias, epilogue, y, hs),
                   "MXFP4 linear launch");
   const int64_t RM = mx::slab_rows(M);
@@ -1203,8 +1175,7 @@ int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_
   const hipError_t e = act == MX_ACT_FP4 ? mx::launch_fp4_quantize_slab(0, x, M, K, ldx, xq, xs, hs)
                                          : mx::launch_quantize_slab(0, x, M, K, ldx, xq, xs, hs);
   if (e != hipSuccess) return hip_fail(e, "quantize launch");
-  const int64_t used = round256((int64_t)(act_code_bytes(act, RM, K) + act_scale_bytes(act, RM, K)));
-  return mx_fp4_linear_slab(act, xq, xs, M, K, wq, ws, N, bias, epilogue, y, xq + used, workspace_bytes - used, stream);
+  return mx_fp4_linear_slab(act, xq, xs, M, K, wq, ws, N, bias, epilogue, y, stream);
 }
 
 int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr, const void* weight,

@@ -1,4 +1,5 @@
-// MXFP4 W4A4 linear for many tokens, on slab operands (mx_fp4_device.h):
+// Linear on MXFP4 weights for many tokens, on slab operands (mx_fp4_device.h;
+// the tokens MXFP4, or MXFP8 in their own slab layout):
 //
 //   y[m][n] = bf16_rne( epi( sum_k xhat[m][k] * what[n][k] + f32(bias[n]) ) )
 //
@@ -22,6 +23,16 @@
 // A 16-row block of a slab is [group][row][16 bytes]: copied to LDS as it is,
 // the 16 lanes of a ds_read_b128 phase (16 rows of one group) read 256
 // consecutive bytes, without bank conflicts.
+//
+// MXFP8 tokens (X8; 128-token tiles): a step's token operand is two 64-K slabs
+// of 128 rows, again 16 KB, and an MFMA takes as long as an FP8 one, so a step
+// has the shape of the MXFP8 GEMM's on 256 x 256 tiles. E4M3 operands are 32
+// bytes per lane: of the MFMA's 64 K, lane half h holds 16 h .. + 15 and 32 +
+// 16 h .. + 15, and its scale is that of K 32 h .. + 31. With the weights' choice
+// of groups, MFMA s takes bytes 32 s + 16 h .. + 15 of the row in both slabs,
+// and the lane's scale is byte s of slab h. The 64-byte rows lie in LDS with
+// chunk c of row r at c ^ ((r >> 2) & 3), which spreads a phase's 16 rows over
+// the banks.
 //
 // The accumulators start at the bias. Sums are fp32 in a fixed order.
 #include <type_traits>
@@ -49,6 +60,7 @@ struct GemmParams {
   uint16_t* y;
   int64_t RM, RN;
   int M, N, nsteps;
+  int x_slabs;  // 64-K slabs of MXFP8 tokens (the last step may have one)
   int tiles_m, tiles_n;
 };
 
@@ -71,18 +83,21 @@ constexpr int SR_OP = 8 * SR_SLOT;
 constexpr int BIAS_TABLE = SR + 2 * SR_OP;
 constexpr int LDS_BYTES = BIAS_TABLE + 4 * 256;
 
-template <int JB>
+template <int JB, bool X8>
 struct Shape {
-  static constexpr int MT = 64 * JB;        // tokens per tile
-  static constexpr int CL = 4 + JB;         // 1 KB code DMAs per wave and step
-  static constexpr int NM = 8 * JB;         // MFMAs per wave and step
-  static constexpr int NC = 2 * (4 + JB);   // 16-byte code reads per wave and step
-  static constexpr int NR = NC + 4 + JB;    // and the scale pairs
-  static constexpr int PRE = JB == 4 ? 6 : 4;   // MFMAs issued ahead of the step's barrier
-  static constexpr int SETUP = 6;               // set-up instructions behind each of them
-  static constexpr int RS = JB == 4 ? 20 : 8;   // MFMAs after it that carry reads
-  static constexpr int DS = JB == 4 ? 18 : 10;  // and loads
-  static constexpr int ND = CL + 1;             // loads: the scale DMA, then the codes
+  static_assert(!X8 || JB == 2, "MXFP8 tokens fill a region with 128 rows");
+  static constexpr int MT = 64 * JB;             // tokens per tile
+  static constexpr int XB = X8 ? 2 * JB : JB;    // 1 KB token blocks per wave and step
+  static constexpr int CL = 4 + XB;              // code DMAs per wave and step
+  static constexpr int NM = 8 * JB;              // MFMAs per wave and step
+  static constexpr int NB = X8 ? 4 * JB : 2 * JB;  // 16-byte token reads per wave and step
+  static constexpr int NC = 8 + NB;              // and with the weights'
+  static constexpr int NR = NC + 4 + JB;         // and the scale pairs
+  static constexpr int PRE = X8 ? 3 : JB == 4 ? 6 : 4;    // MFMAs issued ahead of the step's barrier
+  static constexpr int SETUP = X8 ? 11 : 6;               // set-up instructions behind each of them
+  static constexpr int RS = X8 ? 10 : JB == 4 ? 20 : 8;   // MFMAs after it that carry reads
+  static constexpr int DS = X8 ? 9 : JB == 4 ? 18 : 10;   // and loads
+  static constexpr int ND = CL + 1;              // loads: the scale DMA, then the codes
 };
 
 struct Src {
@@ -91,7 +106,8 @@ struct Src {
   const uint8_t* ws;
   const uint8_t* xs;
   uint64_t w_slab, x_slab;  // bytes between code slabs
-  int nsteps;
+  int nsteps, x_slabs;
+  int xoff;  // lane part of a token DMA's offset
 };
 
 struct LoadRes {
@@ -99,44 +115,61 @@ struct LoadRes {
   uint8_t* reg;
 };
 
-// Steps past the last load zeros (an empty resource) that nobody reads.
-template <int JB>
-__device__ __forceinline__ LoadRes load_res(const Src& S, uint8_t* smem, int j) {
+// Steps past the last (and the slab past K of MXFP8 tokens) load zeros from an
+// empty resource. MXFP8: waves 0, 1 move the step's first token slab, waves 2, 3
+// its second.
+template <int JB, bool X8>
+__device__ __forceinline__ LoadRes load_res(const Src& S, uint8_t* smem, int j, int wave) {
   LoadRes L;
   L.reg = smem + (j & 3) * REGION;
-  const uint32_t n = j < S.nsteps ? 16384u : 0u;
-  L.w = make_rsrc(S.w + (uint64_t)j * S.w_slab, n);
-  L.x = make_rsrc(S.x + (uint64_t)j * S.x_slab, n / 4 * JB);
+  L.w = make_rsrc(S.w + (uint64_t)j * S.w_slab, j < S.nsteps ? 16384u : 0u);
+  if constexpr (X8) {
+    const int sl = 2 * j + (wave >> 1);
+    L.x = make_rsrc(S.x + (uint64_t)sl * S.x_slab, sl < S.x_slabs ? 8192u : 0u);
+  } else {
+    L.x = make_rsrc(S.x + (uint64_t)j * S.x_slab, j < S.nsteps ? 4096u * JB : 0u);
+  }
   return L;
 }
 
 // Code piece D of a step: one 1 KB block (16 rows), weights and tokens in turn.
-template <int D, int JB>
-__device__ __forceinline__ void load_piece(const LoadRes& L, int wave, int lane) {
-  constexpr bool W = (D & 1) == 0 || D >= 2 * JB;
-  constexpr int u = D < 2 * JB ? D / 2 : D - JB;
-  const int q = wave * (W ? 4 : JB) + u;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(W ? L.w : L.x, (lds_ptr)(L.reg + (W ? 0 : R_X) + q * 1024), 16, lane * 16,
-                                           q * 1024, 0, 0);
+template <int D, int JB, bool X8>
+__device__ __forceinline__ void load_piece(const LoadRes& L, const Src& S, int wave, int lane) {
+  constexpr int XB = Shape<JB, X8>::XB;
+  constexpr bool W = (D & 1) == 0 || D >= 2 * XB;
+  constexpr int u = D < 2 * XB ? D / 2 : D - XB;
+  const int q = wave * (W ? 4 : XB) + u;
+  const int from = (W || !X8 ? q : q & 7) * 1024;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(W ? L.w : L.x, (lds_ptr)(L.reg + (W ? 0 : R_X) + q * 1024), 16,
+                                           W ? lane * 16 : S.xoff, from, 0, 0);
 }
 
 // Scales of steps s and s + 1 (s even): 1 KB each for the weights (waves 0, 1)
-// and the tokens (waves 2, 3; with JB = 2 the tile's 512 bytes twice).
+// and the tokens (waves 2, 3). Where a step's token scales are 512 bytes
+// (128-token tiles) lanes 32 .. 63 fetch them again, into the slot's unused half;
+// MXFP8: 256 bytes of each slab (lanes 16 .. 31 the second's).
 struct ScaleLoad {
   __amdgpu_buffer_rsrc_t r;
   uint8_t* dst;
-  int voff;
+  uint32_t voff;
 };
 
-template <int JB>
+template <int JB, bool X8>
 __device__ __forceinline__ ScaleLoad scale_res(const Src& S, uint8_t* smem, int s, int wave, int lane) {
   const bool w = wave < 2;
   const int st = s + (wave & 1);
   ScaleLoad L;
-  const uint64_t slab = (w ? S.w_slab : S.x_slab) >> 4;
-  L.r = make_rsrc((w ? S.ws : S.xs) + (uint64_t)st * slab, st < S.nsteps ? (w ? 1024u : 256u * JB) : 0u);
   L.dst = smem + SR + (w ? 0 : SR_OP) + (st & 7) * SR_SLOT;
-  L.voff = (JB == 4 || w ? lane : (lane & 31)) * 16;
+  if (X8 && !w) {
+    const uint32_t slab = (uint32_t)(S.x_slab >> 5);
+    const uint32_t n = 2 * st + 1 < S.x_slabs ? slab + 256u : 2 * st < S.x_slabs ? 256u : 0u;
+    L.r = make_rsrc(S.xs + (uint64_t)(2 * st) * slab, n);
+    L.voff = (lane & 15) * 16 + ((lane >> 4) & 1) * slab;
+  } else {
+    const uint64_t slab = (w ? S.w_slab : S.x_slab) >> 4;
+    L.r = make_rsrc((w ? S.ws : S.xs) + (uint64_t)st * slab, st < S.nsteps ? (w ? 1024u : 256u * JB) : 0u);
+    L.voff = (JB == 4 || w ? lane : (lane & 31)) * 16;
+  }
   return L;
 }
 
@@ -144,21 +177,22 @@ __device__ __forceinline__ void issue_scales(const ScaleLoad& L) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(L.r, (lds_ptr)L.dst, 16, L.voff, 0, 0, 0);
 }
 
-template <int JB>
+template <int JB, bool X8>
 struct Frags {
-  i32x4 a[4][2];   // [fragment][MFMA of the step]
-  i32x4 b[JB][2];
-  int sa[4], sb[JB];  // byte s: the scale for MFMA s
+  i32x4 a[4][2];               // [fragment][MFMA of the step]
+  i32x4 b[JB][2][X8 ? 2 : 1];  // and, of an E4M3 operand, its two halves
+  int sa[4], sb[JB];           // byte s: the scale for MFMA s
 };
 
 struct FragAddr {
   const uint8_t* a;
-  const uint8_t* b;
+  const uint8_t* b;  // E4M3: of MFMA 0
+  const uint8_t* b1;  // E4M3: of MFMA 1
   const uint8_t* sa;
   const uint8_t* sb;
 };
 
-template <int JB>
+template <int JB, bool X8>
 __device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int wn, int wm, int lane) {
   const int r32 = lane & 31, hi = lane >> 5;
   const uint8_t* reg = smem + (j & 3) * REGION;
@@ -166,40 +200,61 @@ __device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int wn
   const int off = (r32 >> 4) * 1024 + (r32 & 15) * 16 + 512 * hi;
   FragAddr A;
   A.a = reg + wn * 8192 + off;
-  A.b = reg + R_X + wm * (2048 * JB) + off;
   A.sa = sc + (wn * 128 + r32) * 4 + 2 * hi;
-  A.sb = sc + SR_OP + (wm * 32 * JB + r32) * 4 + 2 * hi;
+  if constexpr (X8) {
+    const uint8_t* row = reg + R_X + (wm * 32 * JB + r32) * 64;
+    const int sw = (r32 >> 2) & 3;
+    A.b = row + ((hi ^ sw) << 4);
+    A.b1 = row + (((2 + hi) ^ sw) << 4);
+    A.sb = sc + SR_OP + hi * 256 + (wm * 32 * JB + r32) * 2;
+  } else {
+    A.b = reg + R_X + wm * (2048 * JB) + off;
+    A.b1 = A.b;
+    A.sb = sc + SR_OP + (wm * 32 * JB + r32) * 4 + 2 * hi;
+  }
   return A;
 }
 
-// Read piece r: the fragments' 16-byte halves in the order the MFMAs take
-// them (all of MFMA 0, A and B in turn, then all of MFMA 1), then the scales.
-template <int R, int JB>
-__device__ __forceinline__ void read_piece(Frags<JB>& F, const FragAddr& A) {
-  constexpr int NC = Shape<JB>::NC, H = 4 + JB;
+// Read piece r: the fragments' 16-byte parts in the order the MFMAs take
+// them (all of MFMA 0, then all of MFMA 1; within one, the first parts of A
+// and B in turn, then the rest of A), then the scales.
+template <int R, int JB, bool X8>
+__device__ __forceinline__ void read_piece(Frags<JB, X8>& F, const FragAddr& A) {
+  constexpr int NC = Shape<JB, X8>::NC, H = NC / 2, NBH = H - 4;
   if constexpr (R < NC) {
     constexpr int s = R / H, r = R % H;
-    constexpr bool isA = (r % 2 == 0 && r < 2 * JB) || r >= 2 * JB;
-    constexpr int f = r < 2 * JB ? r / 2 : r - JB;
-    const i32x4 v = *(const i32x4*)((isA ? A.a : A.b) + f * 2048 + s * 256);
-    if constexpr (isA)
-      F.a[f][s] = v;
-    else
-      F.b[f][s] = v;
+    constexpr int both = NBH < 4 ? NBH : 4;
+    constexpr bool isA = r < 2 * both ? r % 2 == 0 : NBH < 4;
+    constexpr int f = r < 2 * both ? r / 2 : r - both;
+    if constexpr (isA) {
+      F.a[f][s] = *(const i32x4*)(A.a + f * 2048 + s * 256);
+    } else if constexpr (X8) {
+      // f: fragment f / 2, slab f % 2.
+      F.b[f / 2][s][f % 2] = *(const i32x4*)((s ? A.b1 : A.b) + (f % 2) * 8192 + (f / 2) * 2048);
+    } else {
+      F.b[f][s][0] = *(const i32x4*)(A.b + f * 2048 + s * 256);
+    }
   } else if constexpr (R < NC + 4) {
     F.sa[R - NC] = *(const uint16_t*)(A.sa + 32 * 4 * (R - NC));
   } else {
-    F.sb[R - NC - 4] = *(const uint16_t*)(A.sb + 32 * 4 * (R - NC - 4));
+    F.sb[R - NC - 4] = *(const uint16_t*)(A.sb + 32 * (X8 ? 2 : 4) * (R - NC - 4));
   }
 }
 
-template <int JB, int B, int E>
-__device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB>& F) {
+template <int JB, bool X8, int B, int E>
+__device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB, X8>& F) {
   static_for<B, E>([&](auto T) {
     constexpr int s = decltype(T)::value / (4 * JB), u = decltype(T)::value % (4 * JB), i = u / JB, j = u % JB;
     const i32x8 a = {F.a[i][s][0], F.a[i][s][1], F.a[i][s][2], F.a[i][s][3], 0, 0, 0, 0};
-    const i32x8 b = {F.b[j][s][0], F.b[j][s][1], F.b[j][s][2], F.b[j][s][3], 0, 0, 0, 0};
-    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, s, F.sa[i], s, F.sb[j]);
+    if constexpr (X8) {
+      const i32x4 &b0 = F.b[j][s][0], &b1 = F.b[j][s][1];
+      const i32x8 b = {b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 0, s, F.sa[i], s, F.sb[j]);
+    } else {
+      const i32x4& b0 = F.b[j][s][0];
+      const i32x8 b = {b0[0], b0[1], b0[2], b0[3], 0, 0, 0, 0};
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, s, F.sa[i], s, F.sb[j]);
+    }
   });
 }
 
@@ -207,17 +262,17 @@ __device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB>& F) {
 // wave's loads of step j + 1, the barrier and the address set-up; the rest run
 // with the LDS reads of step j + 1 and the loads of step j + 4 between them.
 // EVEN: j is even, and the scales of steps j + 4 and j + 5 are fetched too.
-template <bool EVEN, int JB>
-__device__ __forceinline__ void step(f32x16 (&acc)[4][JB], Frags<JB>& cur, Frags<JB>& nxt, const Src& S,
+template <bool EVEN, int JB, bool X8>
+__device__ __forceinline__ void step(f32x16 (&acc)[4][JB], Frags<JB, X8>& cur, Frags<JB, X8>& nxt, const Src& S,
                                      uint8_t* smem, int j, int wave, int wn, int wm, int lane) {
-  using Sh = Shape<JB>;
+  using Sh = Shape<JB, X8>;
   constexpr int NM = Sh::NM, PRE = Sh::PRE;
   __builtin_amdgcn_sched_barrier(0);
-  const FragAddr A = frag_addr<JB>(smem, j + 1, wn, wm, lane);
-  const LoadRes L = load_res<JB>(S, smem, j + 4);
+  const FragAddr A = frag_addr<JB, X8>(smem, j + 1, wn, wm, lane);
+  const LoadRes L = load_res<JB, X8>(S, smem, j + 4, wave);
   ScaleLoad SL;
-  if constexpr (EVEN) SL = scale_res<JB>(S, smem, j + 4, wave, lane);
-  mma<JB, 0, PRE>(acc, cur);
+  if constexpr (EVEN) SL = scale_res<JB, X8>(S, smem, j + 4, wave, lane);
+  mma<JB, X8, 0, PRE>(acc, cur);
   static_for<0, PRE>([&](auto) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
     __builtin_amdgcn_sched_group_barrier(0x006, Sh::SETUP, 0);  // set-up VALU / SALU
@@ -232,17 +287,17 @@ __device__ __forceinline__ void step(f32x16 (&acc)[4][JB], Frags<JB>& cur, Frags
     constexpr int i = decltype(I)::value;
     constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
     constexpr int d0 = i < Sh::DS ? Sh::ND * i / Sh::DS : Sh::ND, d1 = i < Sh::DS ? Sh::ND * (i + 1) / Sh::DS : Sh::ND;
-    static_for<r0, r1>([&](auto R) { read_piece<decltype(R)::value, JB>(nxt, A); });
+    static_for<r0, r1>([&](auto R) { read_piece<decltype(R)::value, JB, X8>(nxt, A); });
     static_for<d0, d1>([&](auto D) {
       constexpr int d = decltype(D)::value;
       if constexpr (d == 0) {
         if constexpr (EVEN) issue_scales(SL);
       } else {
-        load_piece<d - 1, JB>(L, wave, lane);
+        load_piece<d - 1, JB, X8>(L, S, wave, lane);
       }
     });
   });
-  mma<JB, PRE, NM>(acc, cur);
+  mma<JB, X8, PRE, NM>(acc, cur);
   static_for<0, NM - PRE>([&](auto I) {
     constexpr int i = decltype(I)::value;
     constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
@@ -310,10 +365,10 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][JB], const Gem
   }
 }
 
-template <int EPI, int JB>
+template <int EPI, int JB, bool X8>
 __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  using Sh = Shape<JB>;
+  using Sh = Shape<JB, X8>;
   int tm, tn;
   tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
   const int m0 = tm * Sh::MT, n0 = tn * BN;
@@ -329,8 +384,11 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   S.w = p.wq + (size_t)n0 * 64;
   S.x = p.x + (size_t)m0 * 64;
   S.ws = p.ws + (size_t)n0 * 4;
-  S.xs = p.xs + (size_t)m0 * 4;
+  S.xs = p.xs + (size_t)m0 * (X8 ? 2 : 4);
   S.nsteps = p.nsteps;
+  S.x_slabs = p.x_slabs;
+  // MXFP8: lane L takes row L / 4 of a block, chunk (L % 4) ^ (L / 16), into slot L % 4.
+  S.xoff = X8 ? (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4) : lane * 16;
 
   // Bias: the 128 f16 values of the wave's weight rows into its slot, ahead of
   // the ring's first loads (columns past N read what the load leaves there;
@@ -346,9 +404,9 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   // waits count on it): scales of steps 0, 1, codes 0, 1, scales 2, 3, codes 2, 3.
   static_for<0, 4>([&](auto J) {
     constexpr int j = decltype(J)::value;
-    if constexpr (j % 2 == 0) issue_scales(scale_res<JB>(S, smem, j, wave, lane));
-    const LoadRes L = load_res<JB>(S, smem, j);
-    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, JB>(L, wave, lane); });
+    if constexpr (j % 2 == 0) issue_scales(scale_res<JB, X8>(S, smem, j, wave, lane));
+    const LoadRes L = load_res<JB, X8>(S, smem, j, wave);
+    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, JB, X8>(L, S, wave, lane); });
   });
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 * Sh::CL + 2) : "memory");  // the bias
@@ -375,25 +433,25 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * Sh::CL + 1) : "memory");  // step 0
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  Frags<JB> F0, F1;
-  const FragAddr A0 = frag_addr<JB>(smem, 0, wn, wm, lane);
-  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value, JB>(F0, A0); });
+  Frags<JB, X8> F0, F1;
+  const FragAddr A0 = frag_addr<JB, X8>(smem, 0, wn, wm, lane);
+  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value, JB, X8>(F0, A0); });
   int j = 0;
   for (; j + 1 < p.nsteps; j += 2) {
-    step<true, JB>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
-    step<false, JB>(acc, F1, F0, S, smem, j + 1, wave, wn, wm, lane);
+    step<true, JB, X8>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
+    step<false, JB, X8>(acc, F1, F0, S, smem, j + 1, wave, wn, wm, lane);
   }
-  if (j < p.nsteps) step<true, JB>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
+  if (j < p.nsteps) step<true, JB, X8>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   store_tile<EPI, JB>(acc, p, smem + wave * 32768, m0, n0, rows_m, rows_n, wn, wm, lane);
 }
 
-template <int EPI, int JB>
+template <int EPI, int JB, bool X8>
 hipError_t launch(const GemmParams& p, hipStream_t st) {
   static bool configured = false;  // per instantiation; benign race (idempotent)
-  auto kern = fp4_gemm_kernel<EPI, JB>;
+  auto kern = fp4_gemm_kernel<EPI, JB, X8>;
   if (!configured) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
     if (e != hipSuccess) return e;
@@ -405,7 +463,7 @@ hipError_t launch(const GemmParams& p, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_fp4_linear_tiles(int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+hipError_t launch_fp4_linear_tiles(int fp8, int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                                    const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                    hipStream_t stream) {
   GemmParams p;
@@ -420,10 +478,12 @@ hipError_t launch_fp4_linear_tiles(int token_tile, const uint8_t* xq, const uint
   p.M = (int)M;
   p.N = (int)N;
   p.nsteps = (int)fp4_slabs(K);
+  p.x_slabs = (int)(K / 64);
   p.tiles_m = (int)((M + token_tile - 1) / token_tile);
   p.tiles_n = (int)((N + BN - 1) / BN);
-  if (token_tile == 128) return epi == 1 ? launch<1, 2>(p, stream) : launch<0, 2>(p, stream);
-  return epi == 1 ? launch<1, 4>(p, stream) : launch<0, 4>(p, stream);
+  if (fp8) return epi == 1 ? launch<1, 2, true>(p, stream) : launch<0, 2, true>(p, stream);
+  if (token_tile == 128) return epi == 1 ? launch<1, 2, false>(p, stream) : launch<0, 2, false>(p, stream);
+  return epi == 1 ? launch<1, 4, false>(p, stream) : launch<0, 4, false>(p, stream);
 }
 
 }  // namespace mx

@@ -16,13 +16,15 @@
 // Output: lane l holds D[4 (l / 16) + i][l % 16]. A 16-row block of an MXFP4
 // slab is one 1 KB run in lane order, so operands go from memory straight to
 // registers; nothing is shared between the waves but the final sums.
+//
+// Measured (one pass on operands not in the L2): 5120 x 5120 weights, 16
+// tokens 5.0 us (2.8 TB/s of weights, 4.9 us for one token; launch and the
+// first round trip are about half of it), 15360 x 5120 8.5 us (4.9 TB/s).
 #include "mx_fp4_device.h"
 #include "mx_internal.h"
 
 namespace mx {
 namespace {
-
-constexpr int kWaves = 8;
 
 // Token operand: MXFP4 or MXFP8 slab, or bf16 rows quantized to either.
 enum { SRC_FP4 = 0, SRC_FP8 = 1, SRC_BF16_FP4 = 2, SRC_BF16_FP8 = 3 };
@@ -76,41 +78,58 @@ struct Step {
   int sa[WB], sb[TB];
 };
 
+// Loads slab `sl`. Past the wave's range (sl >= s1) nothing is read: the
+// buffer resources are empty and every value becomes zero, so the loop's loads
+// stay in one straight run.
 template <int SRC, int WB, int TB>
-__device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams& p, int64_t sl, int n0, int m0,
+__device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams& p, int sl, int s1, int n0, int m0,
                                           int lane) {
   const int r = lane & 15, G = lane >> 4;
-  const uint8_t* a = p.wq + (sl * (p.RN / 16) + n0 / 16) * 1024 + lane * 16;
-  const uint8_t* sa = p.ws + (sl * p.RN + n0 + r) * 4 + G;
+  const bool on = sl < s1;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.wq + ((int64_t)sl * (p.RN / 16) + n0 / 16) * 1024, on ? WB * 1024 : 0);
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.ws + ((int64_t)sl * p.RN + n0) * 4, on ? WB * 64 : 0);
 #pragma unroll
   for (int i = 0; i < WB; ++i) {
-    s.a[i] = *(const i32x4*)(a + i * 1024);
-    s.sa[i] = sa[i * 64];
+    s.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, lane * 16 + i * 1024, 0, 0);
+    s.sa[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, r * 4 + G + i * 64, 0, 0);
   }
-  const i32x4 zero = {0, 0, 0, 0};
+  if constexpr (SRC == SRC_FP4) {
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + ((int64_t)sl * (p.RM / 16) + m0 / 16) * 1024, on ? TB * 1024 : 0);
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.xs + ((int64_t)sl * p.RM + m0) * 4, on ? TB * 64 : 0);
 #pragma unroll
-  for (int j = 0; j < TB; ++j) {
-    if constexpr (SRC == SRC_FP4) {
-      s.b[j][0] = *(const i32x4*)(p.x + (sl * (p.RM / 16) + m0 / 16 + j) * 1024 + lane * 16);
-      s.sb[j] = p.xs[(sl * p.RM + m0 + 16 * j + r) * 4 + G];
-    } else if constexpr (SRC == SRC_FP8) {
-      // Two 64-K slabs; the second is past K where K % 128 = 64 (its codes
-      // are taken as zeros: the weights' are, but a product with NaN bits
-      // there would not be).
-      const bool two = sl * 128 + 64 < p.K;
-      const int64_t row = m0 + 16 * j + r;
-      s.b[j][0] = *(const i32x4*)(p.x + (2 * sl * p.RM + row) * 64 + 16 * G);
-      s.b[j][1] = two ? *(const i32x4*)(p.x + ((2 * sl + 1) * p.RM + row) * 64 + 16 * G) : zero;
-      s.sb[j] = G < 2 || two ? p.xs[((2 * sl + (G >> 1)) * p.RM + row) * 2 + (G & 1)] : 0;
-    } else {
-      // Rows past M repeat the last one; their outputs are not stored.
-      const int64_t row = min(m0 + 16 * j + r, p.M - 1);
-      const uint16_t* x = (const uint16_t*)p.x + row * p.ldx;
+    for (int j = 0; j < TB; ++j) {
+      s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, lane * 16 + j * 1024, 0, 0);
+      s.sb[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt, r * 4 + G + j * 64, 0, 0);
+    }
+  } else if constexpr (SRC == SRC_FP8) {
+    // Two 64-K slabs of 64-byte rows; the second is past K where K % 128 = 64.
+    // The lane's scale is that of K group G: slab G / 2, byte G % 2.
+    const bool two = on && sl * 128 + 64 < p.K;
+    const uint8_t* x0 = p.x + (2 * (int64_t)sl * p.RM + m0) * 64;
+    const uint8_t* t0 = p.xs + (2 * (int64_t)sl * p.RM + m0) * 2;
+    const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(x0, on ? TB * 1024 : 0);
+    const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(x0 + p.RM * 64, two ? TB * 1024 : 0);
+    const __amdgpu_buffer_rsrc_t rt0 = make_rsrc(t0, on ? TB * 32 : 0);
+    const __amdgpu_buffer_rsrc_t rt1 = make_rsrc(t0 + p.RM * 2, two ? TB * 32 : 0);
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb0, r * 64 + 16 * G + j * 1024, 0, 0);
+      s.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rb1, r * 64 + 16 * G + j * 1024, 0, 0);
+      const int c0 = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt0, r * 2 + (G & 1) + j * 32, 0, 0);
+      const int c1 = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt1, r * 2 + (G & 1) + j * 32, 0, 0);
+      s.sb[j] = G < 2 ? c0 : c1;
+    }
+  } else {
+    // Rows past M repeat the last one; their outputs are not stored.
+    const int kend = on ? p.K : 0;
+#pragma unroll
+    for (int j = 0; j < TB; ++j) {
+      const uint16_t* x = (const uint16_t*)p.x + min(m0 + 16 * j + r, p.M - 1) * p.ldx;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         // E2M1: 32 consecutive elements; E4M3: two runs of 16.
-        const int64_t k = sl * 128 + (SRC == SRC_BF16_FP4 ? 32 * G + 8 * u : 64 * (u >> 1) + 16 * G + 8 * (u & 1));
-        s.b[j][u] = k < p.K ? *(const i32x4*)(x + k) : zero;
+        const int k = sl * 128 + (SRC == SRC_BF16_FP4 ? 32 * G + 8 * u : 64 * (u >> 1) + 16 * G + 8 * (u & 1));
+        s.b[j][u] = k < kend ? *(const i32x4*)(x + k) : i32x4{0, 0, 0, 0};
       }
     }
   }
@@ -161,10 +180,15 @@ __device__ __forceinline__ void mma_step(f32x4 (&acc)[WB][TB], const Step<SRC, W
   }
 }
 
-// U: slabs whose loads are issued together.
-template <int SRC, int WB, int TB, int U, int EPI>
-__global__ __launch_bounds__(64 * kWaves) void fp4_few_kernel(FewParams p) {
-  __shared__ f32x4 sums[kWaves][WB * TB][64];
+// NW waves; D slabs in flight per wave. The partial sums go through LDS in
+// rounds of at most kRound fragments, so that they take at most kRound KB per
+// wave of it.
+constexpr int kRound = 8;
+
+template <int SRC, int WB, int TB, int NW, int D, int EPI>
+__global__ __launch_bounds__(64 * NW) void fp4_few_kernel(FewParams p) {
+  constexpr int NF = WB * TB, C = NF < kRound ? NF : kRound;
+  __shared__ f32x4 sums[NW][C][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Token tile fastest within an XCD's range of workgroups, so that those
@@ -173,66 +197,119 @@ __global__ __launch_bounds__(64 * kWaves) void fp4_few_kernel(FewParams p) {
   const int tn = (int)(lid / (uint32_t)p.tiles_m), tm = (int)(lid - (uint32_t)tn * (uint32_t)p.tiles_m);
   const int n0 = tn * 16 * WB, m0 = tm * 16 * TB;
   const int S = (int)fp4_slabs(p.K);
-  const int s0 = wave * S / kWaves, s1 = (wave + 1) * S / kWaves;
+  const int s0 = wave * S / NW, s1 = (wave + 1) * S / NW;
   f32x4 acc[WB][TB];
 #pragma unroll
   for (int i = 0; i < WB; ++i)
 #pragma unroll
     for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int s = s0; s < s1; s += U) {
-    // Slabs past the wave's range are loaded as its last one and not used,
-    // so that the loads stay in one straight run.
-    Step<SRC, WB, TB> st[U];
+  Step<SRC, WB, TB> st[D];
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_step(st[u], p, min(s + u, s1 - 1), n0, m0, lane);
+  for (int u = 0; u < D; ++u) load_step(st[u], p, s0 + u, s1, n0, m0, lane);
+  for (int s = s0; s < s1; s += D) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < s1) mma_step(acc, st[u], lane);
+    for (int u = 0; u < D; ++u) {
+      mma_step(acc, st[u], lane);
+      load_step(st[u], p, s + u + D, s1, n0, m0, lane);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < WB; ++i)
+  for (int f0 = 0; f0 < NF; f0 += C) {
+    if (f0 > 0) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < TB; ++j) sums[wave][i * TB + j][lane] = acc[i][j];
-  __syncthreads();
-  for (int f = wave; f < WB * TB; f += kWaves) {
-    const int i = f / TB, j = f - i * TB;
-    const int n = n0 + 16 * i + 4 * (lane >> 4), m = m0 + 16 * j + (lane & 15);
-    f32x4 v = sums[0][f][lane];
+    for (int f = f0; f < f0 + C && f < NF; ++f) sums[wave][f - f0][lane] = acc[f / TB][f % TB];
+    __syncthreads();
+    for (int c = wave; c < C && f0 + c < NF; c += NW) {
+      const int i = (f0 + c) / TB, j = f0 + c - i * TB;
+      const int n = n0 + 16 * i + 4 * (lane >> 4), m = m0 + 16 * j + (lane & 15);
+      f32x4 v = sums[0][c][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      const f32x4 o = sums[w][f][lane];
+      for (int w = 1; w < NW; ++w) {
+        const f32x4 o = sums[w][c][lane];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += o[r];
+        for (int r = 0; r < 4; ++r) v[r] += o[r];
+      }
+      if (n >= p.N || m >= p.M) continue;
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] += (float)__builtin_bit_cast(_Float16, p.bias[n + r]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = epilogue<EPI>(v[r]);
+      const bf16x2 q0 = {(__bf16)v[0], (__bf16)v[1]}, q1 = {(__bf16)v[2], (__bf16)v[3]};
+      *(i32x2*)(p.y + (int64_t)m * p.N + n) = i32x2{__builtin_bit_cast(int, q0), __builtin_bit_cast(int, q1)};
     }
-    if (n >= p.N || m >= p.M) continue;
-    if (p.bias != nullptr) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] += (float)__builtin_bit_cast(_Float16, p.bias[n + r]);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = epilogue<EPI>(v[r]);
-    const bf16x2 q0 = {(__bf16)v[0], (__bf16)v[1]}, q1 = {(__bf16)v[2], (__bf16)v[3]};
-    *(i32x2*)(p.y + (int64_t)m * p.N + n) = i32x2{__builtin_bit_cast(int, q0), __builtin_bit_cast(int, q1)};
   }
 }
 
-template <int SRC, int WB, int TB, int U>
+template <int SRC, int WB, int TB, int NW, int D>
 hipError_t launch_few(FewParams& p, int epi, hipStream_t st) {
   p.tiles_m = (p.M + 16 * TB - 1) / (16 * TB);
   const unsigned blocks = (unsigned)(p.tiles_m * ((p.N + 16 * WB - 1) / (16 * WB)));
   if (epi == 1)
-    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, U, 1>), dim3(blocks), dim3(64 * kWaves), 0, st, p);
+    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, D, 1>), dim3(blocks), dim3(64 * NW), 0, st, p);
   else
-    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, U, 0>), dim3(blocks), dim3(64 * kWaves), 0, st, p);
+    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, D, 0>), dim3(blocks), dim3(64 * NW), 0, st, p);
   return hipGetLastError();
 }
 
+// Fragments (16 x 16 outputs) per workgroup: enough that about 256 workgroups
+// or fewer cover the output (one per CU), a power of two.
+int fragments(int64_t M, int64_t N) {
+  const int64_t total = ((M + 15) / 16) * (N / 16);
+  int f = 1;
+  while (f < 32 && f * 256 < total) f *= 2;
+  return f;
+}
+
+// Tile shapes, from a sweep over WB, TB, waves and slabs in flight at N = 1024 ..
+// 15360, K = 4096 .. 14336 and 1 to 512 tokens. Eight waves with one slab in
+// flight are best nearly throughout: a wave's share of K is a handful of slabs,
+// and the other waves hide its latency better than deeper prefetching. At
+// 5120 x 5120: 16 tokens 5.0 us on 32 x 16 tiles (16 x 16: 5.4, 64 x 16: 5.9);
+// 128 tokens 8.9 us on 64 x 64 (128 x 32: 10.3). MXFP8 tokens cost twice their
+// MXFP4 bytes, so their tiles are longer in weight rows: 128 tokens 12.7 us on
+// 128 x 32 by four waves with two slabs in flight (eight waves 13.5; 64 x 64:
+// 13.4). Splitting K over workgroups as well, with a second kernel adding the
+// parts, was slower at every shape but MXFP8 tokens with K = 13824, where it
+// gained up to a fifth (128 tokens: 21.3 against 26.7 us): not kept.
+hipError_t dispatch_fp4(FewParams& p, int epi, hipStream_t st) {
+  const int f = fragments(p.M, p.N);
+  if (f == 1) return launch_few<SRC_FP4, 1, 1, 8, 1>(p, epi, st);
+  if (f == 2) return launch_few<SRC_FP4, 2, 1, 8, 1>(p, epi, st);
+  if (p.M <= 16) return launch_few<SRC_FP4, 4, 1, 8, 1>(p, epi, st);
+  if (f == 4) return launch_few<SRC_FP4, 2, 2, 8, 1>(p, epi, st);
+  if (f == 8 || p.M <= 32) return launch_few<SRC_FP4, 4, 2, 8, 1>(p, epi, st);
+  if (f == 16 || p.M <= 64) return launch_few<SRC_FP4, 4, 4, 8, 1>(p, epi, st);
+  return launch_few<SRC_FP4, 4, 8, 8, 1>(p, epi, st);
+}
+
+hipError_t dispatch_fp8(FewParams& p, int epi, hipStream_t st) {
+  const int f = fragments(p.M, p.N);
+  if (f == 1) return launch_few<SRC_FP8, 1, 1, 8, 1>(p, epi, st);
+  if (f == 2) return launch_few<SRC_FP8, 2, 1, 8, 1>(p, epi, st);
+  if (p.M <= 16 || (f == 4 && p.M <= 32)) return launch_few<SRC_FP8, 4, 1, 8, 1>(p, epi, st);
+  if (f == 4) return launch_few<SRC_FP8, 2, 2, 8, 1>(p, epi, st);
+  if (f == 8) return launch_few<SRC_FP8, 4, 2, 8, 1>(p, epi, st);
+  if (f == 16 || p.M <= 32) return launch_few<SRC_FP8, 8, 2, 4, 2>(p, epi, st);
+  return launch_few<SRC_FP8, 8, 4, 4, 1>(p, epi, st);
+}
+
+// bf16 rows (at most 16): one token fragment. Rounding to E4M3 keeps a wave
+// longer than its loads, so long rows take 16 waves (1 x 13824 x 5120: 13.1
+// against 15.1 us).
 template <int SRC>
-hipError_t dispatch_slab(FewParams& p, int epi, hipStream_t st) {
-  if (p.M <= 16) return launch_few<SRC, 1, 1, 6>(p, epi, st);
-  if (p.M <= 32) return launch_few<SRC, 1, 2, 4>(p, epi, st);
-  if (p.M <= 64) return launch_few<SRC, 1, 4, 2>(p, epi, st);
-  return launch_few<SRC, 1, 8, 2>(p, epi, st);
+hipError_t dispatch_rows(FewParams& p, int epi, hipStream_t st) {
+  const int f = fragments(p.M, p.N);
+  if constexpr (SRC == SRC_BF16_FP8) {
+    if (p.K >= 8192) {
+      if (f == 1) return launch_few<SRC, 1, 1, 16, 1>(p, epi, st);
+      if (f == 2) return launch_few<SRC, 2, 1, 16, 1>(p, epi, st);
+    }
+  }
+  if (f == 1) return launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
+  if (f == 2) return launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
+  return launch_few<SRC, 4, 1, 8, 1>(p, epi, st);
 }
 
 }  // namespace
@@ -253,7 +330,7 @@ hipError_t launch_fp4_linear_few(int fp8, const uint8_t* xq, const uint8_t* xs, 
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  return fp8 ? dispatch_slab<SRC_FP8>(p, epi, stream) : dispatch_slab<SRC_FP4>(p, epi, stream);
+  return fp8 ? dispatch_fp8(p, epi, stream) : dispatch_fp4(p, epi, stream);
 }
 
 hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,
@@ -272,7 +349,7 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  return fp8 ? launch_few<SRC_BF16_FP8, 1, 1, 4>(p, epi, stream) : launch_few<SRC_BF16_FP4, 1, 1, 4>(p, epi, stream);
+  return fp8 ? dispatch_rows<SRC_BF16_FP8>(p, epi, stream) : dispatch_rows<SRC_BF16_FP4>(p, epi, stream);
 }
 
 }  // namespace mx

@@ -113,9 +113,8 @@ hipError_t launch_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t ro
                                   uint8_t* so, hipStream_t stream);
 
 // Few-token MXFP4-weight linear (mx_fp4_small.hip) on a token slab (fp8: an
-// MXFP8 slab, else an MXFP4 one), or on bf16 rows (M <= kFp4RowsMaxTokens)
-// quantized in the kernel.
-constexpr int64_t kFp4RowsMaxTokens = 16;
+// MXFP8 slab, else an MXFP4 one), or on bf16 rows (at most 16) quantized in
+// the kernel.
 hipError_t launch_fp4_linear_few(int fp8, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                                  const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                  hipStream_t stream);
@@ -123,9 +122,9 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
                                   const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                   hipStream_t stream);
 
-// W4A4 linear on token_tile (128 or 256) x 256 tiles (mx_fp4_gemm.hip), both
-// operands MXFP4 slabs; N % 16 == 0, tiles below 2^24.
-hipError_t launch_fp4_linear_tiles(int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
+// MXFP4-weight linear on token_tile (128 or 256; 128 with an MXFP8 token slab)
+// x 256 tiles (mx_fp4_gemm.hip); N % 16 == 0, tiles below 2^24.
+hipError_t launch_fp4_linear_tiles(int fp8, int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                                    const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                    hipStream_t stream);
 

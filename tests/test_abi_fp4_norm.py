@@ -63,8 +63,8 @@ def test_layout_conversions_reject_bad_arguments(L):
     assert un(rows=0, q=0, s=0, qo=0, so=0) == OK
 
 
-def slab(act=1, xq=A, xs=B, M=8, K=96, wq=C, ws=D, N=32, bias=0, epi=0, y=E, work=0, nb=0):
-    return mx().lib().mx_fp4_linear_slab(act, P(xq), P(xs), M, K, P(wq), P(ws), N, P(bias), epi, P(y), P(work), nb, P(0))
+def slab(act=1, xq=A, xs=B, M=8, K=96, wq=C, ws=D, N=32, bias=0, epi=0, y=E):
+    return mx().lib().mx_fp4_linear_slab(act, P(xq), P(xs), M, K, P(wq), P(ws), N, P(bias), epi, P(y), P(0))
 
 
 def test_linear_slab_rejects_bad_arguments():
@@ -93,12 +93,13 @@ def test_one_call_rejects_bad_arguments(L):
     assert one(nb=need - 1) == INV and one(work=0) == INV and one(work=F + 16) == INV
     assert one(work=A - 256) == INV and one(work=E) == INV and one(work=C) == INV  # overlaps x, y, the codes
     assert one(M=0, x=0, wq=0, ws=0, y=0) == OK
-    # Up to 16 tokens no workspace is asked for.
-    assert L.mx_fp4_linear_ws_bytes(16, 96, 32, 1) == 0
-    for f in (L.mx_fp4_linear_ws_bytes, L.mx_fp4_linear_slab_ws_bytes):
-        assert f(8, 40, 32, 1) == -1 and f(-1, 96, 32, 1) == -1 and f(8, 96, -1, 1) == -1
-        assert f(8, 96, 32, 0) == -1 and f(8, 96, 32, 2) == -1
-        assert f(0, 96, 32, 1) == 0 and f(8, 96, 0, 1) == 0
+    f = L.mx_fp4_linear_ws_bytes
+    # A few tokens ask for no workspace; long rows of them do, and so do 17.
+    assert f(16, 96, 32, 1) == 0 and f(16, 6144, 32, 1) == 0 and f(16, 6176, 32, 1) > 0 and f(17, 96, 32, 1) > 0
+    assert f(300, 128, 32, 1) == 512 * (64 + 4) and f(300, 128, 32, 0) == 512 * (128 + 4)
+    assert f(8, 40, 32, 1) == -1 and f(-1, 96, 32, 1) == -1 and f(8, 96, -1, 1) == -1
+    assert f(8, 96, 32, 0) == -1 and f(8, 96, 32, 2) == -1
+    assert f(0, 96, 32, 1) == 0 and f(8, 96, 0, 1) == 0
 
 
 def norm(x=A, ldx=64, res=0, rdt=0, ldr=64, w=0, wdt=0, eps=1e-6, M=4, K=64, ro=0, ldo=64, y=0, ldy=64, act=0, q=B, s=C):

@@ -168,8 +168,8 @@ def test_no_gain_dropped_outputs_and_empty():
     m = mx()
     xd, rd = x.to(d), r.to(d)
     s2 = m.Slab(torch.empty_like(slab.q), torch.empty_like(slab.s), 33)
-    m._run(m.lib().mx_rmsnorm_slab, xd.device, m._ptr(xd), 256, m._ptr(rd), 0, 256, m._ptr(None), 0, 1e-6, 33, 256,
-           m._ptr(None), 0, m._ptr(None), 0, 0, m._ptr(s2.q), m._ptr(s2.s))
+    m._run(m.lib().mx_rmsnorm_slab, xd.device, m._adr(xd), 256, m._adr(rd), 0, 256, m._adr(None), 0, 1e-6, 33, 256,
+           m._adr(None), 0, m._adr(None), 0, 0, m._adr(s2.q), m._adr(s2.s))
     assert torch.equal(s2.q, slab.q) and torch.equal(s2.s, slab.s) and torch.equal(rd.cpu(), r)
     empty, h = m.mx_rmsnorm_slab(torch.empty((0, 64), dtype=torch.bfloat16, device=d))
     assert empty.q.numel() == 0 and h is None
