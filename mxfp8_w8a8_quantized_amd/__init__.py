@@ -782,12 +782,11 @@ def _fp4_shapes(rows, K):
     return torch.Size((S, R // 16, 4, 16, 16)), torch.Size((S, R, 4))
 
 
-def _fp4_out(rows, K, dev, out):
-    sq, ss = _fp4_shapes(rows, K)
+def _fp4_out(rows, K, like, out):
     if out is None:
-        return FP4Slab(torch.empty(sq, dtype=torch.uint8, device=dev), torch.empty(ss, dtype=torch.uint8, device=dev),
-                       rows, K)
-    _need_fp4(out, "out", dev)
+        sq, ss = _fp4_shapes(rows, K)
+        return FP4Slab(like.new_empty(sq, dtype=torch.uint8), like.new_empty(ss, dtype=torch.uint8), rows, K)
+    _need_fp4(out, "out", like.device)
     if out.rows != rows or out.K != K:
         raise ValueError(f"out must hold {rows} rows of K = {K}")
     return out
@@ -796,11 +795,12 @@ def _fp4_out(rows, K, dev, out):
 def _need_fp4(t, name, dev):
     if not isinstance(t, FP4Slab):
         raise TypeError(f"{name} must be an FP4Slab")
-    _need(t.q, name + ".q", torch.uint8, dev)
-    _need(t.s, name + ".s", torch.uint8, dev)
-    sq, ss = _fp4_shapes(t.rows, t.K)
-    if t.q.shape != sq or t.s.shape != ss:
-        raise ValueError(f"{name} is not an MXFP4 slab of {t.rows} rows and K = {t.K}")
+    q, s, rows, K = t
+    _need(q, name, torch.uint8, dev)
+    _need(s, name, torch.uint8, dev)
+    sq, ss = _fp4_shapes(rows, K)
+    if q.shape != sq or s.shape != ss:
+        raise ValueError(f"{name} is not an MXFP4 slab of {rows} rows and K = {K}")
 
 
 def _act_format(act):
@@ -810,9 +810,9 @@ def _act_format(act):
 
 
 def _need_rows(x, name, dtypes):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in dtypes:
+    if not isinstance(x, torch.Tensor) or x.dtype not in dtypes or x.dim() != 2:
         raise TypeError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    if x.stride(1) != 1 and x.shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
 
 
@@ -829,7 +829,7 @@ _DTYPES = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
 
 
 def _adr(t):
-    return t.data_ptr() if t is not None and t.numel() > 0 else None
+    return None if t is None else t.data_ptr()
 
 
 def _run(fn, dev, *args):
@@ -849,7 +849,7 @@ def _fp4_quantize(x, name, dtypes, out):
     rows, K = x.shape
     if K == 0 or K % 32 != 0:
         raise ValueError("MXFP4 needs K to be a positive multiple of 32")
-    return _fp4_out(rows, K, x.device, out)
+    return _fp4_out(rows, K, x, out)
 
 
 def mx_fp4_quantize_act_slab(x, out=None):
@@ -895,7 +895,7 @@ def mx_fp4_slab_pack(q, s, out=None):
     rows, K = q.shape[0], 2 * q.shape[1]
     if s.shape != (rows, K // 32):
         raise ValueError("s must be [rows, K/32]")
-    out = _fp4_out(rows, K, dev, out)
+    out = _fp4_out(rows, K, q, out)
     _run(lib().mx_fp4_slab_pack, dev, _adr(q), _adr(s), rows, K, _adr(out.q), _adr(out.s))
     return out
 
@@ -913,14 +913,15 @@ def mx_fp4_slab_unpack(slab, out=None):
 
 def _fp4_linear_out(M, w, bias, y, dev):
     _need_fp4(w, "w", dev)
+    N = w.rows
     if bias is not None:
         _need(bias, "bias", torch.float16, dev)
-        if bias.shape != (w.rows,):
+        if bias.shape != (N,):
             raise ValueError("bias must be f16 [N]")
     if y is None:
-        return torch.empty((M, w.rows), dtype=torch.bfloat16, device=dev)
+        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     _need(y, "y", torch.bfloat16, dev)
-    if tuple(y.shape) != (M, w.rows):
+    if y.shape != (M, N):
         raise ValueError("y must be bf16 [M, N]")
     return y
 
@@ -1003,7 +1004,7 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
         _need_rows(residual, "residual", (torch.bfloat16, torch.float32))
         rdt = _DTYPES[residual.dtype]
         if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=residual.dtype, device=dev)
+            residual_out = residual.new_empty((M, K))
         _need_rows(residual_out, "residual_out", (residual.dtype,))
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
@@ -1011,7 +1012,7 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
         if weight.dtype not in _DTYPES:
             raise TypeError("weight must be bfloat16 or float32")
         _need(weight, "weight", weight.dtype, dev)
-        if tuple(weight.shape) != (K,):
+        if weight.shape != (K,):
             raise ValueError(f"weight must be [{K}]")
         wdt = _DTYPES[weight.dtype]
     if y is not None:
@@ -1019,7 +1020,7 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
     for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
         if t is not None and (t.device != dev or t.shape != x.shape):
             raise ValueError(f"{name} must be [{M}, {K}] on {dev}")
-    out = _fp4_out(M, K, dev, out) if act == "fp4" else _slab_out(M, K, dev, out)
+    out = _fp4_out(M, K, x, out) if act == "fp4" else _slab_out(M, K, dev, out)
     _run(lib().mx_rmsnorm_slab, dev, _adr(x), _pitch(x), _adr(residual), rdt, 0 if residual is None else _pitch(residual),
          _adr(weight), wdt, float(eps), M, K, _adr(residual_out), 0 if residual_out is None else _pitch(residual_out),
          _adr(y), 0 if y is None else _pitch(y), fmt, _adr(out.q), _adr(out.s))
