@@ -565,9 +565,8 @@ int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t
  * sums FP32. bias f16 [N] or NULL; y bf16 [M][N]; N % 16 == 0 (else
  * MX_ERR_UNSUPPORTED). Codes and y 16-byte aligned, scales 4-byte aligned; y
  * must not overlap an input. One kernel, chosen by the shape and the format
- * alone (a few-token kernel up to 2^21 outputs, 128 or 256 token tiles above),
- * so results are deterministic. Fewer than 2^24 tiles of 256 x 256 (else
- * MX_ERR_UNSUPPORTED). */
+ * alone, so results are deterministic. Fewer than 2^24 tiles of 128 x 128
+ * (else MX_ERR_UNSUPPORTED). */
 int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                        const uint8_t* wq, const uint8_t* ws, int64_t N,
                        const void* bias, int epilogue, void* y, void* stream);

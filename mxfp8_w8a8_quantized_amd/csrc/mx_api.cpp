@@ -952,12 +952,16 @@ uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
   return act == MX_ACT_FP4 ? fp4_scale_bytes(R, K) : (uint64_t)R * (K / 32);
 }
 
-// The few-token kernel up to this many outputs (8192 fragments of 16 x 16, at
-// most 32 in each of 256 workgroups), the tiled GEMMs above: 256 x 5120 x 5120
-// takes 13.3 us there against 16.1 (MXFP8 activations 17.8 against 24.1), 512 x
-// 5120 x 5120 20.1 against 16.0 (30.4 against 24.3).
-constexpr int64_t kFp4FewFragments = 8192;
-bool fp4_few(int64_t M, int64_t N) { return ((M + 15) / 16) * (N / 16) <= kFp4FewFragments; }
+// The few-token kernel up to 4096 fragments of 16 x 16 outputs (16 in each of
+// 256 workgroups), up to 8192 where K is long; the tiled GEMMs above. Their
+// loops run alike; the few-token kernel has the costlier end (the waves' sums),
+// the tiles fewer workgroups: 128 x 5120 x 5120 8.9 us against 12.5 (MXFP8
+// activations 12.7 against 16.0), 256 x 5120 x 5120 14.2 against 12.6 (19.2
+// against 16.4), 256 x 13824 x 5120 24.5 against 28 (36 against 38).
+bool fp4_few(int64_t M, int64_t K, int64_t N) {
+  const int64_t fragments = ((M + 15) / 16) * (N / 16);
+  return fragments <= 4096 || (fragments <= 8192 && K > 12288);
+}
 
 // bf16 rows are quantized inside the product's kernel, by every workgroup for
 // itself, up to 16 tokens and this many elements; past that a quantizer
@@ -966,13 +970,8 @@ bool fp4_few(int64_t M, int64_t N) { return ((M + 15) / 16) * (N / 16) <= kFp4Fe
 constexpr int64_t kFp4RowsMaxTokens = 16;
 constexpr int64_t kFp4RowsMaxElements = 98304;
 bool fp4_rows(int64_t M, int64_t K, int64_t N) {
-  return M <= kFp4RowsMaxTokens && M * K <= kFp4RowsMaxElements && fp4_few(M, N);
+  return M <= kFp4RowsMaxTokens && M * K <= kFp4RowsMaxElements && fp4_few(M, K, N);
 }
-
-// MXFP4 activations on 128-token tiles while the 256 x 256 tiles are at most
-// this many (half a round of CUs): 1024 x 5120 x 5120 (80 tiles) 18.1 against
-// 26.2 us, 2048 x 5120 x 5120 (160) 37.4 against 31.5.
-constexpr int64_t kFp4HalfTiles = 128;
 
 int check_act_k(int act, int64_t K) {
   if (act != MX_ACT_FP8 && act != MX_ACT_FP4) return fail(MX_ERR_INVALID_ARGUMENT, "unknown activation format %d", act);
@@ -1118,19 +1117,21 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   if (overlap(y, yb, xq, xb) || overlap(y, yb, xs, sb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
     return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
   const hipStream_t hs = (hipStream_t)stream;
-  if (fp4_few(M, N)) {
+  if (fp4_few(M, K, N)) {
     if ((st = check_device()) != MX_OK) return st;
     (void)hipGetLastError();
     return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y, hs),
                   "MXFP4 linear launch");
   }
-  const int64_t tiles = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
   if (tiles >= kMaxSplitWorkgroups)
-    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 256 x 256 exceed 2^24", (long long)tiles);
+    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
-  return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, act == MX_ACT_FP8 || tiles <= kFp4HalfTiles ? 128 : 256, xq,
-                                            xs, M, K, wq, ws, N, bias, epilogue, y, hs),
+  int weight_tile, token_tile;
+  mx::fp4_linear_tile(act == MX_ACT_FP8, M, N, &weight_tile, &token_tile);
+  return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, weight_tile, token_tile, xq, xs, M, K, wq, ws, N, bias,
+                                            epilogue, y, hs),
                 "MXFP4 linear launch");
 }
 

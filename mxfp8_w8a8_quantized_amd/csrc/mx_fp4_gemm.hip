@@ -3,14 +3,14 @@
 //
 //   y[m][n] = bf16_rne( epi( sum_k xhat[m][k] * what[n][k] + f32(bias[n]) ) )
 //
-// 256 weight rows x 64 JB tokens per workgroup, four waves of 128 x 32 JB
+// 64 IA weight rows x 64 JB tokens per workgroup, four waves of 32 IA x 32 JB
 // (one per SIMD) on v_mfma_scale_f32_32x32x64_f8f6f4 with the weights as the A
 // operand. K advances in steps of one 128-K slab: 16 KB of codes per 256 rows,
 // the bytes of an MXFP8 step of 64 K, for two MFMAs per fragment pair of half
 // an FP8 MFMA's duration each. So the balance between matrix core, LDS and
 // loads is the one of the MXFP8 slab GEMM at twice the arithmetic, and the
-// same pipeline feeds it: a ring of four LDS regions, each wave issuing a
-// quarter of the refill of step j + 4 during step j; the fragments of step
+// same pipeline feeds it: a ring of RING LDS regions, each wave issuing a
+// quarter of the refill of step j + RING during step j; the fragments of step
 // j + 1 read from LDS into a second register set between the MFMAs of step j;
 // one barrier per step, crossed while MFMAs issued ahead of it still run.
 //
@@ -46,7 +46,6 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-constexpr int BN = 256;  // weight rows per tile
 constexpr int NT = 256;
 constexpr int kDropOffset = 1 << 30;  // beyond every resource: the store is dropped
 constexpr int kStoreAux = 2;          // non-temporal
@@ -72,32 +71,41 @@ __device__ __forceinline__ void static_for(F&& f) {
   }
 }
 
-// LDS: four regions (weight codes 16 KB, token codes 16 KB), then the scale
-// ring [weights, tokens][8 steps][256 rows][4], then a 256-byte bias slot per
-// wave.
-constexpr int R_X = 16384;
-constexpr int REGION = 32768;
-constexpr int SR = 4 * REGION;
+// A tile's shape and its step's schedule. LDS: RING regions (weight codes, then
+// token codes), the scale ring [weights, tokens][8 steps][1 KB], a 256-byte bias
+// slot per wave. The smaller tiles' steps are shorter and need more of them in
+// flight to cover the latency of memory; RING is even, since scales are fetched
+// for two steps at a time, and RING + 2 scale slots are in use.
 constexpr int SR_SLOT = 1024;
 constexpr int SR_OP = 8 * SR_SLOT;
-constexpr int BIAS_TABLE = SR + 2 * SR_OP;
-constexpr int LDS_BYTES = BIAS_TABLE + 4 * 256;
 
-template <int JB, bool X8>
+template <int IA, int JB, bool X8>
 struct Shape {
-  static_assert(!X8 || JB == 2, "MXFP8 tokens fill a region with 128 rows");
-  static constexpr int MT = 64 * JB;             // tokens per tile
-  static constexpr int XB = X8 ? 2 * JB : JB;    // 1 KB token blocks per wave and step
-  static constexpr int CL = 4 + XB;              // code DMAs per wave and step
-  static constexpr int NM = 8 * JB;              // MFMAs per wave and step
-  static constexpr int NB = X8 ? 4 * JB : 2 * JB;  // 16-byte token reads per wave and step
-  static constexpr int NC = 8 + NB;              // and with the weights'
-  static constexpr int NR = NC + 4 + JB;         // and the scale pairs
-  static constexpr int PRE = X8 ? 3 : JB == 4 ? 6 : 4;    // MFMAs issued ahead of the step's barrier
-  static constexpr int SETUP = X8 ? 11 : 6;               // set-up instructions behind each of them
-  static constexpr int RS = X8 ? 10 : JB == 4 ? 20 : 8;   // MFMAs after it that carry reads
-  static constexpr int DS = X8 ? 9 : JB == 4 ? 18 : 10;   // and loads
-  static constexpr int ND = CL + 1;              // loads: the scale DMA, then the codes
+  static_assert(!X8 || JB == 2, "MXFP8 tokens come in tiles of 128");
+  static constexpr int BN = 64 * IA;                      // weight rows per tile
+  static constexpr int MT = 64 * JB;                      // tokens per tile
+  static constexpr int XB = X8 ? 2 * JB : JB;             // 1 KB token blocks per wave and step
+  static constexpr int CL = IA + XB;                      // code DMAs per wave and step
+  static constexpr int R_X = IA * 4096;                   // token codes within a region
+  static constexpr int REGION = CL * 4096;
+  static constexpr int RING = CL <= 5 ? 6 : 4;
+  static constexpr int SR = RING * REGION;
+  static constexpr int BIAS = SR + 2 * SR_OP;
+  static constexpr int STAGE = 32 * JB * 256;             // epilogue staging per wave
+  static constexpr int LDS = BIAS + 4 * 256 > 4 * STAGE ? BIAS + 4 * 256 : 4 * STAGE;
+  static constexpr int NM = 2 * IA * JB;                  // MFMAs per wave and step
+  static constexpr int NBH = X8 ? 2 * JB : JB;            // 16-byte token reads per MFMA set
+  static constexpr int H = IA + NBH;                      // and with the weights'
+  static constexpr int NC = 2 * H;                        // 16-byte reads per wave and step
+  static constexpr int NR = NC + IA + JB;                 // and the scale pairs
+  // MFMAs issued ahead of the step's barrier, about 190 cycles of them, and
+  // set-up instructions behind each.
+  static constexpr int PRE = X8 ? 3 : JB == 4 ? 8 : NM == 8 ? 3 : 4;
+  static constexpr int SETUP = X8 ? 11 : 6;
+  static constexpr int RS = (NM - PRE) * 10 / 13;         // MFMAs after it that carry reads
+  static constexpr int DS = X8 ? (NM - PRE) * 9 / 13 : (NM - PRE) * 18 / 26 + 1;  // and loads
+  static constexpr int ND = CL + 1;                       // loads: the scale DMA, then the codes
+  static_assert(LDS <= 163840 && RING % 2 == 0 && RING + 2 <= 8 && RS > 0 && DS > 0, "shape");
 };
 
 struct Src {
@@ -107,7 +115,8 @@ struct Src {
   const uint8_t* xs;
   uint64_t w_slab, x_slab;  // bytes between code slabs
   int nsteps, x_slabs;
-  int xoff;  // lane part of a token DMA's offset
+  int xoff;          // lane part of a token DMA's offset
+  uint32_t w_bytes;  // codes of a slab that belong to the tile (a last tile may reach past the operand)
 };
 
 struct LoadRes {
@@ -117,49 +126,50 @@ struct LoadRes {
 
 // Steps past the last (and the slab past K of MXFP8 tokens) load zeros from an
 // empty resource. MXFP8: waves 0, 1 move the step's first token slab, waves 2, 3
-// its second.
-template <int JB, bool X8>
-__device__ __forceinline__ LoadRes load_res(const Src& S, uint8_t* smem, int j, int wave) {
+// its second. rg: the step's ring region.
+template <class Sh, bool X8>
+__device__ __forceinline__ LoadRes load_res(const Src& S, uint8_t* smem, int j, int rg, int wave) {
   LoadRes L;
-  L.reg = smem + (j & 3) * REGION;
-  L.w = make_rsrc(S.w + (uint64_t)j * S.w_slab, j < S.nsteps ? 16384u : 0u);
+  L.reg = smem + rg * Sh::REGION;
+  L.w = make_rsrc(S.w + (uint64_t)j * S.w_slab, j < S.nsteps ? S.w_bytes : 0u);
   if constexpr (X8) {
     const int sl = 2 * j + (wave >> 1);
     L.x = make_rsrc(S.x + (uint64_t)sl * S.x_slab, sl < S.x_slabs ? 8192u : 0u);
   } else {
-    L.x = make_rsrc(S.x + (uint64_t)j * S.x_slab, j < S.nsteps ? 4096u * JB : 0u);
+    L.x = make_rsrc(S.x + (uint64_t)j * S.x_slab, j < S.nsteps ? 64u * Sh::MT : 0u);
   }
   return L;
 }
 
-// Code piece D of a step: one 1 KB block (16 rows), weights and tokens in turn.
-template <int D, int JB, bool X8>
+// Code piece D of a step: one 1 KB block (16 rows), weights and tokens in turn
+// while there are both.
+template <int D, int IA, class Sh, bool X8>
 __device__ __forceinline__ void load_piece(const LoadRes& L, const Src& S, int wave, int lane) {
-  constexpr int XB = Shape<JB, X8>::XB;
-  constexpr bool W = (D & 1) == 0 || D >= 2 * XB;
-  constexpr int u = D < 2 * XB ? D / 2 : D - XB;
-  const int q = wave * (W ? 4 : XB) + u;
+  constexpr int XB = Sh::XB, both = IA < XB ? IA : XB;
+  constexpr bool W = D < 2 * both ? D % 2 == 0 : IA > XB;
+  constexpr int u = D < 2 * both ? D / 2 : D - both;
+  const int q = wave * (W ? IA : XB) + u;
   const int from = (W || !X8 ? q : q & 7) * 1024;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(W ? L.w : L.x, (lds_ptr)(L.reg + (W ? 0 : R_X) + q * 1024), 16,
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(W ? L.w : L.x, (lds_ptr)(L.reg + (W ? 0 : Sh::R_X) + q * 1024), 16,
                                            W ? lane * 16 : S.xoff, from, 0, 0);
 }
 
-// Scales of steps s and s + 1 (s even): 1 KB each for the weights (waves 0, 1)
-// and the tokens (waves 2, 3). Where a step's token scales are 512 bytes
-// (128-token tiles) lanes 32 .. 63 fetch them again, into the slot's unused half;
-// MXFP8: 256 bytes of each slab (lanes 16 .. 31 the second's).
+// Scales of steps s and s + 1 (s even): weights by waves 0, 1, tokens by waves
+// 2, 3, each a 1 KB slot (lanes past the tile's rows read zeros). MXFP8: 256
+// bytes of each slab (lanes 16 .. 31 the second's; 32 .. 63 the same again).
 struct ScaleLoad {
   __amdgpu_buffer_rsrc_t r;
   uint8_t* dst;
   uint32_t voff;
 };
 
-template <int JB, bool X8>
+template <class Sh, bool X8>
 __device__ __forceinline__ ScaleLoad scale_res(const Src& S, uint8_t* smem, int s, int wave, int lane) {
   const bool w = wave < 2;
   const int st = s + (wave & 1);
   ScaleLoad L;
-  L.dst = smem + SR + (w ? 0 : SR_OP) + (st & 7) * SR_SLOT;
+  L.dst = smem + Sh::SR + (w ? 0 : SR_OP) + (st & 7) * SR_SLOT;
+  L.voff = lane * 16;
   if (X8 && !w) {
     const uint32_t slab = (uint32_t)(S.x_slab >> 5);
     const uint32_t n = 2 * st + 1 < S.x_slabs ? slab + 256u : 2 * st < S.x_slabs ? 256u : 0u;
@@ -167,8 +177,7 @@ __device__ __forceinline__ ScaleLoad scale_res(const Src& S, uint8_t* smem, int 
     L.voff = (lane & 15) * 16 + ((lane >> 4) & 1) * slab;
   } else {
     const uint64_t slab = (w ? S.w_slab : S.x_slab) >> 4;
-    L.r = make_rsrc((w ? S.ws : S.xs) + (uint64_t)st * slab, st < S.nsteps ? (w ? 1024u : 256u * JB) : 0u);
-    L.voff = (JB == 4 || w ? lane : (lane & 31)) * 16;
+    L.r = make_rsrc((w ? S.ws : S.xs) + (uint64_t)st * slab, st < S.nsteps ? (w ? S.w_bytes >> 4 : 4u * Sh::MT) : 0u);
   }
   return L;
 }
@@ -177,38 +186,40 @@ __device__ __forceinline__ void issue_scales(const ScaleLoad& L) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(L.r, (lds_ptr)L.dst, 16, L.voff, 0, 0, 0);
 }
 
-template <int JB, bool X8>
+template <int IA, int JB, bool X8>
 struct Frags {
-  i32x4 a[4][2];               // [fragment][MFMA of the step]
+  i32x4 a[IA][2];              // [fragment][MFMA of the step]
   i32x4 b[JB][2][X8 ? 2 : 1];  // and, of an E4M3 operand, its two halves
-  int sa[4], sb[JB];           // byte s: the scale for MFMA s
+  int sa[IA], sb[JB];          // byte s: the scale for MFMA s
 };
 
 struct FragAddr {
   const uint8_t* a;
-  const uint8_t* b;  // E4M3: of MFMA 0
+  const uint8_t* b;   // E4M3: of MFMA 0
   const uint8_t* b1;  // E4M3: of MFMA 1
   const uint8_t* sa;
   const uint8_t* sb;
 };
 
-template <int JB, bool X8>
-__device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int wn, int wm, int lane) {
+// Fragments of step j, in ring region rg.
+template <int IA, int JB, bool X8>
+__device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int rg, int wn, int wm, int lane) {
+  using Sh = Shape<IA, JB, X8>;
   const int r32 = lane & 31, hi = lane >> 5;
-  const uint8_t* reg = smem + (j & 3) * REGION;
-  const uint8_t* sc = smem + SR + (j & 7) * SR_SLOT;
+  const uint8_t* reg = smem + rg * Sh::REGION;
+  const uint8_t* sc = smem + Sh::SR + (j & 7) * SR_SLOT;
   const int off = (r32 >> 4) * 1024 + (r32 & 15) * 16 + 512 * hi;
   FragAddr A;
-  A.a = reg + wn * 8192 + off;
-  A.sa = sc + (wn * 128 + r32) * 4 + 2 * hi;
+  A.a = reg + wn * (2048 * IA) + off;
+  A.sa = sc + (wn * 32 * IA + r32) * 4 + 2 * hi;
   if constexpr (X8) {
-    const uint8_t* row = reg + R_X + (wm * 32 * JB + r32) * 64;
+    const uint8_t* row = reg + Sh::R_X + (wm * 32 * JB + r32) * 64;
     const int sw = (r32 >> 2) & 3;
     A.b = row + ((hi ^ sw) << 4);
     A.b1 = row + (((2 + hi) ^ sw) << 4);
     A.sb = sc + SR_OP + hi * 256 + (wm * 32 * JB + r32) * 2;
   } else {
-    A.b = reg + R_X + wm * (2048 * JB) + off;
+    A.b = reg + Sh::R_X + wm * (2048 * JB) + off;
     A.b1 = A.b;
     A.sb = sc + SR_OP + (wm * 32 * JB + r32) * 4 + 2 * hi;
   }
@@ -216,15 +227,16 @@ __device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int wn
 }
 
 // Read piece r: the fragments' 16-byte parts in the order the MFMAs take
-// them (all of MFMA 0, then all of MFMA 1; within one, the first parts of A
-// and B in turn, then the rest of A), then the scales.
-template <int R, int JB, bool X8>
-__device__ __forceinline__ void read_piece(Frags<JB, X8>& F, const FragAddr& A) {
-  constexpr int NC = Shape<JB, X8>::NC, H = NC / 2, NBH = H - 4;
+// them (all of MFMA 0, then all of MFMA 1; within one, parts of A and B in
+// turn while there are both), then the scales.
+template <int R, int IA, int JB, bool X8>
+__device__ __forceinline__ void read_piece(Frags<IA, JB, X8>& F, const FragAddr& A) {
+  using Sh = Shape<IA, JB, X8>;
+  constexpr int NC = Sh::NC, H = Sh::H, NBH = Sh::NBH;
   if constexpr (R < NC) {
     constexpr int s = R / H, r = R % H;
-    constexpr int both = NBH < 4 ? NBH : 4;
-    constexpr bool isA = r < 2 * both ? r % 2 == 0 : NBH < 4;
+    constexpr int both = NBH < IA ? NBH : IA;
+    constexpr bool isA = r < 2 * both ? r % 2 == 0 : IA > NBH;
     constexpr int f = r < 2 * both ? r / 2 : r - both;
     if constexpr (isA) {
       F.a[f][s] = *(const i32x4*)(A.a + f * 2048 + s * 256);
@@ -234,17 +246,17 @@ __device__ __forceinline__ void read_piece(Frags<JB, X8>& F, const FragAddr& A) 
     } else {
       F.b[f][s][0] = *(const i32x4*)(A.b + f * 2048 + s * 256);
     }
-  } else if constexpr (R < NC + 4) {
+  } else if constexpr (R < NC + IA) {
     F.sa[R - NC] = *(const uint16_t*)(A.sa + 32 * 4 * (R - NC));
   } else {
-    F.sb[R - NC - 4] = *(const uint16_t*)(A.sb + 32 * (X8 ? 2 : 4) * (R - NC - 4));
+    F.sb[R - NC - IA] = *(const uint16_t*)(A.sb + 32 * (X8 ? 2 : 4) * (R - NC - IA));
   }
 }
 
-template <int JB, bool X8, int B, int E>
-__device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB, X8>& F) {
+template <int B, int E, int IA, int JB, bool X8>
+__device__ __forceinline__ void mma(f32x16 (&acc)[IA][JB], const Frags<IA, JB, X8>& F) {
   static_for<B, E>([&](auto T) {
-    constexpr int s = decltype(T)::value / (4 * JB), u = decltype(T)::value % (4 * JB), i = u / JB, j = u % JB;
+    constexpr int s = decltype(T)::value / (IA * JB), u = decltype(T)::value % (IA * JB), i = u / JB, j = u % JB;
     const i32x8 a = {F.a[i][s][0], F.a[i][s][1], F.a[i][s][2], F.a[i][s][3], 0, 0, 0, 0};
     if constexpr (X8) {
       const i32x4 &b0 = F.b[j][s][0], &b1 = F.b[j][s][1];
@@ -258,53 +270,59 @@ __device__ __forceinline__ void mma(f32x16 (&acc)[4][JB], const Frags<JB, X8>& F
   });
 }
 
-// Step j: the first MFMAs, which read registers only, cover the wait for this
-// wave's loads of step j + 1, the barrier and the address set-up; the rest run
-// with the LDS reads of step j + 1 and the loads of step j + 4 between them.
-// EVEN: j is even, and the scales of steps j + 4 and j + 5 are fetched too.
-template <bool EVEN, int JB, bool X8>
-__device__ __forceinline__ void step(f32x16 (&acc)[4][JB], Frags<JB, X8>& cur, Frags<JB, X8>& nxt, const Src& S,
-                                     uint8_t* smem, int j, int wave, int wn, int wm, int lane) {
-  using Sh = Shape<JB, X8>;
+// Reads [r0, r1) and loads [d0, d1) issued with the i-th MFMA after the barrier.
+template <class Sh, int I>
+struct Slot {
+  static constexpr int r0 = I < Sh::RS ? Sh::NR * I / Sh::RS : Sh::NR, r1 = I < Sh::RS ? Sh::NR * (I + 1) / Sh::RS : Sh::NR;
+  static constexpr int d0 = I < Sh::DS ? Sh::ND * I / Sh::DS : Sh::ND, d1 = I < Sh::DS ? Sh::ND * (I + 1) / Sh::DS : Sh::ND;
+};
+
+// Step j, in ring region rg: the first MFMAs, which read registers only, cover
+// the wait for this wave's loads of step j + 1, the barrier and the address
+// set-up; the rest run with the LDS reads of step j + 1 and the loads of step j
+// + RING (into region rg) between them. EVEN: j is even, and the scales of steps
+// j + RING and j + RING + 1 are fetched too.
+template <bool EVEN, int IA, int JB, bool X8>
+__device__ __forceinline__ void step(f32x16 (&acc)[IA][JB], Frags<IA, JB, X8>& cur, Frags<IA, JB, X8>& nxt,
+                                     const Src& S, uint8_t* smem, int j, int rg, int wave, int wn, int wm, int lane) {
+  using Sh = Shape<IA, JB, X8>;
   constexpr int NM = Sh::NM, PRE = Sh::PRE;
   __builtin_amdgcn_sched_barrier(0);
-  const FragAddr A = frag_addr<JB, X8>(smem, j + 1, wn, wm, lane);
-  const LoadRes L = load_res<JB, X8>(S, smem, j + 4, wave);
+  const FragAddr A = frag_addr<IA, JB, X8>(smem, j + 1, rg + 1 == Sh::RING ? 0 : rg + 1, wn, wm, lane);
+  const LoadRes L = load_res<Sh, X8>(S, smem, j + Sh::RING, rg, wave);
   ScaleLoad SL;
-  if constexpr (EVEN) SL = scale_res<JB, X8>(S, smem, j + 4, wave, lane);
-  mma<JB, X8, 0, PRE>(acc, cur);
+  if constexpr (EVEN) SL = scale_res<Sh, X8>(S, smem, j + Sh::RING, wave, lane);
+  mma<0, PRE>(acc, cur);
   static_for<0, PRE>([&](auto) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
     __builtin_amdgcn_sched_group_barrier(0x006, Sh::SETUP, 0);  // set-up VALU / SALU
   });
   __builtin_amdgcn_sched_barrier(0);
   // The lgkmcnt(0) keeps a wave's refill from overtaking another wave's last
-  // reads of the region. Younger loads: those of the two steps after j + 1.
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * Sh::CL + 1) : "memory");
+  // reads of the region. Younger loads: those of the RING - 2 steps after j + 1,
+  // each with its codes, every other one with a scale DMA.
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((Sh::RING - 2) * Sh::CL + (Sh::RING - 2) / 2) : "memory");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   static_for<0, NM - PRE>([&](auto I) {
-    constexpr int i = decltype(I)::value;
-    constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
-    constexpr int d0 = i < Sh::DS ? Sh::ND * i / Sh::DS : Sh::ND, d1 = i < Sh::DS ? Sh::ND * (i + 1) / Sh::DS : Sh::ND;
-    static_for<r0, r1>([&](auto R) { read_piece<decltype(R)::value, JB, X8>(nxt, A); });
-    static_for<d0, d1>([&](auto D) {
+    using SL_ = Slot<Sh, decltype(I)::value>;
+    static_for<SL_::r0, SL_::r1>([&](auto R) { read_piece<decltype(R)::value>(nxt, A); });
+    static_for<SL_::d0, SL_::d1>([&](auto D) {
       constexpr int d = decltype(D)::value;
       if constexpr (d == 0) {
         if constexpr (EVEN) issue_scales(SL);
       } else {
-        load_piece<d - 1, JB, X8>(L, S, wave, lane);
+        load_piece<d - 1, IA, Sh, X8>(L, S, wave, lane);
       }
     });
   });
-  mma<JB, X8, PRE, NM>(acc, cur);
+  mma<PRE, NM>(acc, cur);
   static_for<0, NM - PRE>([&](auto I) {
-    constexpr int i = decltype(I)::value;
-    constexpr int r0 = i < Sh::RS ? Sh::NR * i / Sh::RS : Sh::NR, r1 = i < Sh::RS ? Sh::NR * (i + 1) / Sh::RS : Sh::NR;
-    constexpr int d0 = i < Sh::DS ? Sh::ND * i / Sh::DS : Sh::ND, d1 = i < Sh::DS ? Sh::ND * (i + 1) / Sh::DS : Sh::ND;
-    constexpr int nd = d1 - d0 - (!EVEN && d0 == 0 && d1 > 0 ? 1 : 0);
+    using SL_ = Slot<Sh, decltype(I)::value>;
+    constexpr int nr = SL_::r1 - SL_::r0;
+    constexpr int nd = SL_::d1 - SL_::d0 - (!EVEN && SL_::d0 == 0 && SL_::d1 > 0 ? 1 : 0);
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if constexpr (r1 > r0) __builtin_amdgcn_sched_group_barrier(0x100, r1 - r0, 0);
+    if constexpr (nr > 0) __builtin_amdgcn_sched_group_barrier(0x100, nr, 0);
     if constexpr (nd > 0) __builtin_amdgcn_sched_group_barrier(0x020, nd, 0);
   });
   __builtin_amdgcn_sched_barrier(0);
@@ -323,15 +341,15 @@ __device__ inline void tile_coords(uint32_t pid, int tiles_m, int tiles_n, int& 
   tn = in_group / gm;
 }
 
-// The wave's 128 (n) x 32 JB (m) outputs: bf16 through LDS ([m][n], rows of
+// The wave's 32 IA (n) x 32 JB (m) outputs: bf16 through LDS ([m][n], rows of
 // 256 bytes, 8-byte block nb of row m at nb ^ (m & 31): 32 lanes on 32 rows
-// write 32 bank pairs), then whole 256-byte row pieces, 16 bytes a lane.
-template <int EPI, int JB>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][JB], const GemmParams& p, uint8_t* ep, int m0,
+// write 32 bank pairs), then whole row pieces of 64 IA bytes, 16 bytes a lane.
+template <int EPI, int IA, int JB>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[IA][JB], const GemmParams& p, uint8_t* ep, int m0,
                                            int n0, int rows_m, int rows_n, int wn, int wm, int lane) {
   const int r32 = lane & 31, hi = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < IA; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int nb = 8 * i + 2 * q + hi;
@@ -351,12 +369,13 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][JB], const Gem
   // lane's write (LDS order within a wave is kept by the hardware).
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + (size_t)m0 * p.N, (uint32_t)(rows_m * p.N * 2));
-  const int c = lane & 15;
-  const int nl = wn * 128 + 8 * c;
-  const bool n_ok = nl < rows_n;
+  constexpr int LPR = IA == 2 ? 8 : 16;  // lanes per row
+  const int c = lane % LPR;
+  const int nl = wn * 32 * IA + 8 * c;
+  const bool n_ok = c < 4 * IA && nl < rows_n;
 #pragma unroll 8
-  for (int it = 0; it < 8 * JB; ++it) {
-    const int m = 4 * it + (lane >> 4);
+  for (int it = 0; it < 32 * JB * LPR / 64; ++it) {
+    const int m = 64 / LPR * it + lane / LPR;
     const int sw = m & 31;
     const i32x4 v = *(const i32x4*)(ep + m * 256 + ((((2 * c) ^ sw) & ~1) << 3));
     const i32x4 w = (sw & 1) ? i32x4{v[2], v[3], v[0], v[1]} : v;
@@ -365,15 +384,15 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][JB], const Gem
   }
 }
 
-template <int EPI, int JB, bool X8>
+template <int EPI, int IA, int JB, bool X8>
 __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  using Sh = Shape<JB, X8>;
+  using Sh = Shape<IA, JB, X8>;
   int tm, tn;
   tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-  const int m0 = tm * Sh::MT, n0 = tn * BN;
+  const int m0 = tm * Sh::MT, n0 = tn * Sh::BN;
   const int rows_m = min(p.M - m0, Sh::MT);
-  const int rows_n = min(p.N - n0, BN);
+  const int rows_n = min(p.N - n0, Sh::BN);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave & 1, wm = wave >> 1;
@@ -387,32 +406,34 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
   S.xs = p.xs + (size_t)m0 * (X8 ? 2 : 4);
   S.nsteps = p.nsteps;
   S.x_slabs = p.x_slabs;
+  // 192-row tiles need not end where the padded rows do.
+  S.w_bytes = (uint32_t)min(p.RN - n0, (int64_t)Sh::BN) * 64u;
   // MXFP8: lane L takes row L / 4 of a block, chunk (L % 4) ^ (L / 16), into slot L % 4.
   S.xoff = X8 ? (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4) : lane * 16;
 
-  // Bias: the 128 f16 values of the wave's weight rows into its slot, ahead of
-  // the ring's first loads (columns past N read what the load leaves there;
-  // their outputs are not stored).
-  uint8_t* slot = smem + BIAS_TABLE + wave * 256;
+  // Bias: the f16 values of the wave's weight rows into its slot, ahead of the
+  // ring's first loads (columns past N read what the load leaves there; their
+  // outputs are not stored).
+  uint8_t* slot = smem + Sh::BIAS + wave * 256;
   if (p.bias != nullptr) {
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.bias + n0, (uint32_t)rows_n * 2u);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 256, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 64 * IA, 0, 0);
   } else {
     *(int*)(slot + lane * 4) = 0;
   }
   // The ring's first loads in the order the loop would have issued them (its
-  // waits count on it): scales of steps 0, 1, codes 0, 1, scales 2, 3, codes 2, 3.
-  static_for<0, 4>([&](auto J) {
+  // waits count on it): the scales of two steps before the codes of the first.
+  static_for<0, Sh::RING>([&](auto J) {
     constexpr int j = decltype(J)::value;
-    if constexpr (j % 2 == 0) issue_scales(scale_res<JB, X8>(S, smem, j, wave, lane));
-    const LoadRes L = load_res<JB, X8>(S, smem, j, wave);
-    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, JB, X8>(L, S, wave, lane); });
+    if constexpr (j % 2 == 0) issue_scales(scale_res<Sh, X8>(S, smem, j, wave, lane));
+    const LoadRes L = load_res<Sh, X8>(S, smem, j, j, wave);
+    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, IA, Sh, X8>(L, S, wave, lane); });
   });
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 * Sh::CL + 2) : "memory");  // the bias
-  f32x16 acc[4][JB];
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(Sh::RING * Sh::CL + Sh::RING / 2) : "memory");  // the bias
+  f32x16 acc[IA][JB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < IA; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const i32x2 bq = *(const i32x2*)(slot + (32 * i + 8 * q + 4 * (lane >> 5)) * 2);
@@ -426,46 +447,85 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
     }
   // The accumulators are written here, inside the first loads' latency.
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < IA; ++i)
 #pragma unroll
     for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(3 * Sh::CL + 1) : "memory");  // step 0
+  // Step 0: RING - 1 steps' codes and RING / 2 - 1 scale DMAs are younger.
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((Sh::RING - 1) * Sh::CL + Sh::RING / 2 - 1) : "memory");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  Frags<JB, X8> F0, F1;
-  const FragAddr A0 = frag_addr<JB, X8>(smem, 0, wn, wm, lane);
-  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value, JB, X8>(F0, A0); });
-  int j = 0;
+  Frags<IA, JB, X8> F0, F1;
+  const FragAddr A0 = frag_addr<IA, JB, X8>(smem, 0, 0, wn, wm, lane);
+  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value>(F0, A0); });
+  int j = 0, rg = 0;
   for (; j + 1 < p.nsteps; j += 2) {
-    step<true, JB, X8>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
-    step<false, JB, X8>(acc, F1, F0, S, smem, j + 1, wave, wn, wm, lane);
+    step<true>(acc, F0, F1, S, smem, j, rg, wave, wn, wm, lane);
+    step<false>(acc, F1, F0, S, smem, j + 1, rg + 1, wave, wn, wm, lane);
+    rg = rg + 2 == Sh::RING ? 0 : rg + 2;
   }
-  if (j < p.nsteps) step<true, JB, X8>(acc, F0, F1, S, smem, j, wave, wn, wm, lane);
+  if (j < p.nsteps) step<true>(acc, F0, F1, S, smem, j, rg, wave, wn, wm, lane);
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
-  store_tile<EPI, JB>(acc, p, smem + wave * 32768, m0, n0, rows_m, rows_n, wn, wm, lane);
+  store_tile<EPI>(acc, p, smem + wave * Sh::STAGE, m0, n0, rows_m, rows_n, wn, wm, lane);
 }
 
-template <int EPI, int JB, bool X8>
-hipError_t launch(const GemmParams& p, hipStream_t st) {
+template <int EPI, int IA, int JB, bool X8>
+hipError_t launch(GemmParams p, hipStream_t st) {
+  using Sh = Shape<IA, JB, X8>;
   static bool configured = false;  // per instantiation; benign race (idempotent)
-  auto kern = fp4_gemm_kernel<EPI, JB, X8>;
+  auto kern = fp4_gemm_kernel<EPI, IA, JB, X8>;
   if (!configured) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
     if (e != hipSuccess) return e;
     configured = true;
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(NT), LDS_BYTES, st, p);
+  p.tiles_m = (p.M + Sh::MT - 1) / Sh::MT;
+  p.tiles_n = (p.N + Sh::BN - 1) / Sh::BN;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(NT), Sh::LDS, st, p);
   return hipGetLastError();
+}
+
+template <int IA, int JB, bool X8>
+hipError_t launch(const GemmParams& p, int epi, hipStream_t st) {
+  return epi == 1 ? launch<1, IA, JB, X8>(p, st) : launch<0, IA, JB, X8>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_fp4_linear_tiles(int fp8, int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
-                                   const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
-                                   hipStream_t stream) {
+// The tile shape for an output: the one whose rounds of 256 workgroups (one a
+// CU) take the least time, from the measured time of a round at K = 5120 (us;
+// longer or shorter K scale all shapes about alike). Checked over 256 to 16384
+// tokens and 4096 to 15360 outputs, e.g. (us, chosen first): 512 x 5120 128 x 128
+// 13.3, 192 x 128 14.6, 256 x 128 16.7, 256 x 256 25.4; 1024 x 5120 192 x 128
+// 18.5, 256 x 128 19.3, 128 x 128 25.8, 256 x 256 26.5; 4001 x 5120 256 x 128
+// 63.0, 256 x 256 65.8; 3000 x 15360 256 x 256 115, 256 x 128 129. The small
+// tiles are bound by the CU's load path (about 35 bytes a cycle), the large ones
+// by the matrix cores.
+void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile) {
+  struct Tile {
+    int weights, tokens;
+    double us;
+  };
+  static const Tile fp4_tiles[] = {{256, 256, 32.0}, {256, 128, 19.5}, {192, 128, 17.5}, {128, 128, 12.8}};
+  static const Tile fp8_tiles[] = {{256, 128, 28.0}, {192, 128, 24.6}, {128, 128, 17.1}};
+  const Tile* t = fp8 ? fp8_tiles : fp4_tiles;
+  double best = -1.0;
+  for (int i = 0; i < (fp8 ? 3 : 4); ++i) {
+    const int64_t tiles = (M + t[i].tokens - 1) / t[i].tokens * ((N + t[i].weights - 1) / t[i].weights);
+    const double us = (double)((tiles + 255) / 256) * t[i].us;
+    if (best < 0.0 || us < best) {
+      best = us;
+      *weight_tile = t[i].weights;
+      *token_tile = t[i].tokens;
+    }
+  }
+}
+
+hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs,
+                                   int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
+                                   const void* bias, int epi, void* y, hipStream_t stream) {
   GemmParams p;
   p.x = xq;
   p.xs = xs;
@@ -479,11 +539,16 @@ hipError_t launch_fp4_linear_tiles(int fp8, int token_tile, const uint8_t* xq, c
   p.N = (int)N;
   p.nsteps = (int)fp4_slabs(K);
   p.x_slabs = (int)(K / 64);
-  p.tiles_m = (int)((M + token_tile - 1) / token_tile);
-  p.tiles_n = (int)((N + BN - 1) / BN);
-  if (fp8) return epi == 1 ? launch<1, 2, true>(p, stream) : launch<0, 2, true>(p, stream);
-  if (token_tile == 128) return epi == 1 ? launch<1, 2, false>(p, stream) : launch<0, 2, false>(p, stream);
-  return epi == 1 ? launch<1, 4, false>(p, stream) : launch<0, 4, false>(p, stream);
+  p.tiles_m = p.tiles_n = 0;
+  if (fp8) {
+    if (weight_tile == 128) return launch<2, 2, true>(p, epi, stream);
+    if (weight_tile == 192) return launch<3, 2, true>(p, epi, stream);
+    return launch<4, 2, true>(p, epi, stream);
+  }
+  if (token_tile == 256) return launch<4, 4, false>(p, epi, stream);
+  if (weight_tile == 128) return launch<2, 2, false>(p, epi, stream);
+  if (weight_tile == 192) return launch<3, 2, false>(p, epi, stream);
+  return launch<4, 2, false>(p, epi, stream);
 }
 
 }  // namespace mx

@@ -41,9 +41,11 @@ CASES = [
     (300, 352, 2064), (513, 544, 528), (1025, 192, 784),
     # every tile shape of the few-token kernel, and long rows of a few tokens
     (16, 6208, 5136), (3, 8256, 4112), (32, 128, 5136), (30, 320, 16400), (64, 160, 4112), (63, 96, 12304),
-    (130, 96, 8208), (250, 224, 8208), (16, 32, 20496), (10, 13824, 48), (1, 8320, 5136),
-    # 128-token and 256-token tiles: one step, an odd and an even number, ragged
-    (700, 96, 4112), (1000, 256, 2576), (129, 416, 16656), (2100, 416, 4368), (4000, 1184, 2320), (4111, 64, 2576),
+    (130, 96, 6160), (250, 12352, 4368), (16, 32, 20496), (10, 13824, 48), (1, 8320, 5136),
+    # every shape of the tiled kernel: one step, an odd and an even number,
+    # more and fewer than the ring; ragged rows, columns and K
+    (260, 96, 4112), (700, 1184, 2320), (513, 544, 8208), (1000, 416, 5136), (520, 64, 10224), (1500, 288, 4112),
+    (2100, 416, 5136), (4111, 64, 2576), (4000, 1184, 4368), (3100, 320, 8240),
 ]
 
 
