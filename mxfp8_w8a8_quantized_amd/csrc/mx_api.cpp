@@ -953,14 +953,17 @@ uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
 }
 
 // The few-token kernel up to 4096 fragments of 16 x 16 outputs (16 in each of
-// 256 workgroups), up to 8192 where K is long; the tiled GEMMs above. Their
-// loops run alike; the few-token kernel has the costlier end (the waves' sums),
-// the tiles fewer workgroups: 128 x 5120 x 5120 8.9 us against 12.5 (MXFP8
-// activations 12.7 against 16.0), 256 x 5120 x 5120 14.2 against 12.6 (19.2
-// against 16.4), 256 x 13824 x 5120 24.5 against 28 (36 against 38).
+// 256 workgroups), and up to 8192 (32 each) where K is long; the tiled GEMMs
+// above. Their loops are bound alike by the CUs' load paths; 32 fragments a
+// workgroup make the few-token kernel's end (the waves' sums through LDS)
+// costlier by 2 us. 256 x 5120 x 4096: 8.2 us against 12.5 on tiles (MXFP8
+// activations 10.5 against 16.3); 256 x 5120 x 8192 12.2 against 13.0 (15.0
+// against 16.5), 256 x 3584 x 8192 10.5 against 10.4, 256 x 1024 x 8192 7.1
+// against 5.6.
+constexpr int64_t kFp4FewLongK = 4096;
 bool fp4_few(int64_t M, int64_t K, int64_t N) {
   const int64_t fragments = ((M + 15) / 16) * (N / 16);
-  return fragments <= 4096 || (fragments <= 8192 && K > 12288);
+  return fragments <= 4096 || (fragments <= 8192 && K > kFp4FewLongK);
 }
 
 // bf16 rows are quantized inside the product's kernel, by every workgroup for

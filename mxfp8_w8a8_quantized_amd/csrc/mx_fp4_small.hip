@@ -17,9 +17,11 @@
 // slab is one 1 KB run in lane order, so operands go from memory straight to
 // registers; nothing is shared between the waves but the final sums.
 //
-// Measured (one pass on operands not in the L2): 5120 x 5120 weights, 16
-// tokens 5.0 us (2.8 TB/s of weights, 4.9 us for one token; launch and the
-// first round trip are about half of it), 15360 x 5120 8.5 us (4.9 TB/s).
+// Measured (operands not in the L2): 5120 x 5120 weights, 16 tokens 5.0 us (2.8
+// TB/s of weights; launch and the first round trip are about half of it), 15360
+// x 5120 8.5 us (4.9 TB/s).
+#include <type_traits>
+
 #include "mx_fp4_device.h"
 #include "mx_internal.h"
 
@@ -69,14 +71,39 @@ __device__ __forceinline__ uint32_t amax16(i32x4 a, i32x4 b) {
   return bf16_amax_bits(w);
 }
 
-// The operands of one 128-K slab as loaded.
+// The operands of one 128-K slab as loaded. Scales come as one dword per row
+// (its four groups) or, from an MXFP8 slab, two bytes per row and 64-K slab, for
+// up to 64 rows in one load; see the transpositions below.
 template <int SRC, int WB, int TB>
 struct Step {
   static constexpr int NX = SRC == SRC_FP4 ? 1 : SRC == SRC_FP8 ? 2 : 4;  // 16-byte loads per token fragment
+  static constexpr int NSA = (WB + 3) / 4;
+  static constexpr int NSB = SRC == SRC_FP4 ? (TB + 3) / 4 : SRC == SRC_FP8 ? (TB + 1) / 2 : 1;
   i32x4 a[WB];
   i32x4 b[TB][NX];
-  int sa[WB], sb[TB];
+  int sa[NSA], sb[NSB];
 };
+
+// Lane 16 i + r holds the scales of row 16 i + r, group g in byte g; returns,
+// in lane 16 g + r, the scale of group g of row 16 i + r in byte i: what the
+// MFMA wants of that lane for fragment i, which op_sel picks. A 4 x 4
+// transposition of bytes over the four lane rows: halves are exchanged 32 lanes
+// apart, then bytes 16 lanes apart. Two swaps and two permutations replace four
+// byte loads, which cost the load path as much as the codes' loads do.
+__device__ __forceinline__ int transpose_scales(int x, int lane) {
+  const auto h = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
+  const uint32_t y = __builtin_amdgcn_perm(h[1], h[0], lane < 32 ? 0x05040100u : 0x07060302u);
+  const auto q = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+  return (int)__builtin_amdgcn_perm(q[1], q[0], (lane & 16) ? 0x07030501u : 0x06020400u);
+}
+
+// The same for an MXFP8 slab pair: lane 32 h + 16 f + r holds the two scales of
+// row 16 f + r in slab h; returns, in lane 16 g + r, the scale of group g = 2 h
+// + byte of row 16 f + r in byte f.
+__device__ __forceinline__ int transpose_scales_fp8(int x, int lane) {
+  const auto q = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+  return (int)__builtin_amdgcn_perm(q[1], q[0], (lane & 16) ? 0x0C0C0501u : 0x0C0C0400u);
+}
 
 // Loads slab `sl`. Past the wave's range (sl >= s1) nothing is read: the
 // buffer resources are empty and every value becomes zero, so the loop's loads
@@ -89,36 +116,37 @@ __device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams&
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.wq + ((int64_t)sl * (p.RN / 16) + n0 / 16) * 1024, on ? WB * 1024 : 0);
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.ws + ((int64_t)sl * p.RN + n0) * 4, on ? WB * 64 : 0);
 #pragma unroll
-  for (int i = 0; i < WB; ++i) {
-    s.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, lane * 16 + i * 1024, 0, 0);
-    s.sa[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, r * 4 + G + i * 64, 0, 0);
-  }
+  for (int i = 0; i < WB; ++i) s.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, lane * 16 + i * 1024, 0, 0);
+#pragma unroll
+  for (int i = 0; i < Step<SRC, WB, TB>::NSA; ++i)
+    s.sa[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, lane * 4 + i * 256, 0, 0);
   if constexpr (SRC == SRC_FP4) {
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + ((int64_t)sl * (p.RM / 16) + m0 / 16) * 1024, on ? TB * 1024 : 0);
     const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.xs + ((int64_t)sl * p.RM + m0) * 4, on ? TB * 64 : 0);
 #pragma unroll
-    for (int j = 0; j < TB; ++j) {
-      s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, lane * 16 + j * 1024, 0, 0);
-      s.sb[j] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt, r * 4 + G + j * 64, 0, 0);
-    }
+    for (int j = 0; j < TB; ++j) s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, lane * 16 + j * 1024, 0, 0);
+#pragma unroll
+    for (int j = 0; j < Step<SRC, WB, TB>::NSB; ++j)
+      s.sb[j] = (int)__builtin_amdgcn_raw_buffer_load_b32(rt, lane * 4 + j * 256, 0, 0);
   } else if constexpr (SRC == SRC_FP8) {
     // Two 64-K slabs of 64-byte rows; the second is past K where K % 128 = 64.
-    // The lane's scale is that of K group G: slab G / 2, byte G % 2.
+    // Scales: lanes 0 .. 31 the first slab's, 32 .. 63 the second's, two bytes
+    // for each of 32 rows.
     const bool two = on && sl * 128 + 64 < p.K;
     const uint8_t* x0 = p.x + (2 * (int64_t)sl * p.RM + m0) * 64;
     const uint8_t* t0 = p.xs + (2 * (int64_t)sl * p.RM + m0) * 2;
+    const uint32_t next = (uint32_t)p.RM * 2;  // bytes to the next slab's scales
     const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(x0, on ? TB * 1024 : 0);
     const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(x0 + p.RM * 64, two ? TB * 1024 : 0);
-    const __amdgpu_buffer_rsrc_t rt0 = make_rsrc(t0, on ? TB * 32 : 0);
-    const __amdgpu_buffer_rsrc_t rt1 = make_rsrc(t0 + p.RM * 2, two ? TB * 32 : 0);
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(t0, two ? next + TB * 32 : on ? TB * 32 : 0);
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
       s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb0, r * 64 + 16 * G + j * 1024, 0, 0);
       s.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rb1, r * 64 + 16 * G + j * 1024, 0, 0);
-      const int c0 = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt0, r * 2 + (G & 1) + j * 32, 0, 0);
-      const int c1 = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rt1, r * 2 + (G & 1) + j * 32, 0, 0);
-      s.sb[j] = G < 2 ? c0 : c1;
     }
+#pragma unroll
+    for (int j = 0; j < Step<SRC, WB, TB>::NSB; ++j)
+      s.sb[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rt, (lane & 31) * 2 + j * 64 + (lane >> 5) * next, 0, 0);
   } else {
     // Rows past M repeat the last one; their outputs are not stored.
     const int kend = on ? p.K : 0;
@@ -135,20 +163,41 @@ __device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams&
   }
 }
 
+template <int B, int E, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
 template <int SRC, int WB, int TB>
 __device__ __forceinline__ void mma_step(f32x4 (&acc)[WB][TB], const Step<SRC, WB, TB>& s, int lane) {
+  using St = Step<SRC, WB, TB>;
   constexpr int FB = SRC == SRC_FP4 || SRC == SRC_BF16_FP4 ? 4 : 0;  // token format: E2M1 or E4M3
+  int sa[St::NSA], sbt[St::NSB];
 #pragma unroll
-  for (int j = 0; j < TB; ++j) {
+  for (int i = 0; i < St::NSA; ++i) sa[i] = transpose_scales(s.sa[i], lane);
+  if constexpr (SRC == SRC_FP4) {
+#pragma unroll
+    for (int j = 0; j < St::NSB; ++j) sbt[j] = transpose_scales(s.sb[j], lane);
+  } else if constexpr (SRC == SRC_FP8) {
+#pragma unroll
+    for (int j = 0; j < St::NSB; ++j) sbt[j] = transpose_scales_fp8(s.sb[j], lane);
+  }
+  static_for<0, TB>([&](auto J) {
+    constexpr int j = decltype(J)::value;
+    constexpr int PER = SRC == SRC_FP4 ? 4 : 2;                   // token fragments per scale register
+    constexpr int opb = SRC == SRC_FP4 || SRC == SRC_FP8 ? j % PER : 0;
     i32x8 b = {0, 0, 0, 0, 0, 0, 0, 0};
     int sb;
     if constexpr (SRC == SRC_FP4) {
       b = i32x8{s.b[j][0][0], s.b[j][0][1], s.b[j][0][2], s.b[j][0][3], 0, 0, 0, 0};
-      sb = s.sb[j];
+      sb = sbt[j / PER];
     } else if constexpr (SRC == SRC_FP8) {
       b = i32x8{s.b[j][0][0], s.b[j][0][1], s.b[j][0][2], s.b[j][0][3],
                 s.b[j][1][0], s.b[j][1][1], s.b[j][1][2], s.b[j][1][3]};
-      sb = s.sb[j];
+      sb = sbt[j / PER];
     } else if constexpr (SRC == SRC_BF16_FP4) {
       const uint32_t m = max(amax16(s.b[j][0], s.b[j][1]), amax16(s.b[j][2], s.b[j][3]));
       sb = (int)fp4_scale_code(m >> 7);
@@ -172,12 +221,12 @@ __device__ __forceinline__ void mma_step(f32x4 (&acc)[WB][TB], const Step<SRC, W
       const i32x2 e2 = e4m3_encode8_bf16(s.b[j][2], c1), e3 = e4m3_encode8_bf16(s.b[j][3], c1);
       b = i32x8{e0[0], e0[1], e1[0], e1[1], e2[0], e2[1], e3[0], e3[1]};
     }
-#pragma unroll
-    for (int i = 0; i < WB; ++i) {
+    static_for<0, WB>([&](auto I) {
+      constexpr int i = decltype(I)::value;
       const i32x8 a = {s.a[i][0], s.a[i][1], s.a[i][2], s.a[i][3], 0, 0, 0, 0};
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[i][j], 4, FB, 0, s.sa[i], 0, sb);
-    }
-  }
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[i][j], 4, FB, i % 4, sa[i / 4], opb, sb);
+    });
+  });
 }
 
 // NW waves; D slabs in flight per wave. The partial sums go through LDS in
@@ -262,53 +311,49 @@ int fragments(int64_t M, int64_t N) {
   return f;
 }
 
-// Tile shapes, from a sweep over WB, TB, waves and slabs in flight at N = 1024 ..
-// 15360, K = 4096 .. 14336 and 1 to 512 tokens. Eight waves with one slab in
+// Tile shapes, from sweeps over WB, TB, waves and slabs in flight at N = 1024 ..
+// 15360, K = 4096 .. 14336 and 1 to 256 tokens. Eight waves with one slab in
 // flight are best nearly throughout: a wave's share of K is a handful of slabs,
 // and the other waves hide its latency better than deeper prefetching. At
-// 5120 x 5120: 16 tokens 5.0 us on 32 x 16 tiles (16 x 16: 5.4, 64 x 16: 5.9);
-// 128 tokens 8.9 us on 64 x 64 (128 x 32: 10.3). MXFP8 tokens cost twice their
-// MXFP4 bytes, so their tiles are longer in weight rows: 128 tokens 12.7 us on
-// 128 x 32 by four waves with two slabs in flight (eight waves 13.5; 64 x 64:
-// 13.4). Splitting K over workgroups as well, with a second kernel adding the
-// parts, was slower at every shape but MXFP8 tokens with K = 13824, where it
-// gained up to a fifth (128 tokens: 21.3 against 26.7 us): not kept.
+// 5120 x 5120: 16 tokens 5.0 us on 32 x 16 tiles (16 x 16: 5.2, 64 x 16: 5.3);
+// 128 tokens 7.7 us on 64 x 64 (128 x 32: 8.3, 32 x 64: 8.3). MXFP8 tokens cost
+// twice their MXFP4 bytes, so their tiles are longer in weight rows: 128 tokens
+// 9.8 us on 128 x 32 (64 x 64: 10.3); 128 x 13824 x 5120 18.4 (20.1). Long rows
+// on the smallest tiles take 16 waves (16 x 14336 x 2048: 6.2 against 7.6 us).
+// Splitting K over workgroups too, with a second kernel adding the parts, was
+// slower at nearly every shape (at best a fifth faster): not kept.
+constexpr int64_t kLongK = 8192;
+
 hipError_t dispatch_fp4(FewParams& p, int epi, hipStream_t st) {
   const int f = fragments(p.M, p.N);
-  if (f == 1) return launch_few<SRC_FP4, 1, 1, 8, 1>(p, epi, st);
-  if (f == 2) return launch_few<SRC_FP4, 2, 1, 8, 1>(p, epi, st);
+  if (f == 1) return p.K >= kLongK ? launch_few<SRC_FP4, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP4, 1, 1, 8, 1>(p, epi, st);
+  if (f == 2) return p.K >= kLongK ? launch_few<SRC_FP4, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP4, 2, 1, 8, 1>(p, epi, st);
   if (p.M <= 16) return launch_few<SRC_FP4, 4, 1, 8, 1>(p, epi, st);
   if (f == 4) return launch_few<SRC_FP4, 2, 2, 8, 1>(p, epi, st);
   if (f == 8 || p.M <= 32) return launch_few<SRC_FP4, 4, 2, 8, 1>(p, epi, st);
   if (f == 16 || p.M <= 64) return launch_few<SRC_FP4, 4, 4, 8, 1>(p, epi, st);
-  return launch_few<SRC_FP4, 4, 8, 8, 1>(p, epi, st);
+  return launch_few<SRC_FP4, 8, 4, 8, 1>(p, epi, st);
 }
 
 hipError_t dispatch_fp8(FewParams& p, int epi, hipStream_t st) {
   const int f = fragments(p.M, p.N);
-  if (f == 1) return launch_few<SRC_FP8, 1, 1, 8, 1>(p, epi, st);
+  if (f == 1) return p.K >= kLongK ? launch_few<SRC_FP8, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP8, 1, 1, 8, 1>(p, epi, st);
   if (f == 2) return launch_few<SRC_FP8, 2, 1, 8, 1>(p, epi, st);
   if (p.M <= 16 || (f == 4 && p.M <= 32)) return launch_few<SRC_FP8, 4, 1, 8, 1>(p, epi, st);
   if (f == 4) return launch_few<SRC_FP8, 2, 2, 8, 1>(p, epi, st);
   if (f == 8) return launch_few<SRC_FP8, 4, 2, 8, 1>(p, epi, st);
-  if (f == 16 || p.M <= 32) return launch_few<SRC_FP8, 8, 2, 4, 2>(p, epi, st);
-  return launch_few<SRC_FP8, 8, 4, 4, 1>(p, epi, st);
+  if (f == 16 || p.M <= 32) return launch_few<SRC_FP8, 8, 2, 8, 1>(p, epi, st);
+  return launch_few<SRC_FP8, 8, 4, 8, 1>(p, epi, st);
 }
 
-// bf16 rows (at most 16): one token fragment. Rounding to E4M3 keeps a wave
-// longer than its loads, so long rows take 16 waves (1 x 13824 x 5120: 13.1
-// against 15.1 us).
+// bf16 rows (at most 16): one token fragment. Rounding keeps a wave longer than
+// its loads, so long rows take 16 waves here too (1 x 13824 x 5120: 10.6 against
+// 11.7 us, to E4M3 13.4 against 15.2).
 template <int SRC>
 hipError_t dispatch_rows(FewParams& p, int epi, hipStream_t st) {
   const int f = fragments(p.M, p.N);
-  if constexpr (SRC == SRC_BF16_FP8) {
-    if (p.K >= 8192) {
-      if (f == 1) return launch_few<SRC, 1, 1, 16, 1>(p, epi, st);
-      if (f == 2) return launch_few<SRC, 2, 1, 16, 1>(p, epi, st);
-    }
-  }
-  if (f == 1) return launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
-  if (f == 2) return launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
+  if (f == 1) return p.K >= kLongK ? launch_few<SRC, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
+  if (f == 2) return p.K >= kLongK ? launch_few<SRC, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
   return launch_few<SRC, 4, 1, 8, 1>(p, epi, st);
 }
 
