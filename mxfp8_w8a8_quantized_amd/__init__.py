@@ -809,11 +809,14 @@ def _act_format(act):
     return ACT_FORMATS[act]
 
 
-def _need_rows(x, name, dtypes):
+def _need_rows(x, name, dtypes, shape=None, dev=None):
+    """x is 2-D, of one of `dtypes`, with unit column stride (and of `shape`, on `dev`)."""
     if not isinstance(x, torch.Tensor) or x.dtype not in dtypes or x.dim() != 2:
         raise TypeError(f"{name} must be a 2-D tensor of {' or '.join(str(d) for d in dtypes)}")
     if x.stride(1) != 1 and x.shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
+    if shape is not None and (x.shape != shape or x.device != dev):
+        raise ValueError(f"{name} must be {list(shape)} on {dev}")
 
 
 def _pitch(x):
@@ -821,6 +824,7 @@ def _pitch(x):
 
 
 _DTYPES = {torch.float32: MX_DT_F32, torch.bfloat16: MX_DT_BF16}
+_BF16 = (torch.bfloat16,)
 
 
 # A call of a few tokens runs for about as long on the GPU as Python needs to
@@ -876,9 +880,7 @@ def mx_fp4_dequantize_slab(slab, y=None, dtype=torch.bfloat16):
         if dtype not in _DTYPES:
             raise TypeError("dtype must be bfloat16 or float32")
         y = torch.empty((slab.rows, slab.K), dtype=dtype, device=dev)
-    _need_rows(y, "y", (torch.bfloat16, torch.float32))
-    if y.device != dev or tuple(y.shape) != (slab.rows, slab.K):
-        raise ValueError(f"y must be [{slab.rows}, {slab.K}] on {dev}")
+    _need_rows(y, "y", _DTYPES, (slab.rows, slab.K), dev)
     _run(lib().mx_fp4_dequantize_slab, dev, _adr(slab.q), _adr(slab.s), slab.rows, slab.K, _adr(y), _DTYPES[y.dtype],
          _pitch(y))
     return y
@@ -969,7 +971,7 @@ def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None
     mx_fp4_linear_ws_bytes(M, K, N, act) bytes (allocated here when None and
     needed; a few tokens need none)."""
     fmt = _act_format(act)
-    _need_rows(x, "x", (torch.bfloat16,))
+    _need_rows(x, "x", _BF16)
     dev = x.device
     M, K = x.shape
     y = _fp4_linear_out(M, w, bias, y, dev)
@@ -994,18 +996,21 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
     is None without a residual. y: bf16 [M, K] that also receives the norm, if
     given."""
     fmt = _act_format(act)
-    _need_rows(x, "x", (torch.bfloat16,))
-    dev = x.device
-    M, K = x.shape
-    if K == 0 or K % (32 if act == "fp4" else 64) != 0:
+    _need_rows(x, "x", _BF16)
+    dev, shape = x.device, x.shape
+    M, K = shape
+    if K == 0 or K % (32 if fmt == MX_ACT_FP4 else 64) != 0:
         raise ValueError("K must be a positive multiple of 32 (fp4) or 64 (fp8)")
-    rdt = wdt = 0
+    rdt = wdt = ldr = ldo = ldy = 0
     if residual is not None:
-        _need_rows(residual, "residual", (torch.bfloat16, torch.float32))
-        rdt = _DTYPES[residual.dtype]
+        _need_rows(residual, "residual", _DTYPES, shape, dev)
+        rdt, ldr = _DTYPES[residual.dtype], _pitch(residual)
         if residual_out is None:
-            residual_out = residual.new_empty((M, K))
-        _need_rows(residual_out, "residual_out", (residual.dtype,))
+            residual_out = residual.new_empty(shape)
+            ldo = K
+        else:
+            _need_rows(residual_out, "residual_out", (residual.dtype,), shape, dev)
+            ldo = _pitch(residual_out)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
@@ -1016,12 +1021,15 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
             raise ValueError(f"weight must be [{K}]")
         wdt = _DTYPES[weight.dtype]
     if y is not None:
-        _need_rows(y, "y", (torch.bfloat16,))
-    for name, t in (("residual", residual), ("residual_out", residual_out), ("y", y)):
-        if t is not None and (t.device != dev or t.shape != x.shape):
-            raise ValueError(f"{name} must be [{M}, {K}] on {dev}")
-    out = _fp4_out(M, K, x, out) if act == "fp4" else _slab_out(M, K, dev, out)
-    _run(lib().mx_rmsnorm_slab, dev, _adr(x), _pitch(x), _adr(residual), rdt, 0 if residual is None else _pitch(residual),
-         _adr(weight), wdt, float(eps), M, K, _adr(residual_out), 0 if residual_out is None else _pitch(residual_out),
-         _adr(y), 0 if y is None else _pitch(y), fmt, _adr(out.q), _adr(out.s))
+        _need_rows(y, "y", _BF16, shape, dev)
+        ldy = _pitch(y)
+    if fmt == MX_ACT_FP4:
+        out = _fp4_out(M, K, x, out)
+    elif out is None:
+        R = (M + 255) // 256 * 256
+        out = Slab(x.new_empty((K // 64, R, 64), dtype=torch.uint8), x.new_empty((K // 64, R, 2), dtype=torch.uint8), M)
+    else:
+        out = _slab_out(M, K, dev, out)
+    _run(lib().mx_rmsnorm_slab, dev, x.data_ptr(), _pitch(x), _adr(residual), rdt, ldr, _adr(weight), wdt, float(eps), M, K,
+         _adr(residual_out), ldo, _adr(y), ldy, fmt, out.q.data_ptr(), out.s.data_ptr())
     return out, residual_out
