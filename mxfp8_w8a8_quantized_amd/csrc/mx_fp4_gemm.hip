@@ -498,21 +498,22 @@ hipError_t launch(const GemmParams& p, int epi, hipStream_t st) {
 // CU) take the least time, from the measured time of a round at K = 5120 (us;
 // longer or shorter K scale all shapes about alike). Checked over 256 to 16384
 // tokens and 4096 to 15360 outputs, e.g. (us, chosen first): 512 x 5120 128 x 128
-// 13.3, 192 x 128 14.6, 256 x 128 16.7, 256 x 256 25.4; 1024 x 5120 192 x 128
-// 18.5, 256 x 128 19.3, 128 x 128 25.8, 256 x 256 26.5; 4001 x 5120 256 x 128
-// 63.0, 256 x 256 65.8; 3000 x 15360 256 x 256 115, 256 x 128 129. The small
-// tiles are bound by the CU's load path (about 35 bytes a cycle), the large ones
-// by the matrix cores.
+// 13.3, 256 x 128 16.7, 256 x 256 25.4; 1024 x 5120 256 x 128 19.3, 128 x 128
+// 25.8, 256 x 256 26.5; 4001 x 5120 256 x 128 63.0, 256 x 256 65.8; 3000 x 15360
+// 256 x 256 115, 256 x 128 129. 192-row tiles gain only with MXFP8 tokens: 1024
+// x 5120 24.5 against 26.8 on 256 x 128 (MXFP4: 18.2 to 20.5 against 19.2). The
+// small tiles are bound by the CU's load path (about 35 bytes a cycle), the large
+// ones by the matrix cores.
 void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile) {
   struct Tile {
     int weights, tokens;
     double us;
   };
-  static const Tile fp4_tiles[] = {{256, 256, 32.0}, {256, 128, 19.5}, {192, 128, 17.5}, {128, 128, 12.8}};
+  static const Tile fp4_tiles[] = {{256, 256, 32.0}, {256, 128, 19.5}, {128, 128, 12.8}};
   static const Tile fp8_tiles[] = {{256, 128, 28.0}, {192, 128, 24.6}, {128, 128, 17.1}};
   const Tile* t = fp8 ? fp8_tiles : fp4_tiles;
   double best = -1.0;
-  for (int i = 0; i < (fp8 ? 3 : 4); ++i) {
+  for (int i = 0; i < 3; ++i) {
     const int64_t tiles = (M + t[i].tokens - 1) / t[i].tokens * ((N + t[i].weights - 1) / t[i].weights);
     const double us = (double)((tiles + 255) / 256) * t[i].us;
     if (best < 0.0 || us < best) {
@@ -547,7 +548,6 @@ hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, con
   }
   if (token_tile == 256) return launch<4, 4, false>(p, epi, stream);
   if (weight_tile == 128) return launch<2, 2, false>(p, epi, stream);
-  if (weight_tile == 192) return launch<3, 2, false>(p, epi, stream);
   return launch<4, 2, false>(p, epi, stream);
 }
 

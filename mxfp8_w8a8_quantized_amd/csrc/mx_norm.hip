@@ -12,8 +12,10 @@
 //
 // The squares are summed, and h * rstd * gain is multiplied out, in float64.
 // The sum then neither overflows nor underflows for any bf16 or f32 row, and
-// a code differs from the formula's only where float64 itself is in doubt;
-// the float64 operations (five an element) stay hidden behind the loads.
+// a code differs from the formula's only where float64 itself is in doubt. With
+// a residual the float64 operations (three an element, and four conversions)
+// stay hidden behind memory; without one they bound the kernel at about 1.4e12
+// elements a second (75348 x 5120: 264 us, 4.4 TB/s).
 //
 // norm_tile_kernel, for many rows: a block takes 8 rows, a wave each; the
 // codes pass through LDS in slab order, so that every slab's part of them
@@ -332,14 +334,19 @@ hipError_t launch_row(const NormParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Rows from which the tiled form is taken: eight rows a block then give two
-// blocks a CU.
-constexpr int64_t kTileMinRows = 4096;
+// Rows from which the tiled form is taken. Its blocks take eight rows each and
+// their stores are whole lines, but a wave waits for its whole row; the row form
+// spreads a row over 4 or 8 waves. bf16 residual, MXFP8 (us, tiled against row
+// form): 2048 x 2048 8.1, 9.5; 8192 x 2048 22.4, 26.1; 75348 x 2048 209, 233; 8192
+// x 4096 45.6, 39.6; 16384 x 8192 226, 204; 40000 x 5120 286, 311; 75348 x 5120
+// 521 (5.2 TB/s), 624; 75348 x 8192 950, 1059.
+constexpr int64_t kTileMinRows = 32768;
+constexpr int64_t kTileMinRowsShort = 2048;  // K <= 2048
 
 template <int RES, bool FP4>
 hipError_t dispatch(const NormParams& p, hipStream_t st) {
   const int ch = (p.K + 511) / 512;
-  if (p.M >= kTileMinRows) {
+  if (p.M >= (ch <= 4 ? kTileMinRowsShort : kTileMinRows)) {
     if (ch <= 4) return launch_tile<RES, FP4, 4>(p, st);
     if (ch <= 8) return launch_tile<RES, FP4, 8>(p, st);
     if (ch <= 10) return launch_tile<RES, FP4, 10>(p, st);
@@ -347,7 +354,9 @@ hipError_t dispatch(const NormParams& p, hipStream_t st) {
       if (ch <= 16) return launch_tile<RES, FP4, 16>(p, st);
   }
   if (ch <= 8) return launch_row<RES, FP4, 4, 2>(p, st);
+  if (ch <= 12) return launch_row<RES, FP4, 4, 3>(p, st);
   if (ch <= 16) return launch_row<RES, FP4, 4, 4>(p, st);
+  if (ch <= 24) return launch_row<RES, FP4, 8, 3>(p, st);
   if (ch <= 32) return launch_row<RES, FP4, 8, 4>(p, st);
   return launch_row<RES, FP4, 8, 16>(p, st);
 }

@@ -59,7 +59,7 @@ def check(x, r, w, eps, act, slab, h, y, what):
 
 @pytest.mark.parametrize("act", ["fp8", "fp4"])
 @pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("M,K", [(1, 64), (1, 5120), (3, 192), (17, 4096), (257, 576), (16, 8192), (5, 8256), (2, 16448)])
+@pytest.mark.parametrize("M,K", [(1, 64), (1, 5120), (3, 192), (17, 4096), (257, 576), (16, 8192), (5, 8256), (2, 16448), (3, 11008), (2, 65536)])
 def test_few_rows(M, K, res, act):
     print(f"norm M={M} K={K} res={res} {act}", flush=True)
     d = dev()
@@ -80,10 +80,10 @@ def test_fp4_takes_any_multiple_of_32(K):
 
 @pytest.mark.parametrize("act", ["fp8", "fp4"])
 @pytest.mark.parametrize("res", [None, torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("K", [192, 2112, 4096, 5120, 5184])
+@pytest.mark.parametrize("K", [192, 2048, 2112, 4096, 5120, 5184, 8192])
 def test_many_rows(K, res, act):
-    """From 4096 rows: the tiled form (and past it for long f32 rows)."""
-    M = 4100
+    """The tiled form, from 2048 rows or, for K > 2048, 32768 (past it long f32 rows)."""
+    M = 4100 if K <= 2048 else 32772
     print(f"norm M={M} K={K} res={res} {act}", flush=True)
     d = dev()
     g = torch.Generator(device=d).manual_seed(K)
@@ -106,7 +106,7 @@ def test_many_rows(K, res, act):
     else:
         ref = mx().mx_quantize_act_slab(y)
     assert torch.equal(slab.q, ref.q) and torch.equal(slab.s, ref.s)
-    assert R == 4352
+    assert R == (M + 255) // 256 * 256
 
 
 @pytest.mark.parametrize("act", ["fp8", "fp4"])
