@@ -80,6 +80,29 @@ def test_linear_matches_oracle(M, K, N, act):
 
 
 @pytest.mark.parametrize("act", ["fp4", "fp8"])
+@pytest.mark.parametrize("M,K,N", [(1, 5120, 5136), (16, 4096, 2064), (7, 8256, 4112), (5, 13824, 6160), (11, 8832, 1040),
+                                   (9, 8192, 16400)])
+def test_one_call_sums_in_the_slab_calls_order(M, K, N, act):
+    """Products that cancel: the second half of K holds the first's groups in
+    another order with the weights negated, and the groups span many binades,
+    so that what is left is the fp32 sums' rounding, which shows the order of
+    the sums. The one-call linear, which quantizes a few tokens in its kernel,
+    adds in the slab call's order."""
+    print(f"fp4 order M={M} K={K} N={N} {act}", flush=True)
+    d = dev()
+    g = torch.Generator(device=d).manual_seed(M + K)
+    n = K // 64  # groups in a half
+    x = torch.randn((M, n, 32), generator=g, device=d) * torch.exp2(8 * torch.randn((1, n, 1), generator=g, device=d))
+    w = torch.randn((N, n, 32), generator=g, device=d)
+    order = torch.randperm(n, generator=g, device=d)
+    x = torch.cat([x, x[:, order]], 1).reshape(M, K).to(torch.bfloat16)
+    ws = mx().mx_fp4_quantize_weight_slab(torch.cat([w, -w[:, order]], 1).reshape(N, K))
+    y = mx().mx_fp4_linear(x, ws, act=act)
+    assert bool((y != 0).any())
+    assert same(mx().mx_fp4_linear_slab(quantized(x, act), ws), y)
+
+
+@pytest.mark.parametrize("act", ["fp4", "fp8"])
 @pytest.mark.parametrize("M", [1, 13, 40, 300, 700])
 def test_rows_are_independent_of_their_batch(M, act):
     """A token's output does not change with the tokens behind it, as long as
