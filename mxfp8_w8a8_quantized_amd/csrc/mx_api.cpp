@@ -1006,6 +1006,9 @@ int check_fp4_linear(int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws,
   if (!aligned(wq, 16) || !aligned(y, 16) || !aligned(ws, 4))
     return fail(MX_ERR_INVALID_ARGUMENT, "codes and y must be 16-byte aligned, scales 4-byte aligned");
   if (bias != nullptr && !aligned(bias, 2)) return fail(MX_ERR_INVALID_ARGUMENT, "bias must be 2-byte aligned");
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  if (!fp4_few(M, K, N) && tiles >= kMaxSplitWorkgroups)
+    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
   return MX_OK;
 }
 
@@ -1126,9 +1129,6 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
     return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y, hs),
                   "MXFP4 linear launch");
   }
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  if (tiles >= kMaxSplitWorkgroups)
-    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
   int weight_tile, token_tile;

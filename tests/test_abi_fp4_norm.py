@@ -102,6 +102,14 @@ def test_one_call_rejects_bad_arguments(L):
     assert f(0, 96, 32, 1) == 0 and f(8, 96, 0, 1) == 0
 
 
+def test_linears_refuse_too_many_tiles_before_any_launch(L):
+    """2^30 x 2^20 outputs: more workgroups than a launch holds. The one-call
+    linear says so before its quantizer has written to the workspace."""
+    for call in (lambda: slab(M=1 << 30, N=1 << 20), lambda: one(M=1 << 30, N=1 << 20, nb=1 << 62)):
+        assert call() == UNS
+        assert b"tiles" in L.mx_last_error_message()
+
+
 def norm(x=A, ldx=64, res=0, rdt=0, ldr=64, w=0, wdt=0, eps=1e-6, M=4, K=64, ro=0, ldo=64, y=0, ldy=64, act=0, q=B, s=C):
     return mx().lib().mx_rmsnorm_slab(P(x), ldx, P(res), rdt, ldr, P(w), wdt, eps, M, K, P(ro), ldo, P(y), ldy, act, P(q),
                                       P(s), P(0))
