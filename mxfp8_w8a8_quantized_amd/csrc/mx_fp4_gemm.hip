@@ -474,13 +474,10 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
 template <int EPI, int IA, int JB, bool X8>
 hipError_t launch(GemmParams p, hipStream_t st) {
   using Sh = Shape<IA, JB, X8>;
-  static bool configured = false;  // per instantiation; benign race (idempotent)
+  static std::atomic<uint64_t> configured{0};  // per instantiation
   auto kern = fp4_gemm_kernel<EPI, IA, JB, X8>;
-  if (!configured) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  const hipError_t e = allow_dynamic_lds((const void*)kern, Sh::LDS, configured);
+  if (e != hipSuccess) return e;
   p.tiles_m = (p.M + Sh::MT - 1) / Sh::MT;
   p.tiles_n = (p.N + Sh::BN - 1) / Sh::BN;
   hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(NT), Sh::LDS, st, p);

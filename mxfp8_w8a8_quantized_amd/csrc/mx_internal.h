@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mx {
 
 // Elementwise MX quantization of `rows` rows of K elements (pitch ld
@@ -99,6 +101,20 @@ hipError_t launch_pc_quantize_slab(int kind, const void* x, int64_t rows, int64_
 hipError_t launch_pc_linear_slab(const uint8_t* xq, const float* xs, int64_t M, int64_t K, const uint8_t* wq,
                                  const float* ws, int64_t N, const void* bias, int epi, void* y, hipStream_t stream);
 
+// Raises a kernel's limit of dynamic LDS to `bytes`. The attribute belongs to
+// one device's copy of the kernel, so it is set at its first launch on each:
+// bit d of `done`, which the caller keeps per kernel, for device d (< 64).
+inline hipError_t allow_dynamic_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // MXFP4 (mx_fp4_device.h has the slab layout). Rows of bf16 (kind 0) or f32
 // (kind 1) to a slab; a slab to row-major bf16 (kind 0) or f32 (kind 1) y;
 // row-major packed codes to a slab; a slab to the MXFP8 slab of the same
@@ -126,10 +142,11 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
 void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile);
 
 // MXFP4-weight linear on tiles of 128, 256 or (MXFP8 tokens) 192 weight rows x
-// 128 tokens, or (MXFP4 tokens) 256 x 256 (mx_fp4_gemm.hip); N % 16 == 0, tiles below 2^24.
-hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
-                                   const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
-                                   hipStream_t stream);
+// 128 tokens, or (MXFP4 tokens) 256 x 256 (mx_fp4_gemm.hip); N % 16 == 0, tiles
+// below 2^24.
+hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs,
+                                   int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
+                                   const void* bias, int epi, void* y, hipStream_t stream);
 
 // Residual add, RMS norm and quantization into a slab (mx_norm.hip). K up to
 // kNormMaxK (a row stays in one block's registers); residual, residual_out,

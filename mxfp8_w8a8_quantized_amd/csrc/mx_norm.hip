@@ -315,14 +315,10 @@ __global__ __launch_bounds__(64 * WPR) void norm_row_kernel(NormParams p) {
 
 template <int RES, bool FP4, int NCH>
 hipError_t launch_tile(const NormParams& p, hipStream_t st) {
-  static bool configured = false;  // per instantiation; benign race (idempotent)
+  static std::atomic<uint64_t> configured{0};  // per instantiation
   auto kern = norm_tile_kernel<RES, FP4, NCH>;
-  if (!configured) {
-    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             Stage<FP4>::bytes(512 * NCH));
-    if (e != hipSuccess) return e;
-    configured = true;
-  }
+  const hipError_t e = allow_dynamic_lds((const void*)kern, Stage<FP4>::bytes(512 * NCH), configured);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(p.R / kTileRows)), dim3(64 * kTileRows), Stage<FP4>::bytes(p.K), st, p);
   return hipGetLastError();
 }
