@@ -577,8 +577,10 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
  * 16, at most 98304 elements) are quantized inside the product's kernel: one
  * launch, no workspace. More go through a slab in the workspace
  * (mx_fp4_linear_ws_bytes bytes, 256-byte aligned, overlapping no argument; its
- * contents are overwritten and need no initial value). mx_fp4_linear_ws_bytes
- * is 0 where none is needed, -1 on a bad shape or format. Nothing is allocated. */
+ * contents are overwritten and need no initial value). Calls, or graphs that
+ * captured them, that can run at the same time need a workspace each.
+ * mx_fp4_linear_ws_bytes is 0 where none is needed, -1 on a bad shape or format.
+ * Nothing is allocated. */
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
 int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx,
                   const uint8_t* wq, const uint8_t* ws, int64_t N,
@@ -599,7 +601,8 @@ int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx,
  * bf16 or f32 (wdtype) [K], or NULL for ones; eps >= 0 and finite;
  * residual_out (h): of the residual's type [M][ldo], or NULL to drop it; it may
  * be the residual itself with the same pitch, and must otherwise overlap
- * nothing; y: bf16 [M][ldy], or NULL to drop it; q, s: the slab. rdtype and
+ * nothing (a strided buffer counts whole, from its first element to its last);
+ * y: bf16 [M][ldy], or NULL to drop it; q, s: the slab. rdtype and
  * wdtype are ignored for NULL pointers. Every buffer 16-byte aligned, rows a
  * multiple of 16 bytes apart. K as the format requires, at most 65536, M at
  * most 2^22 (else MX_ERR_UNSUPPORTED).

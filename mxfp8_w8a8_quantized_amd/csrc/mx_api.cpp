@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -1190,7 +1191,7 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
   if ((st = check_act_k(act, K)) != MX_OK) return st;
   if (K > mx::kNormMaxK) return fail(MX_ERR_UNSUPPORTED, "K = %lld exceeds the norm's 65536", (long long)K);
   if (M > mx::kNormMaxRows) return fail(MX_ERR_UNSUPPORTED, "M = %lld exceeds the norm's 2^22", (long long)M);
-  if (!(eps >= 0.0 && eps <= 1e30)) return fail(MX_ERR_INVALID_ARGUMENT, "eps = %g must be finite and >= 0", eps);
+  if (!(eps >= 0.0 && std::isfinite(eps))) return fail(MX_ERR_INVALID_ARGUMENT, "eps = %g must be finite and >= 0", eps);
   if (residual != nullptr && rdtype != MX_DT_BF16 && rdtype != MX_DT_F32)
     return fail(MX_ERR_INVALID_ARGUMENT, "unknown residual dtype %d", rdtype);
   if (weight != nullptr && wdtype != MX_DT_BF16 && wdtype != MX_DT_F32)

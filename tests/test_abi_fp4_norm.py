@@ -134,6 +134,10 @@ def test_rmsnorm_rejects_bad_arguments():
     assert norm(M=0, x=0, q=0, s=0) == OK
 
 
+def test_rmsnorm_takes_any_finite_eps():
+    assert all(norm(eps=e, M=0, x=0, q=0, s=0) == OK for e in (0.0, 1e-300, 1.0, 1e31, 1e300))
+
+
 def test_binding_rejects_wrong_tensors():
     m = mx()
     with pytest.raises(TypeError):
