@@ -1,5 +1,6 @@
 // Linear on MXFP4 weights for many tokens, on slab operands (mx_fp4_device.h;
-// the tokens MXFP4, or MXFP8 in their own slab layout):
+// the tokens MXFP4, or MXFP8 in their own slab layout); 128 x 128 tiles of MXFP4
+// tokens have a kernel of their own (mx_fp4_mid.hip):
 //
 //   y[m][n] = bf16_rne( epi( sum_k xhat[m][k] * what[n][k] + f32(bias[n]) ) )
 //
@@ -73,22 +74,21 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 // A tile's shape and its step's schedule. LDS: RING regions (weight codes, then
 // token codes), the scale ring [weights, tokens][8 steps][1 KB], a 256-byte bias
-// slot per wave. The smaller tiles' steps are shorter and need more of them in
-// flight to cover the latency of memory; RING is even, since scales are fetched
-// for two steps at a time, and RING + 2 scale slots are in use.
+// slot per wave. RING is even, since scales are fetched for two steps at a time,
+// and RING + 2 scale slots are in use.
 constexpr int SR_SLOT = 1024;
 constexpr int SR_OP = 8 * SR_SLOT;
 
 template <int IA, int JB, bool X8>
 struct Shape {
-  static_assert(!X8 || JB == 2, "MXFP8 tokens come in tiles of 128");
+  static_assert(X8 ? JB == 2 : IA == 4, "MXFP8 tokens come in tiles of 128, MXFP4 ones with 256 weight rows");
   static constexpr int BN = 64 * IA;                      // weight rows per tile
   static constexpr int MT = 64 * JB;                      // tokens per tile
   static constexpr int XB = X8 ? 2 * JB : JB;             // 1 KB token blocks per wave and step
   static constexpr int CL = IA + XB;                      // code DMAs per wave and step
   static constexpr int R_X = IA * 4096;                   // token codes within a region
   static constexpr int REGION = CL * 4096;
-  static constexpr int RING = CL <= 5 ? 6 : 4;
+  static constexpr int RING = 4;
   static constexpr int SR = RING * REGION;
   static constexpr int BIAS = SR + 2 * SR_OP;
   static constexpr int STAGE = 32 * JB * 256;             // epilogue staging per wave
@@ -100,7 +100,7 @@ struct Shape {
   static constexpr int NR = NC + IA + JB;                 // and the scale pairs
   // MFMAs issued ahead of the step's barrier, about 190 cycles of them, and
   // set-up instructions behind each.
-  static constexpr int PRE = X8 ? 3 : JB == 4 ? 8 : NM == 8 ? 3 : 4;
+  static constexpr int PRE = X8 ? 3 : JB == 4 ? 8 : 4;
   static constexpr int SETUP = X8 ? 11 : 6;
   static constexpr int RS = (NM - PRE) * 10 / 13;         // MFMAs after it that carry reads
   static constexpr int DS = X8 ? (NM - PRE) * 9 / 13 : (NM - PRE) * 18 / 26 + 1;  // and loads
@@ -491,28 +491,40 @@ hipError_t launch(const GemmParams& p, int epi, hipStream_t st) {
 
 }  // namespace
 
-// The tile shape for an output: the one whose rounds of 256 workgroups (one a
+// The tile shape for an output: the one whose rounds of workgroups (256, one a
 // CU) take the least time, from the measured time of a round at K = 5120 (us;
-// longer or shorter K scale all shapes about alike). Checked over 256 to 16384
-// tokens and 4096 to 15360 outputs, e.g. (us, chosen first): 512 x 5120 128 x 128
-// 13.3, 256 x 128 16.7, 256 x 256 25.4; 1024 x 5120 256 x 128 19.3, 128 x 128
-// 25.8, 256 x 256 26.5; 4001 x 5120 256 x 128 63.0, 256 x 256 65.8; 3000 x 15360
-// 256 x 256 115, 256 x 128 129. 192-row tiles gain only with MXFP8 tokens: 1024
-// x 5120 24.5 against 26.8 on 256 x 128 (MXFP4: 18.2 to 20.5 against 19.2). The
-// small tiles are bound by the CU's load path (about 35 bytes a cycle), the large
-// ones by the matrix cores.
+// longer or shorter K scale all shapes about alike). MXFP4 tiles of 128 x 128
+// (mx_fp4_mid.hip) run two a CU: up to 512 a round, and less time up to 256.
+// Checked over 130 to 24000 tokens, 1024 to 16384 outputs and K = 1056 to 12256:
+// the choice was the fastest of the three in 30 of 32 shapes, and 9% slower in the
+// other two. E.g. (us, chosen first): 512 x 5120 128 x 128 12.4, 256 x 128 17.4,
+// 256 x 256 26.3; 1024 x 5120 256 x 128 18.8, 128 x 128 20.6, 256 x 256 26.9; 4001
+// x 5120 128 x 128 59.4, 256 x 128 60.6, 256 x 256 63.7; 3000 x 15360 256 x 256
+// 114, 256 x 128 125, 128 x 128 129. 192-row tiles gain only with MXFP8 tokens:
+// 1024 x 5120 24.5 against 26.8 on 256 x 128 (MXFP4: 18.2 to 20.5 against 19.2).
+// At one workgroup a CU a tile of 256 x 256 spends 1136 cycles a step, 1120 of
+// them in its MFMAs, one of 256 x 128 660 (560); from a few hundred workgroups the
+// clock falls to what power allows (2.4 to 1.4 GHz), so the shapes' times differ by
+// less than their cycles.
 void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile) {
   struct Tile {
     int weights, tokens;
-    double us;
+    double us, us_pair;  // a round, one and (where they fit) two workgroups a CU
   };
-  static const Tile fp4_tiles[] = {{256, 256, 32.0}, {256, 128, 19.5}, {128, 128, 12.8}};
-  static const Tile fp8_tiles[] = {{256, 128, 28.0}, {192, 128, 24.6}, {128, 128, 17.1}};
+  static const Tile fp4_tiles[] = {{256, 256, 32.0, 0.0}, {256, 128, 19.5, 0.0}, {128, 128, 11.6, 21.3}};
+  static const Tile fp8_tiles[] = {{256, 128, 28.0, 0.0}, {192, 128, 24.6, 0.0}, {128, 128, 17.1, 0.0}};
   const Tile* t = fp8 ? fp8_tiles : fp4_tiles;
+  const int shapes = !fp8 && M > kMidMaxRows ? 2 : 3;
   double best = -1.0;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < shapes; ++i) {
     const int64_t tiles = (M + t[i].tokens - 1) / t[i].tokens * ((N + t[i].weights - 1) / t[i].weights);
-    const double us = (double)((tiles + 255) / 256) * t[i].us;
+    double us;
+    if (t[i].us_pair > 0.0) {
+      const int64_t rest = tiles % 512;
+      us = (double)(tiles / 512) * t[i].us_pair + (rest == 0 ? 0.0 : rest <= 256 ? t[i].us : t[i].us_pair);
+    } else {
+      us = (double)((tiles + 255) / 256) * t[i].us;
+    }
     if (best < 0.0 || us < best) {
       best = us;
       *weight_tile = t[i].weights;
@@ -524,6 +536,8 @@ void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token
 hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs,
                                    int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
                                    const void* bias, int epi, void* y, hipStream_t stream) {
+  if (!fp8 && weight_tile == 128)
+    return launch_fp4_linear_mid(xq, xs, M, K, wq, ws, N, bias, epi, y, stream);
   GemmParams p;
   p.x = xq;
   p.xs = xs;
@@ -543,9 +557,7 @@ hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, con
     if (weight_tile == 192) return launch<3, 2, true>(p, epi, stream);
     return launch<4, 2, true>(p, epi, stream);
   }
-  if (token_tile == 256) return launch<4, 4, false>(p, epi, stream);
-  if (weight_tile == 128) return launch<2, 2, false>(p, epi, stream);
-  return launch<4, 2, false>(p, epi, stream);
+  return token_tile == 256 ? launch<4, 4, false>(p, epi, stream) : launch<4, 2, false>(p, epi, stream);
 }
 
 }  // namespace mx

@@ -79,6 +79,22 @@ def test_linear_matches_oracle(M, K, N, act):
     assert same(ys, y)
 
 
+@pytest.mark.parametrize("K", [96, 256, 352, 512, 640, 736, 896, 1024, 1120, 1920, 2048, 2144, 3168])
+def test_every_remainder_of_steps_on_small_tiles(K):
+    """The 128 x 128 tiles run steps of 128 K in blocks of eight: every remainder,
+    less than a block, one, more; ragged rows and columns, with and without GELU."""
+    M, N = 699, 2320
+    gelu = K % 256 == 0
+    print(f"fp4 small tiles K={K}", flush=True)
+    d = dev()
+    x = synth.make_activation(M, K, seed=K)
+    w = synth.make_weight(N, K, seed=K + 1) * 4
+    b = synth.make_bias(N, seed=K) if K % 3 else None
+    y = mx().mx_fp4_linear(x.to(d), mx().mx_fp4_quantize_weight_slab(w.to(d)), None if b is None else b.to(d), gelu=gelu)
+    ref, S = reference(x, w, b, "fp4", gelu)
+    assert_linear_close(y, ref, S, "gelu_tanh" if gelu else "none", what=f"K={K}")
+
+
 @pytest.mark.parametrize("act", ["fp4", "fp8"])
 @pytest.mark.parametrize("M,K,N", [(1, 5120, 5136), (16, 4096, 2064), (7, 8256, 4112), (5, 13824, 6160), (11, 8832, 1040),
                                    (9, 8192, 16400)])
