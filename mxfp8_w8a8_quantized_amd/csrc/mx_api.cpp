@@ -953,18 +953,23 @@ uint64_t act_scale_bytes(int act, int64_t R, int64_t K) {
   return act == MX_ACT_FP4 ? fp4_scale_bytes(R, K) : (uint64_t)R * (K / 32);
 }
 
-// The few-token kernel up to 4096 fragments of 16 x 16 outputs (16 in each of
-// 256 workgroups), and up to 8192 (32 each) where K is long; the tiled GEMMs
-// above. Their loops are bound alike by the CUs' load paths; 32 fragments a
-// workgroup make the few-token kernel's end (the waves' sums through LDS)
-// costlier by 2 us. 256 x 5120 x 4096: 8.2 us against 12.5 on tiles (MXFP8
-// activations 10.5 against 16.3); 256 x 5120 x 8192 12.2 against 13.0 (15.0
-// against 16.5), 256 x 3584 x 8192 10.5 against 10.4, 256 x 1024 x 8192 7.1
-// against 5.6.
-constexpr int64_t kFp4FewLongK = 4096;
-bool fp4_few(int64_t M, int64_t K, int64_t N) {
+// Few-token kernel or tiles. Up to 16 tokens both stream the weights, and the
+// few-token kernel takes up to 4096 fragments of 16 x 16 outputs (16 in each of 256
+// workgroups), up to 8192 where K is long. For more tokens its time goes with
+// fp4_few_cost and K; a round of 128 x 128 tiles costs the same whatever the
+// output, with less at short K (us, few-token kernel against tiles; cost): MXFP4
+// 256 x 4096 (10) K = 1024 4.8, 5.3, K = 5120 8.2, 11.1; 200 x 5120 (12) K = 1024 5.5,
+// 5.3, K = 2048 6.2, 6.8; 256 x 6144 (13) K = 2048 7.1, 7.1, K = 5120 10.3, 11.2; 256 x
+// 8192 (15) K = 5120 12.1, 11.6. MXFP8 activations 256 x 4096 (15) K = 512 4.8, 5.0; 200
+// x 5120 (17) K = 512 5.5, 5.0, K = 1024 6.2, 6.3; 256 x 6144 (18) K = 1024 6.9, 6.4, K =
+// 2048 8.6, 9.2; 256 x 8192 (20) K = 2048 10.1, 9.4, K = 5120 14.9, 16.6.
+bool fp4_few(int act, int64_t M, int64_t K, int64_t N) {
   const int64_t fragments = ((M + 15) / 16) * (N / 16);
-  return fragments <= 4096 || (fragments <= 8192 && K > kFp4FewLongK);
+  if (fragments > 8192) return false;
+  if (M <= 16) return fragments <= 4096 || K > 4096;
+  const double cost = mx::fp4_few_cost(act == MX_ACT_FP8, M, N);
+  if (act == MX_ACT_FP8) return cost <= (K >= 4096 ? 20 : K >= 2048 ? 18 : K >= 1024 ? 17 : 15);
+  return cost <= (K >= 4096 ? 13 : K >= 2048 ? 12 : 10);
 }
 
 // bf16 rows are quantized inside the product's kernel, by every workgroup for
@@ -974,7 +979,7 @@ bool fp4_few(int64_t M, int64_t K, int64_t N) {
 constexpr int64_t kFp4RowsMaxTokens = 16;
 constexpr int64_t kFp4RowsMaxElements = 98304;
 bool fp4_rows(int64_t M, int64_t K, int64_t N) {
-  return M <= kFp4RowsMaxTokens && M * K <= kFp4RowsMaxElements && fp4_few(M, K, N);
+  return M <= kFp4RowsMaxTokens && M * K <= kFp4RowsMaxElements && fp4_few(MX_ACT_FP4, M, K, N);
 }
 
 int check_act_k(int act, int64_t K) {
@@ -1008,7 +1013,7 @@ int check_fp4_linear(int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws,
     return fail(MX_ERR_INVALID_ARGUMENT, "codes and y must be 16-byte aligned, scales 4-byte aligned");
   if (bias != nullptr && !aligned(bias, 2)) return fail(MX_ERR_INVALID_ARGUMENT, "bias must be 2-byte aligned");
   const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  if (!fp4_few(M, K, N) && tiles >= kMaxSplitWorkgroups)
+  if (tiles >= kMaxSplitWorkgroups)
     return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
   return MX_OK;
 }
@@ -1124,7 +1129,7 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   if (overlap(y, yb, xq, xb) || overlap(y, yb, xs, sb) || overlaps_fp4_weights(y, yb, K, wq, ws, N, bias))
     return fail(MX_ERR_INVALID_ARGUMENT, "y overlaps an input");
   const hipStream_t hs = (hipStream_t)stream;
-  if (fp4_few(M, K, N)) {
+  if (fp4_few(act, M, K, N)) {
     if ((st = check_device()) != MX_OK) return st;
     (void)hipGetLastError();
     return finish(mx::launch_fp4_linear_few(act == MX_ACT_FP8, xq, xs, M, K, wq, ws, N, bias, epilogue, y, hs),

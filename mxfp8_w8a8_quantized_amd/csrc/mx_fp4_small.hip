@@ -113,16 +113,19 @@ __device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams&
                                           int lane) {
   const int r = lane & 15, G = lane >> 4;
   const bool on = sl < s1;
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.wq + ((int64_t)sl * (p.RN / 16) + n0 / 16) * 1024, on ? WB * 1024 : 0);
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.ws + ((int64_t)sl * p.RN + n0) * 4, on ? WB * 64 : 0);
+  // Tiles need not divide the padded rows.
+  const uint32_t wr = (uint32_t)min((int64_t)16 * WB, p.RN - n0);
+  const uint32_t xr = SRC == SRC_FP4 || SRC == SRC_FP8 ? (uint32_t)min((int64_t)16 * TB, p.RM - m0) : 0u;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.wq + ((int64_t)sl * (p.RN / 16) + n0 / 16) * 1024, on ? wr * 64 : 0u);
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.ws + ((int64_t)sl * p.RN + n0) * 4, on ? wr * 4 : 0u);
 #pragma unroll
   for (int i = 0; i < WB; ++i) s.a[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, lane * 16 + i * 1024, 0, 0);
 #pragma unroll
   for (int i = 0; i < Step<SRC, WB, TB>::NSA; ++i)
     s.sa[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, lane * 4 + i * 256, 0, 0);
   if constexpr (SRC == SRC_FP4) {
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + ((int64_t)sl * (p.RM / 16) + m0 / 16) * 1024, on ? TB * 1024 : 0);
-    const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.xs + ((int64_t)sl * p.RM + m0) * 4, on ? TB * 64 : 0);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + ((int64_t)sl * (p.RM / 16) + m0 / 16) * 1024, on ? xr * 64 : 0u);
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(p.xs + ((int64_t)sl * p.RM + m0) * 4, on ? xr * 4 : 0u);
 #pragma unroll
     for (int j = 0; j < TB; ++j) s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, lane * 16 + j * 1024, 0, 0);
 #pragma unroll
@@ -136,9 +139,9 @@ __device__ __forceinline__ void load_step(Step<SRC, WB, TB>& s, const FewParams&
     const uint8_t* x0 = p.x + (2 * (int64_t)sl * p.RM + m0) * 64;
     const uint8_t* t0 = p.xs + (2 * (int64_t)sl * p.RM + m0) * 2;
     const uint32_t next = (uint32_t)p.RM * 2;  // bytes to the next slab's scales
-    const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(x0, on ? TB * 1024 : 0);
-    const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(x0 + p.RM * 64, two ? TB * 1024 : 0);
-    const __amdgpu_buffer_rsrc_t rt = make_rsrc(t0, two ? next + TB * 32 : on ? TB * 32 : 0);
+    const __amdgpu_buffer_rsrc_t rb0 = make_rsrc(x0, on ? xr * 64 : 0u);
+    const __amdgpu_buffer_rsrc_t rb1 = make_rsrc(x0 + p.RM * 64, two ? xr * 64 : 0u);
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(t0, two ? next + xr * 2 : on ? xr * 2 : 0u);
 #pragma unroll
     for (int j = 0; j < TB; ++j) {
       s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb0, r * 64 + 16 * G + j * 1024, 0, 0);
@@ -302,59 +305,86 @@ hipError_t launch_few(FewParams& p, int epi, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Fragments (16 x 16 outputs) per workgroup: enough that about 256 workgroups
-// or fewer cover the output (one per CU), a power of two.
+// Fragments (16 x 16 outputs) per workgroup for one token fragment: enough that
+// about 256 workgroups or fewer cover the output (one per CU), 1, 2 or 4.
 int fragments(int64_t M, int64_t N) {
   const int64_t total = ((M + 15) / 16) * (N / 16);
   int f = 1;
-  while (f < 32 && f * 256 < total) f *= 2;
+  while (f < 4 && f * 256 < total) f *= 2;
   return f;
 }
 
-// Tile shapes, from sweeps over WB, TB, waves and slabs in flight at N = 1024 ..
-// 15360, K = 4096 .. 14336 and 1 to 256 tokens. Eight waves with one slab in
-// flight are best nearly throughout: a wave's share of K is a handful of slabs,
-// and the other waves hide its latency better than deeper prefetching. At
-// 5120 x 5120: 16 tokens 5.0 us on 32 x 16 tiles (16 x 16: 5.2, 64 x 16: 5.3);
-// 128 tokens 7.7 us on 64 x 64 (128 x 32: 8.3, 32 x 64: 8.3). MXFP8 tokens cost
-// twice their MXFP4 bytes, so their tiles are longer in weight rows: 128 tokens
-// 9.8 us on 128 x 32 (64 x 64: 10.3); 128 x 13824 x 5120 18.4 (20.1). Long rows
-// on the smallest tiles take 16 waves (16 x 14336 x 2048: 6.2 against 7.6 us).
-// Splitting K over workgroups too, with a second kernel adding the parts, was
-// slower at nearly every shape (at best a fifth faster): not kept.
-constexpr int64_t kLongK = 8192;
-
-hipError_t dispatch_fp4(FewParams& p, int epi, hipStream_t st) {
-  const int f = fragments(p.M, p.N);
-  if (f == 1) return p.K >= kLongK ? launch_few<SRC_FP4, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP4, 1, 1, 8, 1>(p, epi, st);
-  if (f == 2) return p.K >= kLongK ? launch_few<SRC_FP4, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP4, 2, 1, 8, 1>(p, epi, st);
-  if (p.M <= 16) return launch_few<SRC_FP4, 4, 1, 8, 1>(p, epi, st);
-  if (f == 4) return launch_few<SRC_FP4, 2, 2, 8, 1>(p, epi, st);
-  if (f == 8 || p.M <= 32) return launch_few<SRC_FP4, 4, 2, 8, 1>(p, epi, st);
-  if (f == 16 || p.M <= 64) return launch_few<SRC_FP4, 4, 4, 8, 1>(p, epi, st);
-  return launch_few<SRC_FP4, 8, 4, 8, 1>(p, epi, st);
+// Tile shapes. A sweep over WB = 1 .. 8, TB = 1 .. 4 (N = 3584 .. 13824, K = 2048 ..
+// 13824, 33 to 200 tokens) has the time go with the loads that a wave issues per
+// slab, codes and scales alike, as long as a CU has one workgroup; each further
+// round of 256 workgroups adds about 0.6 of the first. With MXFP8 activations
+// (us; loads): 128 x 13824 x 5120 on 80 x 32 15.2 (12), 96 x 32 16.8 (13), 128 x 32
+// 18.4 (15), 64 x 64 19.9 (15), 48 x 32 on 428 workgroups 18.6 (9). MXFP4: 128 x 5120
+// x 5120 on 64 x 48 6.9 (9), 64 x 64 7.7 (10), 80 x 32 7.8 (10); 200 x 5120 x 5120 on
+// 80 x 64 9.1 (12), 128 x 64 10.7 (15).
+struct Choice {
+  double cost;  // loads a wave and slab, with the rounds
+  hipError_t (*launch)(FewParams&, int, hipStream_t);
+};
+template <int SRC, int WB, int TB>
+void consider(Choice& c, uint32_t nf, uint32_t mf) {
+  constexpr int loads = WB + (WB + 3) / 4 + (SRC == SRC_FP8 ? 2 * TB + (TB + 1) / 2 : TB + (TB + 3) / 4);
+  const uint64_t groups = (uint64_t)((nf + WB - 1) / WB) * ((mf + TB - 1) / TB);
+  const double cost = loads * (0.4 + 0.6 * (double)((groups + 255) / 256));
+  if (cost < c.cost) c = {cost, &launch_few<SRC, WB, TB, 8, 1>};
+}
+template <int SRC>
+Choice choose(int64_t M, int64_t N) {
+  const uint32_t nf = (uint32_t)(N / 16), mf = (uint32_t)((M + 15) / 16);
+  Choice c{1e300, nullptr};
+  consider<SRC, 1, 1>(c, nf, mf);
+  consider<SRC, 2, 1>(c, nf, mf);
+  consider<SRC, 3, 1>(c, nf, mf);
+  consider<SRC, 4, 1>(c, nf, mf);
+  if constexpr (SRC == SRC_FP8) consider<SRC, 5, 1>(c, nf, mf);
+  consider<SRC, 2, 2>(c, nf, mf);
+  consider<SRC, 3, 2>(c, nf, mf);
+  consider<SRC, 4, 2>(c, nf, mf);
+  consider<SRC, 5, 2>(c, nf, mf);
+  consider<SRC, 7, 2>(c, nf, mf);
+  consider<SRC, 4, 3>(c, nf, mf);
+  consider<SRC, 4, 4>(c, nf, mf);
+  consider<SRC, 5, 4>(c, nf, mf);
+  consider<SRC, 6, 4>(c, nf, mf);
+  // (MXFP4 outputs of these costs are faster on tiles.)
+  if constexpr (SRC == SRC_FP8) consider<SRC, 8, 4>(c, nf, mf);
+  return c;
 }
 
-hipError_t dispatch_fp8(FewParams& p, int epi, hipStream_t st) {
-  const int f = fragments(p.M, p.N);
-  if (f == 1) return p.K >= kLongK ? launch_few<SRC_FP8, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC_FP8, 1, 1, 8, 1>(p, epi, st);
-  // Eight waves are faster by up to 5% on a slab of these (16 x 8192 x 8192: 8.0
-  // against 8.4 us), but slower on bf16 rows (below), and up to 16 tokens both
-  // calls add in the same order.
-  if (f == 2)
-    return p.K >= kLongK && p.M <= 16 ? launch_few<SRC_FP8, 2, 1, 16, 1>(p, epi, st)
-                                      : launch_few<SRC_FP8, 2, 1, 8, 1>(p, epi, st);
-  if (p.M <= 16 || (f == 4 && p.M <= 32)) return launch_few<SRC_FP8, 4, 1, 8, 1>(p, epi, st);
-  if (f == 4) return launch_few<SRC_FP8, 2, 2, 8, 1>(p, epi, st);
-  if (f == 8) return launch_few<SRC_FP8, 4, 2, 8, 1>(p, epi, st);
-  if (f == 16 || p.M <= 32) return launch_few<SRC_FP8, 8, 2, 8, 1>(p, epi, st);
-  return launch_few<SRC_FP8, 8, 4, 8, 1>(p, epi, st);
+// Waves: eight, with one slab in flight each, nearly throughout: a wave's share of
+// K is a handful of slabs, and the other waves hide its latency better than deeper
+// prefetching. Long rows on the smallest tiles take 16 (16 x 14336 x 2048: 6.2
+// against 7.6 us). Splitting K over workgroups too, with a second kernel adding the
+// parts, was slower at nearly every shape (at best a fifth faster): not kept.
+constexpr int64_t kLongK = 8192;
+
+template <int SRC>
+hipError_t dispatch(FewParams& p, int epi, hipStream_t st) {
+  if (p.M <= 16) {
+    // One token fragment. MXFP8, two fragments of weights: eight waves are faster by
+    // up to 5% on a slab (16 x 8192 x 8192: 8.0 against 8.4 us), but slower on bf16
+    // rows (below), and up to 16 tokens both calls add in the same order.
+    const int f = fragments(p.M, p.N);
+    if (f == 1)
+      return p.K >= kLongK ? launch_few<SRC, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
+    if (f == 2)
+      return p.K >= kLongK ? launch_few<SRC, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
+    return launch_few<SRC, 4, 1, 8, 1>(p, epi, st);
+  }
+  const Choice c = choose<SRC>(p.M, p.N);
+  if (c.launch == &launch_few<SRC, 1, 1, 8, 1> && p.K >= kLongK) return launch_few<SRC, 1, 1, 16, 1>(p, epi, st);
+  return c.launch(p, epi, st);
 }
 
 // bf16 rows (at most 16): one token fragment. Rounding keeps a wave longer than
 // its loads, so long rows take 16 waves here too (1 x 13824 x 5120: 10.6 against
 // 11.7 us, to E4M3 13.4 against 15.2). The waves are those of the slab dispatch
-// above, so that both add their sums in the same order.
+// above for as many tokens, so that both add their sums in the same order.
 template <int SRC>
 hipError_t dispatch_rows(FewParams& p, int epi, hipStream_t st) {
   const int f = fragments(p.M, p.N);
@@ -364,6 +394,10 @@ hipError_t dispatch_rows(FewParams& p, int epi, hipStream_t st) {
 }
 
 }  // namespace
+
+double fp4_few_cost(int fp8, int64_t M, int64_t N) {
+  return fp8 ? choose<SRC_FP8>(M, N).cost : choose<SRC_FP4>(M, N).cost;
+}
 
 hipError_t launch_fp4_linear_few(int fp8, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
                                  const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
@@ -381,7 +415,7 @@ hipError_t launch_fp4_linear_few(int fp8, const uint8_t* xq, const uint8_t* xs, 
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  return fp8 ? dispatch_fp8(p, epi, stream) : dispatch_fp4(p, epi, stream);
+  return fp8 ? dispatch<SRC_FP8>(p, epi, stream) : dispatch<SRC_FP4>(p, epi, stream);
 }
 
 hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* wq,

@@ -138,6 +138,10 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
                                   const uint8_t* ws, int64_t N, const void* bias, int epi, void* y,
                                   hipStream_t stream);
 
+// Loads that a wave of the few-token kernel issues per slab on an output of more
+// than 16 tokens, in units of a round of 256 workgroups: what its time goes with.
+double fp4_few_cost(int fp8, int64_t M, int64_t N);
+
 // The tile shape that launch_fp4_linear_tiles should be given for an output.
 void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile);
 

@@ -79,6 +79,28 @@ def test_linear_matches_oracle(M, K, N, act):
     assert same(ys, y)
 
 
+@pytest.mark.parametrize("act,M,K,N", [
+    ("fp4", 17, 96, 2160), ("fp4", 18, 96, 6160), ("fp4", 17, 96, 4160), ("fp4", 17, 96, 8480), ("fp4", 33, 96, 4112),
+    ("fp4", 33, 96, 6304), ("fp4", 34, 96, 8352), ("fp4", 49, 96, 10320), ("fp4", 50, 96, 8224), ("fp4", 65, 2080, 9616),
+    ("fp4", 66, 4128, 10976), ("fp4", 65, 2080, 8240),
+    ("fp8", 17, 64, 2192), ("fp8", 146, 64, 1616), ("fp8", 17, 192, 4240), ("fp8", 17, 192, 8224), ("fp8", 17, 64, 6160),
+    ("fp8", 17, 192, 12368), ("fp8", 33, 64, 10896), ("fp8", 97, 192, 7216), ("fp8", 33, 192, 6464),
+    ("fp8", 33, 64, 8368), ("fp8", 98, 1152, 8224), ("fp8", 65, 2112, 10960), ("fp8", 49, 64, 10352),
+    ("fp8", 65, 4160, 13808),
+])
+def test_every_few_token_tile(act, M, K, N):
+    """Each shape of the few-token kernel's tiles, at sizes that it does not divide."""
+    print(f"fp4 few-token tile M={M} K={K} N={N} {act}", flush=True)
+    d = dev()
+    gelu = M % 2 == 0
+    x = synth.make_activation(M, K, seed=M)
+    w = synth.make_weight(N, K, seed=N) * 4
+    b = synth.make_bias(N, seed=K)
+    y = mx().mx_fp4_linear(x.to(d), mx().mx_fp4_quantize_weight_slab(w.to(d)), b.to(d), gelu=gelu, act=act)
+    ref, S = reference(x, w, b, act, gelu)
+    assert_linear_close(y, ref, S, "gelu_tanh" if gelu else "none", what=f"{M}x{K}x{N} {act}")
+
+
 @pytest.mark.parametrize("K", [96, 256, 352, 512, 640, 736, 896, 1024, 1120, 1920, 2048, 2144, 3168])
 def test_every_remainder_of_steps_on_small_tiles(K):
     """The 128 x 128 tiles run steps of 128 K in blocks of eight: every remainder,
