@@ -969,7 +969,8 @@ def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None
     [M, K] (rows may be strided) is quantized to MXFP4 (act="fp4") or MXFP8
     (act="fp8") and multiplied by the FP4Slab w. workspace: uint8 of at least
     mx_fp4_linear_ws_bytes(M, K, N, act) bytes (allocated here when None and
-    needed; a few tokens need none)."""
+    needed; a few tokens need none); calls that can run at the same time, and
+    graphs that captured them, need one each."""
     fmt = _act_format(act)
     _need_rows(x, "x", _BF16)
     dev = x.device
@@ -1006,7 +1007,7 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
         _need_rows(residual, "residual", _DTYPES, shape, dev)
         rdt, ldr = _DTYPES[residual.dtype], _pitch(residual)
         if residual_out is None:
-            residual_out = residual.new_empty(shape)
+            residual_out = torch.empty_like(residual) if residual.is_contiguous() else residual.new_empty(shape)
             ldo = K
         else:
             _need_rows(residual_out, "residual_out", (residual.dtype,), shape, dev)
