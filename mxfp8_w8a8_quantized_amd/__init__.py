@@ -782,6 +782,11 @@ def _fp4_shapes(rows, K):
     return torch.Size((S, R // 16, 4, 16, 16)), torch.Size((S, R, 4))
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp4_ws_bytes(M, K, N, fmt):
+    return lib().mx_fp4_linear_ws_bytes(M, K, N, fmt)
+
+
 def _fp4_out(rows, K, like, out):
     if out is None:
         sq, ss = _fp4_shapes(rows, K)
@@ -978,7 +983,7 @@ def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None
     y = _fp4_linear_out(M, w, bias, y, dev)
     if w.K != K:
         raise ValueError(f"x has K = {K}, w has K = {w.K}")
-    workspace = _fp4_workspace(workspace, lib().mx_fp4_linear_ws_bytes(M, K, w.rows, fmt), dev)
+    workspace = _fp4_workspace(workspace, _fp4_ws_bytes(M, K, w.rows, fmt), dev)
     _run(lib().mx_fp4_linear, dev, _adr(x), M, K, _pitch(x), _adr(w.q), _adr(w.s), w.rows, _adr(bias),
          MX_EPI_GELU_TANH if gelu else MX_EPI_NONE, fmt, _adr(y), _adr(workspace),
          0 if workspace is None else workspace.numel())
