@@ -1137,10 +1137,10 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   }
   if ((st = check_device()) != MX_OK) return st;
   (void)hipGetLastError();
-  int weight_tile, token_tile;
-  mx::fp4_linear_tile(act == MX_ACT_FP8, M, N, &weight_tile, &token_tile);
-  return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, weight_tile, token_tile, xq, xs, M, K, wq, ws, N, bias,
-                                            epilogue, y, hs),
+  int weight_tile, token_tile, halve;
+  mx::fp4_linear_tile(act == MX_ACT_FP8, M, N, &weight_tile, &token_tile, &halve);
+  return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, weight_tile, token_tile, halve, xq, xs, M, K, wq, ws, N,
+                                            bias, epilogue, y, hs),
                 "MXFP4 linear launch");
 }
 

@@ -62,6 +62,7 @@ struct GemmParams {
   int M, N, nsteps;
   int x_slabs;  // 64-K slabs of MXFP8 tokens (the last step may have one)
   int tiles_m, tiles_n;
+  int whole;  // tiles of their full size, the first in order; the others are halved
 };
 
 template <int B, int E, typename F>
@@ -328,12 +329,11 @@ __device__ __forceinline__ void step(f32x16 (&acc)[IA][JB], Frags<IA, JB, X8>& c
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Workgroup -> (token tile, weight tile): a contiguous range of tiles per XCD,
-// walked in groups of 4 token tiles x all weight tiles (token tile fastest), so
-// that the tiles in flight on an XCD share panels in its L2.
-__device__ inline void tile_coords(uint32_t pid, int tiles_m, int tiles_n, int& tm, int& tn) {
+// Tile `lid` in the order of work -> (token tile, weight tile): groups of 4 token
+// tiles x all weight tiles (token tile fastest), of which each XCD walks a
+// contiguous range, so that the tiles in flight on an XCD share panels in its L2.
+__device__ inline void tile_coords(int lid, int tiles_m, int tiles_n, int& tm, int& tn) {
   constexpr int GM = 4;
-  const int lid = (int)xcd_order(pid, (uint32_t)(tiles_m * tiles_n));
   const int group = lid / (GM * tiles_n);
   const int gm = min(tiles_m - group * GM, GM);
   const int in_group = lid - group * GM * tiles_n;
@@ -384,13 +384,10 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[IA][JB], const Ge
   }
 }
 
+// The tile whose first token is m0 and first weight row n0.
 template <int EPI, int IA, int JB, bool X8>
-__global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+__device__ __forceinline__ void compute_tile(const GemmParams& p, uint8_t* smem, int m0, int n0) {
   using Sh = Shape<IA, JB, X8>;
-  int tm, tn;
-  tile_coords(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-  const int m0 = tm * Sh::MT, n0 = tn * Sh::BN;
   const int rows_m = min(p.M - m0, Sh::MT);
   const int rows_n = min(p.N - n0, Sh::BN);
   const int lane = threadIdx.x & 63;
@@ -472,68 +469,121 @@ __global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
 }
 
 template <int EPI, int IA, int JB, bool X8>
-hipError_t launch(GemmParams p, hipStream_t st) {
+__global__ __launch_bounds__(NT, 1) void fp4_gemm_kernel(GemmParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using Sh = Shape<IA, JB, X8>;
+  int tm, tn;
+  tile_coords((int)xcd_order(blockIdx.x, gridDim.x), p.tiles_m, p.tiles_n, tm, tn);
+  compute_tile<EPI, IA, JB, X8>(p, smem, tm * Sh::MT, tn * Sh::BN);
+}
+
+// Whole rounds of tiles, then the last round's, at most half a round of them, in
+// two halves each: along the tokens where there are 256 (MXFP4), else along the
+// weights. 4001 x 5120 x 5120 with MXFP8 tokens (2.5 rounds) 94.7 to 87.6 us, 2900 x
+// 5120 x 7168 on MXFP4 tiles of 256 x 256 (1.3 rounds) 67.7 to 59.0.
+template <int EPI, int IA, int JB, bool X8>
+__global__ __launch_bounds__(NT, 1) void fp4_gemm_halved_kernel(GemmParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using Sh = Shape<IA, JB, X8>;
+  constexpr int IH = JB == 4 ? IA : IA / 2, JH = JB == 4 ? JB / 2 : JB;
+  int tm, tn;
+  if ((int)blockIdx.x < p.whole) {
+    tile_coords((int)xcd_order(blockIdx.x, (uint32_t)p.whole), p.tiles_m, p.tiles_n, tm, tn);
+    compute_tile<EPI, IA, JB, X8>(p, smem, tm * Sh::MT, tn * Sh::BN);
+  } else {
+    const int r = (int)xcd_order(blockIdx.x - (uint32_t)p.whole, gridDim.x - (uint32_t)p.whole);
+    tile_coords(p.whole + (r >> 1), p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = tm * Sh::MT + (JB == 4 ? (r & 1) * (Sh::MT / 2) : 0);
+    const int n0 = tn * Sh::BN + (JB == 4 ? 0 : (r & 1) * (Sh::BN / 2));
+    if (m0 < p.M && n0 < p.N) compute_tile<EPI, IH, JH, X8>(p, smem, m0, n0);
+  }
+}
+
+template <int EPI, int IA, int JB, bool X8>
+hipError_t launch(GemmParams p, bool halve, hipStream_t st) {
+  using Sh = Shape<IA, JB, X8>;
+  p.tiles_m = (p.M + Sh::MT - 1) / Sh::MT;
+  p.tiles_n = (p.N + Sh::BN - 1) / Sh::BN;
+  const int tiles = p.tiles_m * p.tiles_n;
+  if constexpr (IA == 4 && (JB == 4 || X8)) {
+    if (halve) {
+      static std::atomic<uint64_t> halved_configured{0};  // per instantiation
+      auto kern = fp4_gemm_halved_kernel<EPI, IA, JB, X8>;
+      const hipError_t e = allow_dynamic_lds((const void*)kern, Sh::LDS, halved_configured);
+      if (e != hipSuccess) return e;
+      p.whole = tiles & ~255;
+      hipLaunchKernelGGL(kern, dim3((unsigned)(2 * tiles - p.whole)), dim3(NT), Sh::LDS, st, p);
+      return hipGetLastError();
+    }
+  }
   static std::atomic<uint64_t> configured{0};  // per instantiation
   auto kern = fp4_gemm_kernel<EPI, IA, JB, X8>;
   const hipError_t e = allow_dynamic_lds((const void*)kern, Sh::LDS, configured);
   if (e != hipSuccess) return e;
-  p.tiles_m = (p.M + Sh::MT - 1) / Sh::MT;
-  p.tiles_n = (p.N + Sh::BN - 1) / Sh::BN;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(NT), Sh::LDS, st, p);
+  p.whole = tiles;
+  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(NT), Sh::LDS, st, p);
   return hipGetLastError();
 }
 
 template <int IA, int JB, bool X8>
-hipError_t launch(const GemmParams& p, int epi, hipStream_t st) {
-  return epi == 1 ? launch<1, IA, JB, X8>(p, st) : launch<0, IA, JB, X8>(p, st);
+hipError_t launch(const GemmParams& p, bool halve, int epi, hipStream_t st) {
+  return epi == 1 ? launch<1, IA, JB, X8>(p, halve, st) : launch<0, IA, JB, X8>(p, halve, st);
 }
 
 }  // namespace
 
 // The tile shape for an output: the one whose rounds of workgroups (256, one a
 // CU) take the least time, from the measured time of a round at K = 5120 (us;
-// longer or shorter K scale all shapes about alike). MXFP4 tiles of 128 x 128
-// (mx_fp4_mid.hip) run two a CU: up to 512 a round, and less time up to 256.
-// Checked over 130 to 24000 tokens, 1024 to 16384 outputs and K = 1056 to 12256:
-// the choice was the fastest of the three in 30 of 32 shapes, and 9% slower in the
-// other two. E.g. (us, chosen first): 512 x 5120 128 x 128 12.4, 256 x 128 17.4,
-// 256 x 256 26.3; 1024 x 5120 256 x 128 18.8, 128 x 128 20.6, 256 x 256 26.9; 4001
-// x 5120 128 x 128 59.4, 256 x 128 60.6, 256 x 256 63.7; 3000 x 15360 256 x 256
-// 114, 256 x 128 125, 128 x 128 129. 192-row tiles gain only with MXFP8 tokens:
-// 1024 x 5120 24.5 against 26.8 on 256 x 128 (MXFP4: 18.2 to 20.5 against 19.2).
+// longer or shorter K scale all shapes about alike). A last round of at most 128
+// tiles behind whole ones is run in halves; MXFP4 tiles of 128 x 128 (mx_fp4_mid.hip)
+// run two a CU: up to 512 a round, and less time up to 256. Over 130 to 24000
+// tokens, 1024 to 16384 outputs and K = 1056 to 12256 the choice was the fastest, or
+// within 4% of it, in nearly every shape (at worst 18% slower, at K < 2048). E.g.
+// MXFP4 (us, chosen first): 512 x 5120 128 x 128 12.4, 256 x 128 17.4, 256 x 256 26.3;
+// 1024 x 5120 256 x 128 18.8, 128 x 128 20.6, 256 x 256 26.9; 4001 x 5120 256 x 256
+// halved 58.0, 128 x 128 58.8, 256 x 128 63.6; 3000 x 15360 256 x 256 114, 256 x 128
+// 125, 128 x 128 129. MXFP8 tokens: 1792 x 5120 256 x 128 halved 47.5, 192 x 128 47.3,
+// 128 x 128 52.9; 9000 x 5120 256 x 128 182, 192 x 128 194, 128 x 128 213. 192-row tiles
+// gain only with MXFP8 tokens: 1024 x 5120 24.5 against 26.8 on 256 x 128 (MXFP4: 18.2
+// to 20.5 against 19.2), and so do halves of 256 x 128 (4001 x 5120 MXFP4: 58.3).
 // At one workgroup a CU a tile of 256 x 256 spends 1136 cycles a step, 1120 of
 // them in its MFMAs, one of 256 x 128 660 (560); from a few hundred workgroups the
 // clock falls to what power allows (2.4 to 1.4 GHz), so the shapes' times differ by
 // less than their cycles.
-void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile) {
+void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile, int* halve) {
   struct Tile {
     int weights, tokens;
-    double us, us_pair;  // a round, one and (where they fit) two workgroups a CU
+    double us;       // a round
+    double us_pair;  // two workgroups a CU, where they fit
+    double us_half;  // a round of halved tiles
   };
-  static const Tile fp4_tiles[] = {{256, 256, 32.0, 0.0}, {256, 128, 19.5, 0.0}, {128, 128, 11.6, 21.3}};
-  static const Tile fp8_tiles[] = {{256, 128, 28.0, 0.0}, {192, 128, 24.6, 0.0}, {128, 128, 17.1, 0.0}};
+  static const Tile fp4_tiles[] = {{256, 256, 32.0, 0.0, 19.5}, {256, 128, 19.5, 0.0, 0.0}, {128, 128, 11.6, 21.3, 0.0}};
+  static const Tile fp8_tiles[] = {{256, 128, 28.0, 0.0, 17.1}, {192, 128, 24.6, 0.0, 0.0}, {128, 128, 17.1, 0.0, 0.0}};
   const Tile* t = fp8 ? fp8_tiles : fp4_tiles;
   const int shapes = !fp8 && M > kMidMaxRows ? 2 : 3;
   double best = -1.0;
   for (int i = 0; i < shapes; ++i) {
     const int64_t tiles = (M + t[i].tokens - 1) / t[i].tokens * ((N + t[i].weights - 1) / t[i].weights);
+    const int64_t rest = tiles % 256;
+    const bool half = t[i].us_half > 0.0 && tiles > 256 && rest > 0 && rest <= 128;
     double us;
-    if (t[i].us_pair > 0.0) {
-      const int64_t rest = tiles % 512;
-      us = (double)(tiles / 512) * t[i].us_pair + (rest == 0 ? 0.0 : rest <= 256 ? t[i].us : t[i].us_pair);
-    } else {
+    if (t[i].us_pair > 0.0)
+      us = (double)(tiles / 512) * t[i].us_pair +
+           (tiles % 512 == 0 ? 0.0 : tiles % 512 <= 256 ? t[i].us : t[i].us_pair);
+    else if (half)
+      us = (double)(tiles / 256) * t[i].us + t[i].us_half;
+    else
       us = (double)((tiles + 255) / 256) * t[i].us;
-    }
     if (best < 0.0 || us < best) {
       best = us;
       *weight_tile = t[i].weights;
       *token_tile = t[i].tokens;
+      *halve = half;
     }
   }
 }
 
-hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs,
+hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, int halve, const uint8_t* xq, const uint8_t* xs,
                                    int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
                                    const void* bias, int epi, void* y, hipStream_t stream) {
   if (!fp8 && weight_tile == 128)
@@ -551,13 +601,13 @@ hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, con
   p.N = (int)N;
   p.nsteps = (int)fp4_slabs(K);
   p.x_slabs = (int)(K / 64);
-  p.tiles_m = p.tiles_n = 0;
+  p.tiles_m = p.tiles_n = p.whole = 0;
   if (fp8) {
-    if (weight_tile == 128) return launch<2, 2, true>(p, epi, stream);
-    if (weight_tile == 192) return launch<3, 2, true>(p, epi, stream);
-    return launch<4, 2, true>(p, epi, stream);
+    if (weight_tile == 128) return launch<2, 2, true>(p, false, epi, stream);
+    if (weight_tile == 192) return launch<3, 2, true>(p, false, epi, stream);
+    return launch<4, 2, true>(p, halve, epi, stream);
   }
-  return token_tile == 256 ? launch<4, 4, false>(p, epi, stream) : launch<4, 2, false>(p, epi, stream);
+  return token_tile == 256 ? launch<4, 4, false>(p, halve, epi, stream) : launch<4, 2, false>(p, false, epi, stream);
 }
 
 }  // namespace mx

@@ -143,13 +143,14 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
 double fp4_few_cost(int fp8, int64_t M, int64_t N);
 
 // The tile shape that launch_fp4_linear_tiles should be given for an output.
-void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile);
+void fp4_linear_tile(int fp8, int64_t M, int64_t N, int* weight_tile, int* token_tile, int* halve);
 
 // MXFP4-weight linear on tiles of 256, 128 or (MXFP8 tokens) 192 weight rows x
-// 128 tokens, or (MXFP4 tokens) 256 x 256; N % 16 == 0, tiles below 2^24.
-hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, const uint8_t* xq, const uint8_t* xs,
-                                   int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N,
-                                   const void* bias, int epi, void* y, hipStream_t stream);
+// 128 tokens, or (MXFP4 tokens) 256 x 256; N % 16 == 0, tiles below 2^24. halve:
+// the tiles past the last whole round of 256 in two halves (256 weight rows only).
+hipError_t launch_fp4_linear_tiles(int fp8, int weight_tile, int token_tile, int halve, const uint8_t* xq,
+                                   const uint8_t* xs, int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws,
+                                   int64_t N, const void* bias, int epi, void* y, hipStream_t stream);
 
 // MXFP4 weights and tokens on tiles of 128 x 128 (mx_fp4_mid.hip); the same
 // limits, and M <= kMidMaxRows (32-bit offsets between slabs of scales).

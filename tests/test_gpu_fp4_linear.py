@@ -101,6 +101,27 @@ def test_every_few_token_tile(act, M, K, N):
     assert_linear_close(y, ref, S, "gelu_tanh" if gelu else "none", what=f"{M}x{K}x{N} {act}")
 
 
+@pytest.mark.parametrize("act,M,K,N", [
+    ("fp4", 2310, 96, 7184), ("fp4", 2561, 416, 7184), ("fp4", 4400, 160, 4112), ("fp4", 8300, 672, 2320),
+    ("fp8", 1100, 192, 8208), ("fp8", 1281, 448, 7440), ("fp8", 2100, 64, 5136), ("fp8", 6000, 320, 2832),
+])
+def test_halved_last_round(act, M, K, N):
+    """A last round of at most half the tiles behind whole ones runs in halves:
+    halves that are empty or ragged, one whole round and two."""
+    print(f"fp4 halved M={M} K={K} N={N} {act}", flush=True)
+    d = dev()
+    gelu = M % 4 == 0
+    x = synth.make_activation(M, K, seed=M)
+    w = synth.make_weight(N, K, seed=N) * 4
+    b = synth.make_bias(N, seed=K)
+    yb = torch.full((M * N + 4096,), -1, dtype=torch.int16, device=d)
+    y = yb[: M * N].view(torch.bfloat16).view(M, N)
+    mx().mx_fp4_linear(x.to(d), mx().mx_fp4_quantize_weight_slab(w.to(d)), b.to(d), gelu=gelu, act=act, y=y)
+    assert bool((yb[M * N :] == -1).all()) and not bool((yb[: M * N] == -1).any())
+    ref, S = reference(x, w, b, act, gelu)
+    assert_linear_close(y, ref, S, "gelu_tanh" if gelu else "none", what=f"{M}x{K}x{N} {act}")
+
+
 @pytest.mark.parametrize("K", [96, 256, 352, 512, 640, 736, 896, 1024, 1120, 1920, 2048, 2144, 3168])
 def test_every_remainder_of_steps_on_small_tiles(K):
     """The 128 x 128 tiles run steps of 128 K in blocks of eight: every remainder,
