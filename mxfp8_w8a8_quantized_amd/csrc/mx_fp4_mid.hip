@@ -13,7 +13,7 @@
 //     in and 32 KB out a step. Four loads a wave and step, each of 1 KB.
 //   - The scales of four steps come in one load, into a ring in LDS (a load for
 //     each operand and step took 90 cycles).
-//   - 80 KB of LDS and 213 registers let two workgroups share a CU: 512 tiles run
+//   - 80 KB of LDS and 215 registers let two workgroups share a CU: 512 tiles run
 //     in 21.3 us at K = 5120, 256 in 11.6 (25.6 and 12.6 before; a round of
 //     workgroups is bound by power as well, at 1.5 GHz with two a CU).
 //
