@@ -779,7 +779,7 @@ class FP4Slab(NamedTuple):
 @functools.lru_cache(maxsize=4096)
 def _fp4_shapes(rows, K):
     S, R = (K + 127) // 128, (rows + 255) // 256 * 256
-    return torch.Size((S, R // 16, 4, 16, 16)), torch.Size((S, R, 4))
+    return (S, R // 16, 4, 16, 16), (S, R, 4)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -884,8 +884,9 @@ def mx_fp4_dequantize_slab(slab, y=None, dtype=torch.bfloat16):
     if y is None:
         if dtype not in _DTYPES:
             raise TypeError("dtype must be bfloat16 or float32")
-        y = torch.empty((slab.rows, slab.K), dtype=dtype, device=dev)
-    _need_rows(y, "y", _DTYPES, (slab.rows, slab.K), dev)
+        y = slab.q.new_empty((slab.rows, slab.K), dtype=dtype)
+    else:
+        _need_rows(y, "y", _DTYPES, (slab.rows, slab.K), dev)
     _run(lib().mx_fp4_dequantize_slab, dev, _adr(slab.q), _adr(slab.s), slab.rows, slab.K, _adr(y), _DTYPES[y.dtype],
          _pitch(y))
     return y
@@ -926,7 +927,7 @@ def _fp4_linear_out(M, w, bias, y, dev):
         if bias.shape != (N,):
             raise ValueError("bias must be f16 [N]")
     if y is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        return w.q.new_empty((M, N), dtype=torch.bfloat16)
     _need(y, "y", torch.bfloat16, dev)
     if y.shape != (M, N):
         raise ValueError("y must be bf16 [M, N]")
