@@ -16,6 +16,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmxfp8.so")
 
+MX_ABI_VERSION = 12
 MX_OK = 0
 MX_ERR_INVALID_ARGUMENT = 1
 MX_ERR_UNSUPPORTED = 2
@@ -103,12 +104,19 @@ _lib = None
 
 
 def lib():
-    """The loaded library (raises if it has not been built)."""
+    """The loaded library (raises if it has not been built, or if it was built
+    from other sources: another ABI version, or a call missing)."""
     global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise MXError(-1, f"{LIB_PATH} is not built; run __graft_entry__.build()")
         handle = ctypes.CDLL(LIB_PATH)
+        missing = [name for name in SIGNATURES if not hasattr(handle, name)]
+        if missing:
+            raise MXError(-1, f"{LIB_PATH} is out of date (no {missing[0]}); run __graft_entry__.build()")
+        if handle.mx_abi_version() != MX_ABI_VERSION:
+            raise MXError(-1, f"{LIB_PATH} is out of date (ABI version {handle.mx_abi_version()}, not "
+                              f"{MX_ABI_VERSION}); run __graft_entry__.build()")
         for name, (args, res) in SIGNATURES.items():
             fn = getattr(handle, name)
             fn.argtypes = args
