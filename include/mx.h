@@ -582,6 +582,15 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
  * mx_fp4_linear_ws_bytes is 0 where none is needed, -1 on a bad shape or format.
  * Nothing is allocated. */
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act);
+
+/* The kernel that both linears take for a shape: tiles of *weight_rows x
+ * *tokens, 0 x 0 for the few-token kernel, and *halved = 1 where the last
+ * round's tiles run in halves. A token's sums are added in the same order at
+ * every M that gives tiles, of whatever shape; the few-token kernel's order
+ * goes with its own tiles. Host only. MX_ERR_INVALID_ARGUMENT on a NULL
+ * pointer; other errors as the linears' for the shape and format. M = 0 or N =
+ * 0 gives 0, 0, 0. */
+int mx_fp4_linear_tile(int64_t M, int64_t K, int64_t N, int act, int* weight_rows, int* tokens, int* halved);
 int mx_fp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx,
                   const uint8_t* wq, const uint8_t* ws, int64_t N,
                   const void* bias, int epilogue, int act, void* y,

@@ -88,6 +88,7 @@ SIGNATURES = {
     "mx_fp4_slab_unpack": ([_P, _P, _I64, _I64, _P, _P, _P], _INT),
     "mx_fp4_linear_slab": ([_INT, _P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P], _INT),
     "mx_fp4_linear_ws_bytes": ([_I64, _I64, _I64, _INT], _I64),
+    "mx_fp4_linear_tile": ([_I64, _I64, _I64, _INT, _PI, _PI, _PI], _INT),
     "mx_fp4_linear": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _P], _INT),
     "mx_rmsnorm_slab": ([_P, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P,
                          _P, _P], _INT),
@@ -976,6 +977,14 @@ def mx_fp4_linear_slab(x, w, bias=None, gelu=False, y=None):
 
 def mx_fp4_linear_ws_bytes(M, K, N, act="fp4"):
     return lib().mx_fp4_linear_ws_bytes(M, K, N, _act_format(act))
+
+
+def mx_fp4_linear_tile(M, K, N, act="fp4"):
+    """(weight rows, tokens, halved): the tiles on which mx_fp4_linear and
+    mx_fp4_linear_slab compute a shape, (0, 0, False) for the few-token kernel."""
+    w, t, h = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    _check(lib().mx_fp4_linear_tile(M, K, N, _act_format(act), ctypes.byref(w), ctypes.byref(t), ctypes.byref(h)))
+    return w.value, t.value, bool(h.value)
 
 
 def mx_fp4_linear(x, w, bias=None, gelu=False, act="fp4", y=None, workspace=None):

@@ -996,25 +996,32 @@ bool bad_fp4_shape(int64_t M, int64_t K, int64_t N, int act) {
          (act != MX_ACT_FP8 && act != MX_ACT_FP4) || (act == MX_ACT_FP8 && K % 64 != 0);
 }
 
-// Everything of an MXFP4-weight linear but its token operand.
-int check_fp4_linear(int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias,
-                     int epilogue, int act, const void* y) {
+int check_fp4_linear_shape(int64_t M, int64_t K, int64_t N, int act) {
   int st;
   if ((st = check_rows("M", M)) != MX_OK) return st;
   if ((st = check_act_k(act, K)) != MX_OK) return st;
   if (N < 0) return fail(MX_ERR_INVALID_ARGUMENT, "N = %lld is negative", (long long)N);
   if (N > kMaxKN) return fail(MX_ERR_UNSUPPORTED, "N = %lld exceeds the supported 2^20", (long long)N);
+  if (M == 0 || N == 0) return MX_OK;
+  if (N % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "N = %lld must be a multiple of 16", (long long)N);
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  if (tiles >= kMaxSplitWorkgroups)
+    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
+  return MX_OK;
+}
+
+// Everything of an MXFP4-weight linear but its token operand.
+int check_fp4_linear(int64_t M, int64_t K, const uint8_t* wq, const uint8_t* ws, int64_t N, const void* bias,
+                     int epilogue, int act, const void* y) {
+  const int st = check_fp4_linear_shape(M, K, N, act);
+  if (st != MX_OK) return st;
   if (epilogue != MX_EPI_NONE && epilogue != MX_EPI_GELU_TANH)
     return fail(MX_ERR_INVALID_ARGUMENT, "unknown epilogue %d", epilogue);
   if (M == 0 || N == 0) return MX_OK;
-  if (N % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "N = %lld must be a multiple of 16", (long long)N);
   if (wq == nullptr || ws == nullptr || y == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL weight or output pointer");
   if (!aligned(wq, 16) || !aligned(y, 16) || !aligned(ws, 4))
     return fail(MX_ERR_INVALID_ARGUMENT, "codes and y must be 16-byte aligned, scales 4-byte aligned");
   if (bias != nullptr && !aligned(bias, 2)) return fail(MX_ERR_INVALID_ARGUMENT, "bias must be 2-byte aligned");
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-  if (tiles >= kMaxSplitWorkgroups)
-    return fail(MX_ERR_UNSUPPORTED, "%lld tiles of 128 x 128 exceed 2^24", (long long)tiles);
   return MX_OK;
 }
 
@@ -1142,6 +1149,17 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
   return finish(mx::launch_fp4_linear_tiles(act == MX_ACT_FP8, weight_tile, token_tile, halve, xq, xs, M, K, wq, ws, N,
                                             bias, epilogue, y, hs),
                 "MXFP4 linear launch");
+}
+
+int mx_fp4_linear_tile(int64_t M, int64_t K, int64_t N, int act, int* weight_rows, int* tokens, int* halved) {
+  if (weight_rows == nullptr || tokens == nullptr || halved == nullptr)
+    return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  const int st = check_fp4_linear_shape(M, K, N, act);
+  if (st != MX_OK) return st;
+  *weight_rows = *tokens = *halved = 0;
+  if (M > 0 && N > 0 && !fp4_few(act, M, K, N))
+    mx::fp4_linear_tile(act == MX_ACT_FP8, M, N, weight_rows, tokens, halved);
+  return MX_OK;
 }
 
 int64_t mx_fp4_linear_ws_bytes(int64_t M, int64_t K, int64_t N, int act) {
