@@ -563,8 +563,8 @@ int mx_fp4_slab_unpack(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t
  * with xhat the values of an MXFP4 or MXFP8 activation slab (act), what those
  * of the MXFP4 weight slab wq, ws (R = mx_slab_rows(N)). Products are exact,
  * sums FP32. bias f16 [N] or NULL; y bf16 [M][N]; N % 16 == 0 (else
- * MX_ERR_UNSUPPORTED). Codes and y 16-byte aligned, scales 4-byte aligned; y
- * must not overlap an input. One kernel, chosen by the shape and the format
+ * MX_ERR_UNSUPPORTED). Codes and y 16-byte aligned, scales 4-byte aligned, the
+ * bias 2-byte aligned; y must not overlap an input. One kernel, chosen by the shape and the format
  * alone, so results are deterministic. Fewer than 2^24 tiles of 128 x 128
  * (else MX_ERR_UNSUPPORTED). */
 int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,

@@ -410,11 +410,19 @@ __device__ __forceinline__ void compute_tile(const GemmParams& p, uint8_t* smem,
 
   // Bias: the f16 values of the wave's weight rows into its slot, ahead of the
   // ring's first loads (columns past N read what the load leaves there; their
-  // outputs are not stored).
+  // outputs are not stored). The DMA moves dwords, from 4-byte aligned addresses;
+  // n0 is even, so the tensor's own address says whether they are. Halves are
+  // loaded one by one otherwise, which waits for them here.
   uint8_t* slot = smem + Sh::BIAS + wave * 256;
   if (p.bias != nullptr) {
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.bias + n0, (uint32_t)rows_n * 2u);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 64 * IA, 0, 0);
+    if (((uintptr_t)p.bias & 2) == 0) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 64 * IA, 0, 0);
+    } else {
+      const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, lane * 4, wn * 64 * IA, 0);
+      const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, lane * 4 + 2, wn * 64 * IA, 0);
+      *(uint32_t*)(slot + lane * 4) = lo | (hi << 16);
+    }
   } else {
     *(int*)(slot + lane * 4) = 0;
   }
