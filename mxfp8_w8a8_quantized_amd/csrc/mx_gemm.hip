@@ -1153,7 +1153,9 @@ constexpr int LDS_PC = PC_TABLE + 2048;
 // load latency; the per-channel output, whose bias follows the row scales,
 // reads its slot in the epilogue. Before: the epilogue waited a memory round
 // trip for the bias after the last MFMA (0.85 us of a 61 us tile at
-// 75348 x 5120 x 15360). Without a bias the slot is zeroed with ordinary LDS
+// 75348 x 5120 x 15360). The DMA moves dwords, from 4-byte aligned addresses;
+// a bias that is only 2-byte aligned is loaded by halves, which waits for them
+// ahead of the ring's loads. Without a bias the slot is zeroed with ordinary LDS
 // writes. Columns past N (a ragged last weight tile) read whatever the DMA
 // leaves there; their outputs are not stored.
 constexpr int BIAS_TABLE = LDS_PC;
@@ -1167,7 +1169,13 @@ __device__ __forceinline__ void issue_bias_slot(const Params& p, uint8_t* smem, 
   uint8_t* slot = smem + BIAS_TABLE + wave * 256;
   if (p.bias != nullptr) {
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.bias + n0, (uint32_t)rows_n * 2u);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 256, 0, 0);
+    if (((uintptr_t)p.bias & 2) == 0) {  // n0 is even
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)slot, 4, lane * 4, wn * 256, 0, 0);
+    } else {
+      const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, lane * 4, wn * 256, 0);
+      const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, lane * 4 + 2, wn * 256, 0);
+      *(uint32_t*)(slot + lane * 4) = lo | (hi << 16);
+    }
   } else {
     *(int*)(slot + lane * 4) = 0;
   }

@@ -53,3 +53,42 @@ def test_mxfp4_linears(act, M, N, tile):
     assert bool(((y - plain).float() - b.float()).abs().max() < 0.5)
     for v in shifted:
         assert same(mx().mx_fp4_linear(x, w, v, act=act), y)
+
+
+@pytest.mark.parametrize("M,N", [(300, 272), (520, 784)])
+@pytest.mark.parametrize("kind", ["slab", "m128", "splitk", "small", "small split", "balanced", "requant", "per channel",
+                                  "row-major", "row-major, K % 128 = 64", "fused", "one call"])
+def test_mxfp8_linears(kind, M, N):
+    print(f"bias alignment {kind} M={M} N={N}", flush=True)
+    m = mx()
+    K = 320 if kind == "row-major, K % 128 = 64" else 512
+    if kind == "requant":
+        N = N // 64 * 64
+    x = synth.make_activation(M, K, seed=M).to(dev())
+    w = synth.make_weight(N, K, seed=N).to(dev())
+    xs, ws = m.mx_quantize_act_slab(x), m.mx_quantize_weight_slab(w)
+    xr, wr = m.mx_quantize_act(x), m.mx_quantize_weight(w)
+    xp, wp = m.mx_pc_quantize_act_slab(x), m.mx_pc_quantize_weight_slab(w)
+
+    def run(b):
+        if kind == "requant":
+            out = m.mx_linear_slab_requant(xs, ws, b)
+            return torch.cat([out.q.reshape(-1), out.s.reshape(-1)])
+        y = {
+            "slab": lambda: m.mx_linear_slab(xs, ws, b),
+            "m128": lambda: m.mx_linear_slab_m128(xs, ws, b),
+            "splitk": lambda: m.mx_linear_slab_splitk(xs, ws, b, splits=2),
+            "small": lambda: m.mx_linear_slab_small(xs, ws, b, splits=1),
+            "small split": lambda: m.mx_linear_slab_small(xs, ws, b, splits=2),
+            "balanced": lambda: m.mx_linear_slab_balanced(xs, ws, b),
+            "per channel": lambda: m.mx_pc_linear_slab(xp, wp, b),
+            "fused": lambda: m.mx_linear_fused(x, *wr, b),
+            "one call": lambda: m.mx_linear(x, ws, b),
+        }.get(kind, lambda: m.mx_linear_q(*xr, *wr, b))()
+        return y.view(torch.int16)
+
+    b, shifted = biases(N, M + N)
+    y = run(b)
+    assert not torch.equal(y, run(None))
+    for v in shifted:
+        assert torch.equal(run(v), y)
