@@ -1418,7 +1418,10 @@ hipError_t launch_linear(const void* x, const uint8_t* xs, int64_t M, int64_t K,
   p.tiles_n = (int)((N + BN - 1) / BN);
   const int nwg = p.tiles_m * p.tiles_n;
   const bool ktail = (K % BK) != 0;
-  if (xs != nullptr && !ktail)
+  // The eight-wave pipeline moves a row's four scales of a step as a dword, from
+  // 4-byte aligned addresses; scales at other ones are loaded byte by byte.
+  const bool dwords = (((uintptr_t)xs | (uintptr_t)ws) & 3) == 0;
+  if (xs != nullptr && !ktail && dwords)
     return epi == 1 ? pp::launch<1>(p, nwg, stream) : pp::launch<0>(p, nwg, stream);
   return xs == nullptr ? dispatch_epi<true>(p, ktail, epi, nwg, stream)
                        : dispatch_epi<false>(p, ktail, epi, nwg, stream);
