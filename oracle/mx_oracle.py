@@ -183,10 +183,12 @@ def bf16_ulp(y):
 
 def bf16_round(v):
     """Round float64 values to the nearest bfloat16, ties to even; values
-    past the rounding boundary of the largest bf16 become +-inf."""
+    past the rounding boundary of the largest bf16 become +-inf, which stay
+    what they are."""
     v = np.asarray(v, dtype=np.float64)
     q = bf16_ulp(v)
-    r = np.round(v / q) * q  # numpy rounds halves to even
+    with np.errstate(invalid="ignore"):
+        r = np.where(np.isinf(v), v, np.round(v / q) * q)  # numpy rounds halves to even
     big = np.abs(r) > np.ldexp(2.0 - 2.0**-7, 127)
     return np.where(big, np.copysign(np.inf, v), r)
 
