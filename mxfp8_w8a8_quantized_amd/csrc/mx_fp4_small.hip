@@ -4,9 +4,9 @@
 //
 // Bound by the weights' bytes (N K / 2, read once from HBM) for a few tokens,
 // and by the token operand's re-reads from the L2 (once per weight tile) for
-// hundreds. A workgroup of 8 waves takes 16 WB weight rows and 16 TB tokens;
-// its waves split K among themselves and add their partial sums in LDS in
-// wave order, so there is one launch, no workspace and no dependence on
+// hundreds. A workgroup of 8 waves, or 16 on long rows, takes 16 WB weight rows
+// and 16 TB tokens; its waves split K among themselves and add their partial sums
+// in LDS in wave order, so there is one launch, no workspace and no dependence on
 // timing, and N / (16 WB) workgroups are enough to fill the GPU.
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4, weights as the A operand (found on the
@@ -232,12 +232,12 @@ __device__ __forceinline__ void mma_step(f32x4 (&acc)[WB][TB], const Step<SRC, W
   });
 }
 
-// NW waves; D slabs in flight per wave. The partial sums go through LDS in
+// NW waves, each with one slab in flight. The partial sums go through LDS in
 // rounds of at most kRound fragments, so that they take at most kRound KB per
 // wave of it.
 constexpr int kRound = 8;
 
-template <int SRC, int WB, int TB, int NW, int D, int EPI>
+template <int SRC, int WB, int TB, int NW, int EPI>
 __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(FewParams p) {
   constexpr int NF = WB * TB, C = NF < kRound ? NF : kRound;
   __shared__ f32x4 sums[NW][C][64];
@@ -255,15 +255,11 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(FewParams p) {
   for (int i = 0; i < WB; ++i)
 #pragma unroll
     for (int j = 0; j < TB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  Step<SRC, WB, TB> st[D];
-#pragma unroll
-  for (int u = 0; u < D; ++u) load_step(st[u], p, s0 + u, s1, n0, m0, lane);
-  for (int s = s0; s < s1; s += D) {
-#pragma unroll
-    for (int u = 0; u < D; ++u) {
-      mma_step(acc, st[u], lane);
-      load_step(st[u], p, s + u + D, s1, n0, m0, lane);
-    }
+  Step<SRC, WB, TB> st;
+  load_step(st, p, s0, s1, n0, m0, lane);
+  for (int s = s0; s < s1; ++s) {
+    mma_step(acc, st, lane);
+    load_step(st, p, s + 1, s1, n0, m0, lane);
   }
 #pragma unroll
   for (int f0 = 0; f0 < NF; f0 += C) {
@@ -294,14 +290,14 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(FewParams p) {
   }
 }
 
-template <int SRC, int WB, int TB, int NW, int D>
+template <int SRC, int WB, int TB, int NW>
 hipError_t launch_few(FewParams& p, int epi, hipStream_t st) {
   p.tiles_m = (p.M + 16 * TB - 1) / (16 * TB);
   const unsigned blocks = (unsigned)(p.tiles_m * ((p.N + 16 * WB - 1) / (16 * WB)));
   if (epi == 1)
-    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, D, 1>), dim3(blocks), dim3(64 * NW), 0, st, p);
+    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, 1>), dim3(blocks), dim3(64 * NW), 0, st, p);
   else
-    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, D, 0>), dim3(blocks), dim3(64 * NW), 0, st, p);
+    hipLaunchKernelGGL((fp4_few_kernel<SRC, WB, TB, NW, 0>), dim3(blocks), dim3(64 * NW), 0, st, p);
   return hipGetLastError();
 }
 
@@ -331,7 +327,7 @@ void consider(Choice& c, uint32_t nf, uint32_t mf) {
   constexpr int loads = WB + (WB + 3) / 4 + (SRC == SRC_FP8 ? 2 * TB + (TB + 1) / 2 : TB + (TB + 3) / 4);
   const uint64_t groups = (uint64_t)((nf + WB - 1) / WB) * ((mf + TB - 1) / TB);
   const double cost = loads * (0.4 + 0.6 * (double)((groups + 255) / 256));
-  if (cost < c.cost) c = {cost, &launch_few<SRC, WB, TB, 8, 1>};
+  if (cost < c.cost) c = {cost, &launch_few<SRC, WB, TB, 8>};
 }
 template <int SRC>
 Choice choose(int64_t M, int64_t N) {
@@ -356,41 +352,31 @@ Choice choose(int64_t M, int64_t N) {
   return c;
 }
 
-// Waves: eight, with one slab in flight each, nearly throughout: a wave's share of
-// K is a handful of slabs, and the other waves hide its latency better than deeper
-// prefetching. Long rows on the smallest tiles take 16 (16 x 14336 x 2048: 6.2
-// against 7.6 us). Splitting K over workgroups too, with a second kernel adding the
-// parts, was slower at nearly every shape (at best a fifth faster): not kept.
+// Waves: eight; long rows on the smallest tiles take 16 (16 x 14336 x 2048: 6.2
+// against 7.6 us). Not measured: more than one slab in flight a wave, and 16 waves
+// on the larger tiles. Splitting K over workgroups too, with a second kernel adding
+// the parts, was slower at nearly every shape (at best a fifth faster): not kept.
 constexpr int64_t kLongK = 8192;
+
+// Up to 16 tokens: one token fragment. Slab operands and bf16 rows take the same
+// tiles and waves, so that both add their sums in the same order. 16 waves on long
+// rows: rounding keeps a wave longer than its loads on bf16 rows (1 x 13824 x 5120:
+// 10.6 against 11.7 us, to E4M3 13.4 against 15.2); with two fragments of weights
+// an MXFP8 slab is faster on eight by up to 5% (16 x 8192 x 8192: 8.0 against 8.4).
+template <int SRC>
+hipError_t dispatch16(FewParams& p, int epi, hipStream_t st) {
+  const int f = fragments(p.M, p.N);
+  if (f == 1) return p.K >= kLongK ? launch_few<SRC, 1, 1, 16>(p, epi, st) : launch_few<SRC, 1, 1, 8>(p, epi, st);
+  if (f == 2) return p.K >= kLongK ? launch_few<SRC, 2, 1, 16>(p, epi, st) : launch_few<SRC, 2, 1, 8>(p, epi, st);
+  return launch_few<SRC, 4, 1, 8>(p, epi, st);
+}
 
 template <int SRC>
 hipError_t dispatch(FewParams& p, int epi, hipStream_t st) {
-  if (p.M <= 16) {
-    // One token fragment. MXFP8, two fragments of weights: eight waves are faster by
-    // up to 5% on a slab (16 x 8192 x 8192: 8.0 against 8.4 us), but slower on bf16
-    // rows (below), and up to 16 tokens both calls add in the same order.
-    const int f = fragments(p.M, p.N);
-    if (f == 1)
-      return p.K >= kLongK ? launch_few<SRC, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
-    if (f == 2)
-      return p.K >= kLongK ? launch_few<SRC, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
-    return launch_few<SRC, 4, 1, 8, 1>(p, epi, st);
-  }
+  if (p.M <= 16) return dispatch16<SRC>(p, epi, st);
   const Choice c = choose<SRC>(p.M, p.N);
-  if (c.launch == &launch_few<SRC, 1, 1, 8, 1> && p.K >= kLongK) return launch_few<SRC, 1, 1, 16, 1>(p, epi, st);
+  if (c.launch == &launch_few<SRC, 1, 1, 8> && p.K >= kLongK) return launch_few<SRC, 1, 1, 16>(p, epi, st);
   return c.launch(p, epi, st);
-}
-
-// bf16 rows (at most 16): one token fragment. Rounding keeps a wave longer than
-// its loads, so long rows take 16 waves here too (1 x 13824 x 5120: 10.6 against
-// 11.7 us, to E4M3 13.4 against 15.2). The waves are those of the slab dispatch
-// above for as many tokens, so that both add their sums in the same order.
-template <int SRC>
-hipError_t dispatch_rows(FewParams& p, int epi, hipStream_t st) {
-  const int f = fragments(p.M, p.N);
-  if (f == 1) return p.K >= kLongK ? launch_few<SRC, 1, 1, 16, 1>(p, epi, st) : launch_few<SRC, 1, 1, 8, 1>(p, epi, st);
-  if (f == 2) return p.K >= kLongK ? launch_few<SRC, 2, 1, 16, 1>(p, epi, st) : launch_few<SRC, 2, 1, 8, 1>(p, epi, st);
-  return launch_few<SRC, 4, 1, 8, 1>(p, epi, st);
 }
 
 }  // namespace
@@ -434,7 +420,7 @@ hipError_t launch_fp4_linear_rows(int fp8, const void* x, int64_t M, int64_t K, 
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  return fp8 ? dispatch_rows<SRC_BF16_FP8>(p, epi, stream) : dispatch_rows<SRC_BF16_FP4>(p, epi, stream);
+  return fp8 ? dispatch16<SRC_BF16_FP8>(p, epi, stream) : dispatch16<SRC_BF16_FP4>(p, epi, stream);
 }
 
 }  // namespace mx
