@@ -6,13 +6,13 @@
 // nothing else in the loop), so what bounds it is the issue of everything else by
 // the one wave of each SIMD, and loads cost most: about 25 cycles each, whatever
 // their size. On four waves of 64 x 64 with both operands in LDS, as in
-// mx_fp4_gemm.hip, a step takes 485 cycles; here 370:
+// mx_fp4_gemm.hip, a step takes 485 cycles; here 400:
 //   - The four waves split the weight rows only, 32 each, and load their
 //     fragments from memory straight into registers (a 16-row block of a slab is
 //     in fragment order); the tokens, which all four share, go through LDS: 8 KB
 //     in and 32 KB out a step. Four loads a wave and step, each of 1 KB.
-//   - The scales of four steps come in one load, into a ring in LDS (a load for
-//     each operand and step took 90 cycles).
+//   - The scales of four steps come in one load, into a ring in LDS (with a load
+//     for each operand and step, a step takes 454 cycles).
 //   - 80 KB of LDS and 215 registers let two workgroups share a CU: 512 tiles run
 //     in 21.3 us at K = 5120, 256 in 11.6 (25.6 and 12.6 before; a round of
 //     workgroups is bound by power as well, at 1.5 GHz with two a CU).

@@ -302,7 +302,12 @@ hipError_t launch_few(FewParams& p, int epi, hipStream_t st) {
 }
 
 // Fragments (16 x 16 outputs) per workgroup for one token fragment: enough that
-// about 256 workgroups or fewer cover the output (one per CU), 1, 2 or 4.
+// about 256 workgroups or fewer cover the output (one per CU), 1, 2 or 4. Weights
+// from HBM, K = 5120 (us on 1, 2 and 4 fragments): one token on an MXFP4 slab, N =
+// 4096 5.8, 6.0, 7.1; 5120 6.6, 6.1, 7.2; 8192 7.0, 6.4, 7.5; 13824 11.6, 9.8, 9.4;
+// 16 bf16 rows to MXFP4, which every workgroup rounds for itself, N = 4096 8.7, 9.8,
+// 12.0; 5120 16.3, 9.9, 12.1; 13824 30.5, 19.3, 13.0. So two workgroups a CU do not
+// pay, though one round of them leaves CUs idle (160 workgroups at N = 5120).
 int fragments(int64_t M, int64_t N) {
   const int64_t total = ((M + 15) / 16) * (N / 16);
   int f = 1;

@@ -332,10 +332,23 @@ hipError_t launch_row(const NormParams& p, hipStream_t st) {
 
 // Rows from which the tiled form is taken. Its blocks take eight rows each and
 // their stores are whole lines, but a wave waits for its whole row; the row form
-// spreads a row over 4 or 8 waves. bf16 residual, MXFP8 (us, tiled against row
-// form): 2048 x 2048 8.1, 9.5; 8192 x 2048 22.4, 26.1; 75348 x 2048 209, 233; 8192
-// x 4096 45.6, 39.6; 16384 x 8192 226, 204; 40000 x 5120 286, 311; 75348 x 5120
-// 521 (5.2 TB/s), 624; 75348 x 8192 950, 1059.
+// spreads a row over 4 or 8 waves. us, tiled against row form, to MXFP8:
+//                  no residual    bf16 residual          f32 residual
+//   1024 x 2048    5.6, 4.9       6.8, 5.8               7.9, 6.5
+//   2048 x 2048    5.9, 7.4       8.0, 9.3               11.0, 10.8
+//   8192 x 2048    14.6, 22.6     22.4, 25.6             34.0, 31.3
+//   75348 x 2048   110, 207       210, 233               322, 333
+//   8192 x 4096    29.0, 28.0     46.1, 40.9             94.1, 78.4
+//   32768 x 4096   99, 119        191, 197               317, 303
+//   75348 x 4096   212, 266       426, 481               698, 737
+//   32768 x 5120   122, 152       237, 263               385, 399
+//   75348 x 5120   261, 344       521 (5.2 TB/s), 648    860, 969
+//   32768 x 6144   181, 172       357, 307
+//   75348 x 6144   392, 394       789, 774
+//   75348 x 8192   451, 538       953, 1047
+// To MXFP4 the tiled form does better by another 5 to 15%. One rule for all: at the
+// border it costs up to 16% (bf16 residual, 6144, whose tiles hold registers for
+// 8192) and 9% (f32 residual, 8192 x 2048) against the better form.
 constexpr int64_t kTileMinRows = 32768;
 constexpr int64_t kTileMinRowsShort = 2048;  // K <= 2048
 
