@@ -577,8 +577,9 @@ int mx_fp4_linear_slab(int act, const uint8_t* xq, const uint8_t* xs, int64_t M,
 /* The same in one call: bf16 activations x [M][ldx] (ldx >= K, ldx % 8 == 0)
  * quantized to MXFP4 or MXFP8 (act) at run time, then the product,
  * bit-identical to the quantizer and mx_fp4_linear_slab. A few tokens (up to
- * 16, at most 98304 elements) are quantized inside the product's kernel: one
- * launch, no workspace. More go through a slab in the workspace
+ * 16, at most 98304 elements, on up to 65536 weight rows, or 131072 where K >
+ * 4096) are quantized inside the product's kernel: one launch, no workspace.
+ * More go through a slab in the workspace
  * (mx_fp4_linear_ws_bytes bytes, 256-byte aligned, overlapping no argument; its
  * contents are overwritten and need no initial value). Calls, or graphs that
  * captured them, that can run at the same time need a workspace each.

@@ -48,3 +48,9 @@ def test_a_call_without_workspace_is_the_few_token_kernels():
             for N in (16, 4096, 15360):
                 assert mx().mx_fp4_linear_ws_bytes(M, 5120, N, act) == 0
                 assert mx().mx_fp4_linear_tile(M, 5120, N, act) == (0, 0, False)
+
+
+def test_up_to_how_many_weight_rows_a_few_tokens_need_no_workspace():
+    ws = mx().mx_fp4_linear_ws_bytes
+    for K, rows in ((4096, 65536), (4128, 131072)):
+        assert ws(16, K, rows, "fp4") == 0 and ws(16, K, rows + 16, "fp4") > 0
