@@ -255,3 +255,35 @@ def test_sums_that_fp32_holds_are_exact(act, M, N, tile):
     exact = xh @ oracle.dequantize_fp4(wc, sw).T + b  # exact in float64 too
     y = mx().mx_fp4_linear_slab(to_slab(xc, sx, act), to_slab(wc, sw, "fp4"), torch.from_numpy(b).half().to(dev()))
     assert np.array_equal(f64(y), oracle.bf16_round(exact))
+
+
+@pytest.mark.parametrize("act,tiles", [
+    ("fp4", {300: (128, 128, False), 800: (256, 128, False), 1600: (256, 256, False), 3100: (256, 256, True)}),
+    ("fp8", {300: (128, 128, False), 800: (192, 128, False), 1200: (256, 128, False), 1600: (256, 128, True)}),
+])
+def test_every_tile_adds_in_the_same_order(act, tiles):
+    """A token's outputs are the same bits on tiles of every shape. The second half
+    of K holds the first's groups in another order with the weights negated, over
+    many binades, so that what is left is the sums' rounding, which shows their
+    order."""
+    K, N = 2048, 5136
+    d = dev()
+    g = torch.Generator(device=d).manual_seed(12)
+    n, M = K // 64, max(tiles)
+    x = torch.randn((M, n, 32), generator=g, device=d) * torch.exp2(8 * torch.randn((1, n, 1), generator=g, device=d))
+    w = torch.randn((N, n, 32), generator=g, device=d)
+    order = torch.randperm(n, generator=g, device=d)
+    x = torch.cat([x, x[:, order]], 1).reshape(M, K).to(torch.bfloat16)
+    ws = mx().mx_fp4_quantize_weight_slab(torch.cat([w, -w[:, order]], 1).reshape(N, K))
+    ys = {}
+    for m, tile in tiles.items():
+        case(act, m, N, tile, K)
+        ys[m] = mx().mx_fp4_linear(x[:m], ws, act=act)
+    first = min(tiles)
+    assert bool((ys[first] != 0).any())
+    for m, y in ys.items():
+        assert same(y[:first], ys[first]), tiles[m]
+    # The few-token kernel's order is another one, which these inputs show.
+    few = mx().mx_fp4_linear(x[:100], ws, act=act)
+    case(act, 100, N, FEW, K)
+    assert not same(few, ys[first][:100])
