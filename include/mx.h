@@ -625,6 +625,46 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
                     void* residual_out, int64_t ldo, void* y, int64_t ldy,
                     int act, uint8_t* q, uint8_t* s, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Mixture of experts: the feed-forward block whose linears are MXFP4, one set
+ * for each of E experts, of which every token takes k.
+ * ------------------------------------------------------------------------ */
+
+/* Activation of the gate in mx_fp4_experts: g / (1 + exp(-g)), or GELU in the
+ * tanh form. */
+typedef enum { MX_GATE_SILU = 0, MX_GATE_GELU_TANH = 1 } mx_gate;
+
+/* The experts' products: for token t and its pairs (e, w) = (ids[t][j],
+ * weights[t][j]), j = 0 .. k-1,
+ *   a = gate(sum_h up[e][i][h] xhat[t][h]) * sum_h up[e][I + i][h] xhat[t][h]
+ *   o = sum_i down[e][n][i] ahat[i],  ahat = the MX values of bf16_rne(a)
+ *   y[t][n] = bf16_rne( sum_j w_j o_j )
+ * with xhat the MX quantization of x (act: MXFP8 or MXFP4, the rule of
+ * mx_quantize_act / mx_fp4_quantize_act_slab, for ahat too). Sums are FP32; the
+ * products are added as in mx_fp4_linear_slab, the pairs in the order of j. A
+ * pair whose id is outside 0 .. E-1 is skipped, whatever its weight (a token
+ * with none gives a row of zeros); an expert may occur twice in a token's list.
+ * x: bf16 [T][ldx]; ids: int32 [T][k]; weights: f32 [T][k]; up: one MXFP4 slab
+ * of 2 I rows and K = H (mx_fp4_quantize_weight_slab; the gate's rows first)
+ * for each expert, up_q uint8 [E][ceil(H/128)][R/16][4][16][16], up_s uint8
+ * [E][ceil(H/128)][R][4] with R = mx_slab_rows(2 I); down: the same with H rows
+ * and K = I; y: bf16 [T][H]. H and I are multiples of 32, at most 65536 (else
+ * MX_ERR_UNSUPPORTED); 1 <= k <= 64, 1 <= E <= 1024; T k at most 2^24, T H below
+ * 2^31, and with tiles = T k / 128 + min(E, T k) fewer than 2^24 of tiles * 2
+ * ceil(I/128) and tiles * ceil(H/128) (else MX_ERR_UNSUPPORTED). x, codes and y
+ * 16-byte aligned, ldx a multiple of 8; scales, ids and weights 4-byte aligned.
+ * workspace: mx_fp4_experts_ws_bytes(...) bytes, 256-byte aligned, overlapping
+ * no argument; its contents are overwritten and need no initial value. Calls, or
+ * graphs that captured them, that can run at the same time need one each.
+ * mx_fp4_experts_ws_bytes gives -1 on a bad shape or format. Nothing is
+ * allocated. Deterministic. T = 0 is an empty call. */
+int64_t mx_fp4_experts_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int act);
+int mx_fp4_experts(const void* x, int64_t T, int64_t H, int64_t ldx,
+                   const int32_t* ids, const float* weights, int64_t k,
+                   const uint8_t* up_q, const uint8_t* up_s, const uint8_t* down_q, const uint8_t* down_s,
+                   int64_t E, int64_t I, int gate, int act, void* y,
+                   void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

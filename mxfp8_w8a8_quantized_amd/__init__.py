@@ -28,6 +28,9 @@ MX_DT_F32 = 1
 MX_ACT_FP8 = 0
 MX_ACT_FP4 = 1
 ACT_FORMATS = {"fp8": MX_ACT_FP8, "fp4": MX_ACT_FP4}
+MX_GATE_SILU = 0
+MX_GATE_GELU_TANH = 1
+GATES = {"silu": MX_GATE_SILU, "gelu": MX_GATE_GELU_TANH}
 MX_PLAN_SLAB = 0
 MX_PLAN_SPLITK = 1
 MX_PLAN_SMALL = 2
@@ -92,6 +95,9 @@ SIGNATURES = {
     "mx_fp4_linear": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _P], _INT),
     "mx_rmsnorm_slab": ([_P, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P,
                          _P, _P], _INT),
+    "mx_fp4_experts_ws_bytes": ([_I64, _I64, _I64, _I64, _I64, _INT], _I64),
+    "mx_fp4_experts": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _INT, _INT, _P, _P, _I64, _P],
+                       _INT),
 }
 
 
@@ -1057,3 +1063,96 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
     _run(lib().mx_rmsnorm_slab, dev, x.data_ptr(), _pitch(x), _adr(residual), rdt, ldr, _adr(weight), wdt, float(eps), M, K,
          _adr(residual_out), ldo, _adr(y), ldy, fmt, out.q.data_ptr(), out.s.data_ptr())
     return out, residual_out
+
+
+class FP4Experts(NamedTuple):
+    """MXFP4 weights of E experts, a slab of `rows` rows each: codes q uint8
+    [E, ceil(K/128), R/16, 4, 16, 16], scales s uint8 [E, ceil(K/128), R, 4]
+    with R = mx_slab_rows(rows)."""
+
+    q: torch.Tensor
+    s: torch.Tensor
+    rows: int
+    K: int
+
+
+def mx_fp4_quantize_experts(w, out=None):
+    """fp32 or bf16 weights [E, N, K] (K % 32 == 0) -> FP4Experts: expert by
+    expert the codes and scales of mx_fp4_quantize_weight_slab."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or w.dtype not in _DTYPES:
+        raise TypeError("w must be a 3-D tensor of float32 or bfloat16")
+    E, N, K = w.shape
+    if K == 0 or K % 32 != 0:
+        raise ValueError("MXFP4 needs K to be a positive multiple of 32")
+    sq, ss = _fp4_shapes(N, K)
+    if out is None:
+        out = FP4Experts(w.new_empty((E,) + sq, dtype=torch.uint8), w.new_empty((E,) + ss, dtype=torch.uint8), N, K)
+    else:
+        _need_experts(out, "out", w.device)
+        if out.rows != N or out.K != K or out.q.shape[0] != E:
+            raise ValueError(f"out must hold {E} experts of {N} rows and K = {K}")
+    for e in range(E):
+        mx_fp4_quantize_weight_slab(w[e], out=FP4Slab(out.q[e], out.s[e], N, K))
+    return out
+
+
+def _need_experts(t, name, dev):
+    if not isinstance(t, FP4Experts):
+        raise TypeError(f"{name} must be an FP4Experts")
+    q, s, rows, K = t
+    _need(q, name, torch.uint8, dev)
+    _need(s, name, torch.uint8, dev)
+    sq, ss = _fp4_shapes(rows, K)
+    if q.dim() != 6 or q.shape[1:] != sq or s.shape != q.shape[:1] + ss:
+        raise ValueError(f"{name} is not MXFP4 slabs of {rows} rows and K = {K}")
+
+
+@functools.lru_cache(maxsize=4096)
+def _experts_ws_bytes(T, k, E, H, I, fmt):
+    return lib().mx_fp4_experts_ws_bytes(T, k, E, H, I, fmt)
+
+
+def mx_fp4_experts_ws_bytes(T, k, E, H, I, act="fp8"):
+    return lib().mx_fp4_experts_ws_bytes(T, k, E, H, I, _act_format(act))
+
+
+def mx_fp4_experts(x, ids, weights, up, down, gate="silu", act="fp8", y=None, workspace=None):
+    """The feed-forward block of a mixture of experts on MXFP4 weights (mx.h
+    mx_fp4_experts): y[t] = sum_j weights[t, j] * expert ids[t, j] of x[t].
+
+    x: bf16 [T, H] (rows may be strided); ids int32 and weights fp32 [T, k], as
+    mx_route gives them (a pair with an id outside 0 .. E-1 is skipped); up:
+    FP4Experts of 2 I rows (the gate's first) and K = H; down: FP4Experts of H
+    rows and K = I. gate: "silu" or "gelu"; act: format that x and the
+    intermediate are quantized to. workspace: uint8 of at least
+    mx_fp4_experts_ws_bytes(T, k, E, H, I, act) bytes (allocated here when
+    None); calls that can run at the same time, and graphs that captured them,
+    need one each."""
+    fmt = _act_format(act)
+    if gate not in GATES:
+        raise ValueError(f"gate must be 'silu' or 'gelu', got {gate!r}")
+    _need_rows(x, "x", _BF16)
+    dev = x.device
+    T, H = x.shape
+    _need(ids, "ids", torch.int32, dev)
+    _need(weights, "weights", torch.float32, dev)
+    if ids.dim() != 2 or ids.shape[0] != T or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [T, k]")
+    _need_experts(up, "up", dev)
+    _need_experts(down, "down", dev)
+    E, I, k = up.q.shape[0], down.K, ids.shape[1]
+    if up.K != H or down.rows != H or up.rows != 2 * I or down.q.shape[0] != E:
+        raise ValueError(f"up must be {E} experts of [2 I, H] and down of [H, I] with H = {H}")
+    if y is None:
+        y = x.new_empty((T, H))
+    else:
+        _need(y, "y", torch.bfloat16, dev)
+        if y.shape != (T, H):
+            raise ValueError("y must be bf16 [T, H]")
+    if workspace is None:
+        workspace = x.new_empty((max(_experts_ws_bytes(T, k, E, H, I, fmt), 0),), dtype=torch.uint8)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+    _run(lib().mx_fp4_experts, dev, _adr(x), T, H, _pitch(x), _adr(ids), _adr(weights), k, _adr(up.q), _adr(up.s),
+         _adr(down.q), _adr(down.s), E, I, GATES[gate], fmt, _adr(y), _adr(workspace), workspace.numel())
+    return y

@@ -1281,3 +1281,104 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Mixture of experts.
+namespace {
+
+constexpr int64_t kExpertsMaxDim = 65536;
+constexpr int64_t kExpertsMaxPairs = int64_t(1) << 24;
+constexpr int64_t kExpertsMaxK = 64;
+
+int check_experts_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int act) {
+  int st;
+  if ((st = check_rows("T", T)) != MX_OK) return st;
+  if (act != MX_ACT_FP8 && act != MX_ACT_FP4) return fail(MX_ERR_INVALID_ARGUMENT, "unknown activation format %d", act);
+  if ((st = check_k(H)) != MX_OK || (st = check_k(I)) != MX_OK) return st;
+  if (H > kExpertsMaxDim || I > kExpertsMaxDim)
+    return fail(MX_ERR_UNSUPPORTED, "H = %lld, I = %lld: at most 65536", (long long)H, (long long)I);
+  if (k < 1 || E < 1) return fail(MX_ERR_INVALID_ARGUMENT, "k = %lld and E = %lld must be positive", (long long)k, (long long)E);
+  if (k > kExpertsMaxK || E > mx::kMaxExperts)
+    return fail(MX_ERR_UNSUPPORTED, "k = %lld, E = %lld: at most 64 and 1024", (long long)k, (long long)E);
+  if (T == 0) return MX_OK;
+  if (T * k > kExpertsMaxPairs) return fail(MX_ERR_UNSUPPORTED, "%lld pairs exceed 2^24", (long long)(T * k));
+  if (T * H >= (int64_t(1) << 31)) return fail(MX_ERR_UNSUPPORTED, "T H = %lld must be below 2^31", (long long)(T * H));
+  // Every launch has fewer than 2^24 workgroups, of 256 threads.
+  const int64_t tiles = mx::experts_max_tiles(T, k, E);
+  if (tiles * 2 * ((I + 127) / 128) >= kMaxSplitWorkgroups || tiles * ((H + 127) / 128) >= kMaxSplitWorkgroups ||
+      T * ((H + 1023) / 1024) >= kMaxSplitWorkgroups)
+    return fail(MX_ERR_UNSUPPORTED, "%lld pairs of %lld experts are too many for H = %lld, I = %lld", (long long)(T * k),
+                (long long)E, (long long)H, (long long)I);
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mx_fp4_experts_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int act) {
+  if (check_experts_shape(T, k, E, H, I, act) != MX_OK) return -1;
+  return T == 0 ? 0 : mx::experts_workspace(T, k, E, H, I, act == MX_ACT_FP4).bytes;
+}
+
+int mx_fp4_experts(const void* x, int64_t T, int64_t H, int64_t ldx, const int32_t* ids, const float* weights, int64_t k,
+                   const uint8_t* up_q, const uint8_t* up_s, const uint8_t* down_q, const uint8_t* down_s, int64_t E,
+                   int64_t I, int gate, int act, void* y, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st = check_experts_shape(T, k, E, H, I, act);
+  if (st != MX_OK) return st;
+  if (gate != MX_GATE_SILU && gate != MX_GATE_GELU_TANH) return fail(MX_ERR_INVALID_ARGUMENT, "unknown gate %d", gate);
+  if (ldx < H || ldx % 8 != 0) return fail(MX_ERR_INVALID_ARGUMENT, "ldx = %lld must be >= H and a multiple of 8", (long long)ldx);
+  if (T == 0) return MX_OK;
+  if (x == nullptr || ids == nullptr || weights == nullptr || up_q == nullptr || up_s == nullptr || down_q == nullptr ||
+      down_s == nullptr || y == nullptr)
+    return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  if (!aligned(x, 16) || !aligned(up_q, 16) || !aligned(down_q, 16) || !aligned(y, 16))
+    return fail(MX_ERR_INVALID_ARGUMENT, "x, codes and y must be 16-byte aligned");
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(up_s, 4) || !aligned(down_s, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ids, weights and scales must be 4-byte aligned");
+  const mx::ExpertsWorkspace w = mx::experts_workspace(T, k, E, H, I, act == MX_ACT_FP4);
+  if (workspace == nullptr || !aligned(workspace, 256))
+    return fail(MX_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned and not NULL");
+  if (workspace_bytes < w.bytes)
+    return fail(MX_ERR_INVALID_ARGUMENT, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)w.bytes);
+  const int64_t RU = mx::slab_rows(2 * I), RD = mx::slab_rows(H);
+  struct Range {
+    const void* p;
+    uint64_t n;
+  };
+  const Range in[7] = {{x, ((uint64_t)(T - 1) * ldx + H) * 2},
+                       {ids, (uint64_t)(T * k) * 4},
+                       {weights, (uint64_t)(T * k) * 4},
+                       {up_q, E * fp4_code_bytes(RU, H)},
+                       {up_s, E * fp4_scale_bytes(RU, H)},
+                       {down_q, E * fp4_code_bytes(RD, I)},
+                       {down_s, E * fp4_scale_bytes(RD, I)}};
+  const uint64_t yb = (uint64_t)T * H * 2;
+  for (const Range& r : in)
+    if (overlap(y, yb, r.p, r.n) || overlap(workspace, w.bytes, r.p, r.n))
+      return fail(MX_ERR_INVALID_ARGUMENT, "y or the workspace overlaps an input");
+  if (overlap(workspace, w.bytes, y, yb)) return fail(MX_ERR_INVALID_ARGUMENT, "the workspace overlaps y");
+  if ((st = check_device()) != MX_OK) return st;
+  mx::ExpertsArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.ids = ids;
+  a.weights = weights;
+  a.T = T;
+  a.k = k;
+  a.E = E;
+  a.H = H;
+  a.I = I;
+  a.up_q = up_q;
+  a.up_s = up_s;
+  a.down_q = down_q;
+  a.down_s = down_s;
+  a.gate = gate;
+  a.fp4 = act == MX_ACT_FP4;
+  a.y = y;
+  a.workspace = workspace;
+  (void)hipGetLastError();
+  return finish(mx::launch_fp4_experts(a, (hipStream_t)stream), "experts launch");
+}
+
+}  // extern "C"

@@ -184,6 +184,40 @@ struct RmsNormArgs {
 };
 hipError_t launch_rmsnorm_slab(const RmsNormArgs& a, hipStream_t stream);
 
+// The experts' products on MXFP4 weights (mx_experts.hip): x bf16 [T][ldx], k
+// pairs (ids, weights) a token, up slabs of 2 I rows and K = H, down slabs of H
+// rows and K = I for each of E experts; y bf16 [T][H]. gate: 0 SiLU, 1 GELU-tanh.
+constexpr int kExpertTile = 128;  // pairs of a tile
+constexpr int kMaxExperts = 1024;
+struct ExpertTile {
+  int32_t expert, first, count, pad;  // sorted rows first .. first + count - 1
+};
+struct ExpertsArgs {
+  const void* x;
+  int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  int64_t T, k, E, H, I;
+  const uint8_t* up_q;
+  const uint8_t* up_s;
+  const uint8_t* down_q;
+  const uint8_t* down_s;
+  int gate, fp4;
+  void* y;
+  void* workspace;
+};
+struct ExpertsWorkspace {  // offsets of its parts
+  int64_t xq, xs, hq, hs, o, rows, pos, tiles, n_tiles, bytes;
+  uint32_t xpitch_q, xpitch_s, hpitch_q, hpitch_s;
+  int64_t max_tiles;
+};
+// The most tiles that T k pairs of E experts can take.
+inline int64_t experts_max_tiles(int64_t T, int64_t k, int64_t E) {
+  return T * k / kExpertTile + (E < T * k ? E : T * k);
+}
+ExpertsWorkspace experts_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int fp4);
+hipError_t launch_fp4_experts(const ExpertsArgs& a, hipStream_t stream);
+
 // Bytes of the library-owned scratch array of mx_linear_noalloc (per GPU).
 constexpr int64_t kScratchBytes = int64_t(64) << 20;
 
