@@ -626,9 +626,68 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
                     int act, uint8_t* q, uint8_t* s, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The norms after and before a block, fused with the block's gate and the
+ * scaled residual, written as the next quantized linear's activation slab:
+ *   n    = x (the block's output), with post * post_weight / sqrt(mean_k x^2 + eps)
+ *   h    = residual_scale * residual + gate * n, rounded to the residual's type
+ *   y    = bf16_rne( norm(h) * weight * (1 + scale) + shift ), with norm(h)
+ *          h / sqrt(mean_k h^2 + eps)            (MX_NORM_RMS) or
+ *          (h - mean h) / sqrt(var h + eps)      (MX_NORM_LAYER, var over K)
+ *   q, s = the MX quantization of y (act), as in mx_rmsnorm_slab
+ * Means, sums and products are computed in f64; h and y are rounded to f32 and
+ * that to bf16. A row holding NaN or Inf gives what the formula gives in floating
+ * point.
+ * x: bf16 [M][ldx]; residual: bf16 or f32 (rdtype) [M][ldr]; vectors of type
+ * vdtype, each NULL for none: post_weight, weight [K]; gate [gate_rows][ldg],
+ * scale and shift [mod_rows][ldm], whose row i serves rows i M / rows .. (i + 1) M
+ * / rows - 1 of x (gate_rows and mod_rows divide M: one row for all, one for each
+ * sequence of a batch, or one for each row). post_weight without post is an error.
+ * residual_out (h): [M][ldo] of the residual's type or NULL to drop it; it may
+ * be the residual itself with the same pitch. y: bf16 [M][ldy] or NULL to drop it;
+ * q, s: the slab, or both NULL for none (then y is needed; act is ignored and K a
+ * multiple of 32). Outputs must otherwise overlap nothing. Every buffer 16-byte
+ * aligned, rows a multiple of 16 bytes apart; pitches, dtypes and row counts of
+ * NULL pointers are ignored. eps >= 0 and finite, residual_scale finite. K as the
+ * format requires, at most 65536, M at most 2^22 (else MX_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+typedef enum { MX_NORM_RMS = 0, MX_NORM_LAYER = 1 } mx_norm_kind;
+int mx_block_norm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr,
+                       double residual_scale, int post, const void* post_weight,
+                       const void* gate, int64_t gate_rows, int64_t ldg, int kind, const void* weight,
+                       const void* scale, const void* shift, int64_t mod_rows, int64_t ldm, int vdtype,
+                       double eps, int64_t M, int64_t K, void* residual_out, int64_t ldo, void* y, int64_t ldy,
+                       int act, uint8_t* q, uint8_t* s, void* stream);
+
+/* ------------------------------------------------------------------------
  * Mixture of experts: the feed-forward block whose linears are MXFP4, one set
  * for each of E experts, of which every token takes k.
  * ------------------------------------------------------------------------ */
+
+/* Scores of mx_route. */
+typedef enum { MX_ROUTE_SOFTMAX = 0, MX_ROUTE_SIGMOID = 1 } mx_route_scores;
+
+/* The k experts of every token, and their weights, from the router's logits:
+ *   l = logits, NaN as -inf and +inf as the largest f32
+ *   s = softmax(l) over the E experts, or 1 / (1 + exp(-l)); 0 where l = -inf
+ *   c = l without a bias, f32(s + bias) with one (s in f64); -inf where l is
+ *       (a masked expert) or where c is NaN
+ * With groups > 1 (equal runs of E / groups experts) the top_groups best stay and
+ * the others' c become -inf. A group's score is its highest c, with a bias the
+ * f32 sum of its two highest (a second one of -inf adds nothing).
+ *   ids     = the k highest c, in falling order, ties to the lower index (groups
+ *             too); experts of c = -inf come last, lowest index first
+ *   weights = s of those (0 where c = -inf); with renorm divided by their sum (0
+ *             where that is 0); times scale
+ * Scores of the chosen are computed in f64. The bias steers the choice only.
+ * logits: f32 or bf16 (dtype, mx_dtype) [T][ld], ld >= E; bias: f32 [E] or NULL;
+ * ids: int32 [T][k], weights: f32 [T][k]. Buffers aligned to their elements;
+ * outputs overlap neither an input nor each other. 1 <= k <= E, groups divides E, 1 <=
+ * top_groups <= groups, k <= top_groups E / groups, scale finite (else
+ * MX_ERR_INVALID_ARGUMENT); E at most 1024, k and groups at most 64, T at most
+ * 2^26 (else MX_ERR_UNSUPPORTED). T = 0 is an empty call. */
+int mx_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias,
+             int scores, int64_t groups, int64_t top_groups, int64_t k, int renorm, double scale,
+             int32_t* ids, float* weights, void* stream);
 
 /* Activation of the gate in mx_fp4_experts: g / (1 + exp(-g)), or GELU in the
  * tanh form. */

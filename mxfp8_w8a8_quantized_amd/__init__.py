@@ -30,6 +30,12 @@ MX_ACT_FP4 = 1
 ACT_FORMATS = {"fp8": MX_ACT_FP8, "fp4": MX_ACT_FP4}
 MX_GATE_SILU = 0
 MX_GATE_GELU_TANH = 1
+MX_NORM_RMS = 0
+MX_NORM_LAYER = 1
+NORM_KINDS = {"rms": MX_NORM_RMS, "layer": MX_NORM_LAYER}
+MX_ROUTE_SOFTMAX = 0
+MX_ROUTE_SIGMOID = 1
+SCORES = {"softmax": MX_ROUTE_SOFTMAX, "sigmoid": MX_ROUTE_SIGMOID}
 GATES = {"silu": MX_GATE_SILU, "gelu": MX_GATE_GELU_TANH}
 MX_PLAN_SLAB = 0
 MX_PLAN_SPLITK = 1
@@ -95,6 +101,9 @@ SIGNATURES = {
     "mx_fp4_linear": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _INT, _INT, _P, _P, _I64, _P], _INT),
     "mx_rmsnorm_slab": ([_P, _I64, _P, _INT, _I64, _P, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P,
                          _P, _P], _INT),
+    "mx_block_norm_slab": ([_P, _I64, _P, _INT, _I64, ctypes.c_double, _INT, _P, _P, _I64, _I64, _INT, _P, _P, _P, _I64,
+                            _I64, _INT, ctypes.c_double, _I64, _I64, _P, _I64, _P, _I64, _INT, _P, _P, _P], _INT),
+    "mx_route": ([_P, _INT, _I64, _I64, _I64, _P, _INT, _I64, _I64, _I64, _INT, ctypes.c_double, _P, _P, _P], _INT),
     "mx_fp4_experts_ws_bytes": ([_I64, _I64, _I64, _I64, _I64, _INT], _I64),
     "mx_fp4_experts": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _INT, _INT, _P, _P, _I64, _P],
                        _INT),
@@ -1063,6 +1072,121 @@ def mx_rmsnorm_slab(x, weight=None, residual=None, eps=1e-6, act="fp8", out=None
     _run(lib().mx_rmsnorm_slab, dev, x.data_ptr(), _pitch(x), _adr(residual), rdt, ldr, _adr(weight), wdt, float(eps), M, K,
          _adr(residual_out), ldo, _adr(y), ldy, fmt, out.q.data_ptr(), out.s.data_ptr())
     return out, residual_out
+
+
+def mx_block_norm_slab(x, residual, post=False, post_weight=None, gate=None, residual_scale=1.0, kind="rms", weight=None,
+                       scale=None, shift=None, eps=1e-6, act="fp8", out=None, residual_out=None, y=None):
+    """The norms after and before a block, fused with its gate and the scaled
+    residual (mx.h mx_block_norm_slab): h = residual_scale * residual + gate * n,
+    n = x or (post) its RMS norm times post_weight; then norm(h) * weight * (1 +
+    scale) + shift as the activation slab of a quantized linear. Returns (slab, h).
+
+    x: bf16 [M, K], the block's output; residual: bf16 or fp32 [M, K]; kind:
+    "rms" or "layer". post_weight, weight: [K]; gate, scale, shift: [K] or [n, K]
+    with n dividing M (row i serves M / n consecutive rows of x); all of these bf16
+    or all fp32, None for none. Rows may be strided (scale and shift alike). act:
+    "fp8" (Slab), "fp4" (FP4Slab), or None for no slab: y, bf16 [M, K], is then
+    allocated if it is None, and (y, h) is returned. residual_out: h goes here
+    (allocated when None; may be `residual` itself). y also receives the norm, if
+    given."""
+    fmt = MX_ACT_FP4 if act is None else _act_format(act)
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+    _need_rows(x, "x", _BF16)
+    dev, shape = x.device, x.shape
+    M, K = shape
+    if K == 0 or K % (32 if fmt == MX_ACT_FP4 else 64) != 0:
+        raise ValueError("K must be a positive multiple of 32 (no slab, fp4) or 64 (fp8)")
+    _need_rows(residual, "residual", _DTYPES, shape, dev)
+    vt = None
+    gate_rows = ldg = mod_rows = ldm = ldy = 0
+    for name, v in (("post_weight", post_weight), ("weight", weight), ("gate", gate), ("scale", scale), ("shift", shift)):
+        if v is None:
+            continue
+        if vt is None:
+            vt = v.dtype
+        if v.dtype != vt or vt not in _DTYPES:
+            raise TypeError(f"{name}: the vectors must be all bfloat16 or all float32")
+        one = name in ("post_weight", "weight")
+        if v.device != dev or v.dim() > (1 if one else 2) or v.dim() < 1 or v.shape[-1] != K or v.stride(-1) != 1:
+            raise ValueError(f"{name} must be {[K] if one else [K, 'or n', K]} on {dev} with unit column stride")
+        if one:
+            continue
+        rows, ld = (1, K) if v.dim() == 1 else (v.shape[0], _pitch(v))
+        if rows == 0 or M % rows != 0:
+            raise ValueError(f"{name} must have a number of rows that divides {M}")
+        if name == "gate":
+            gate_rows, ldg = rows, ld
+        elif mod_rows and (mod_rows, ldm) != (rows, ld):
+            raise ValueError("scale and shift must have the same rows and pitch")
+        else:
+            mod_rows, ldm = rows, ld
+    if residual_out is None:
+        residual_out = torch.empty_like(residual) if residual.is_contiguous() else residual.new_empty(shape)
+        ldo = K
+    else:
+        _need_rows(residual_out, "residual_out", (residual.dtype,), shape, dev)
+        ldo = _pitch(residual_out)
+    if y is not None:
+        _need_rows(y, "y", _BF16, shape, dev)
+    elif act is None:
+        y = x.new_empty(shape)
+    if y is not None:
+        ldy = _pitch(y)
+    q = s = None
+    if act is None:
+        if out is not None:
+            raise ValueError("out without a format")
+        out = y
+    else:
+        if fmt == MX_ACT_FP4:
+            out = _fp4_out(M, K, x, out)
+        elif out is None:
+            R = (M + 255) // 256 * 256
+            out = Slab(x.new_empty((K // 64, R, 64), dtype=torch.uint8), x.new_empty((K // 64, R, 2), dtype=torch.uint8), M)
+        else:
+            out = _slab_out(M, K, dev, out)
+        q, s = out.q.data_ptr(), out.s.data_ptr()
+    _run(lib().mx_block_norm_slab, dev, x.data_ptr(), _pitch(x), residual.data_ptr(), _DTYPES[residual.dtype],
+         _pitch(residual), float(residual_scale), int(bool(post)), _adr(post_weight), _adr(gate), gate_rows, ldg,
+         NORM_KINDS[kind], _adr(weight), _adr(scale), _adr(shift), mod_rows, ldm, _DTYPES.get(vt, 0), float(eps), M, K,
+         residual_out.data_ptr(), ldo, _adr(y), ldy, fmt, q, s)
+    return out, residual_out
+
+
+def mx_route(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, renorm=True, scale=1.0, ids=None,
+             weights=None):
+    """The k experts of every token and their weights (mx.h mx_route): returns
+    (ids int32 [T, k], weights fp32 [T, k]), in falling order of the choice.
+
+    logits: fp32 or bf16 [T, E] (rows may be strided); scores: "softmax" or
+    "sigmoid"; bias: fp32 [E] added to the scores for the choice only; with
+    groups > 1 the choice is among the top_groups best of `groups` equal groups;
+    renorm: weights divided by their sum; scale: times this."""
+    if scores not in SCORES:
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', got {scores!r}")
+    _need_rows(logits, "logits", _DTYPES)
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, dev)
+        if bias.shape != (E,):
+            raise ValueError(f"bias must be [{E}]")
+    if k < 1:
+        raise ValueError("k must be positive")
+    if ids is None:
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+    else:
+        _need(ids, "ids", torch.int32, dev)
+    if weights is None:
+        weights = logits.new_empty((T, k), dtype=torch.float32)
+    else:
+        _need(weights, "weights", torch.float32, dev)
+    if ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError(f"ids and weights must be [{T}, {k}]")
+    _run(lib().mx_route, dev, _adr(logits), _DTYPES[logits.dtype], T, E, _pitch(logits), _adr(bias), SCORES[scores], groups,
+         top_groups, k, int(bool(renorm)), float(scale), _adr(ids), _adr(weights))
+    return ids, weights
 
 
 class FP4Experts(NamedTuple):

@@ -1282,6 +1282,111 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
 
 }  // extern "C"
 
+extern "C" int mx_block_norm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr,
+                                  double residual_scale, int post, const void* post_weight, const void* gate,
+                                  int64_t gate_rows, int64_t ldg, int kind, const void* weight, const void* scale,
+                                  const void* shift, int64_t mod_rows, int64_t ldm, int vdtype, double eps, int64_t M,
+                                  int64_t K, void* residual_out, int64_t ldo, void* y, int64_t ldy, int act, uint8_t* q,
+                                  uint8_t* s, void* stream) {
+  int st;
+  const bool slab = q != nullptr || s != nullptr;
+  if ((st = check_rows("M", M)) != MX_OK) return st;
+  if ((st = slab ? check_act_k(act, K) : check_k(K)) != MX_OK) return st;
+  if (K > mx::kNormMaxK) return fail(MX_ERR_UNSUPPORTED, "K = %lld exceeds the norm's 65536", (long long)K);
+  if (M > mx::kNormMaxRows) return fail(MX_ERR_UNSUPPORTED, "M = %lld exceeds the norm's 2^22", (long long)M);
+  if (!(eps >= 0.0 && std::isfinite(eps))) return fail(MX_ERR_INVALID_ARGUMENT, "eps = %g must be finite and >= 0", eps);
+  if (!std::isfinite(residual_scale)) return fail(MX_ERR_INVALID_ARGUMENT, "residual_scale must be finite");
+  if (rdtype != MX_DT_BF16 && rdtype != MX_DT_F32) return fail(MX_ERR_INVALID_ARGUMENT, "unknown residual dtype %d", rdtype);
+  const bool vectors = post_weight != nullptr || gate != nullptr || weight != nullptr || scale != nullptr || shift != nullptr;
+  if (vectors && vdtype != MX_DT_BF16 && vdtype != MX_DT_F32)
+    return fail(MX_ERR_INVALID_ARGUMENT, "unknown dtype %d of the vectors", vdtype);
+  if (kind != MX_NORM_RMS && kind != MX_NORM_LAYER) return fail(MX_ERR_INVALID_ARGUMENT, "unknown norm %d", kind);
+  if (!post && post_weight != nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "post_weight without post");
+  const int64_t es = rdtype == MX_DT_F32 ? 4 : 2, vs = vdtype == MX_DT_F32 ? 4 : 2;
+  const bool mod = scale != nullptr || shift != nullptr;
+  if (ldx < K || ldx % 8 != 0) return fail(MX_ERR_INVALID_ARGUMENT, "ldx = %lld must be >= K and a multiple of 8", (long long)ldx);
+  if (ldr < K || (ldr * es) % 16 != 0)
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldr = %lld must be >= K with 16-byte aligned rows", (long long)ldr);
+  if (residual_out != nullptr && (ldo < K || (ldo * es) % 16 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldo = %lld must be >= K with 16-byte aligned rows", (long long)ldo);
+  if (y != nullptr && (ldy < K || ldy % 8 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "ldy = %lld must be >= K and a multiple of 8", (long long)ldy);
+  if (gate != nullptr && (gate_rows < 1 || ldg < K || (ldg * vs) % 16 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "gate: at least one row, ldg = %lld >= K with 16-byte aligned rows", (long long)ldg);
+  if (mod && (mod_rows < 1 || ldm < K || (ldm * vs) % 16 != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "scale and shift: at least one row, ldm = %lld >= K with 16-byte aligned rows", (long long)ldm);
+  if (M == 0) return MX_OK;
+  if ((gate != nullptr && M % gate_rows != 0) || (mod && M % mod_rows != 0))
+    return fail(MX_ERR_INVALID_ARGUMENT, "gate_rows and mod_rows must divide M = %lld", (long long)M);
+  if (x == nullptr || residual == nullptr || (q == nullptr) != (s == nullptr) || (!slab && y == nullptr))
+    return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  for (const void* p : {x, residual, post_weight, gate, weight, scale, shift, (const void*)residual_out, (const void*)y,
+                        (const void*)q, (const void*)s})
+    if (!aligned(p, 16)) return fail(MX_ERR_INVALID_ARGUMENT, "every buffer must be 16-byte aligned");
+  const int64_t R = mx::slab_rows(M);
+  auto span = [&](const void* p, int64_t rows, int64_t ld, int64_t e) {
+    return p == nullptr ? uint64_t(0) : ((uint64_t)(rows - 1) * ld + K) * e;
+  };
+  struct Range {
+    const void* p;
+    uint64_t n;
+  };
+  const Range in[7] = {{x, span(x, M, ldx, 2)},
+                       {residual, span(residual, M, ldr, es)},
+                       {post_weight, span(post_weight, 1, K, vs)},
+                       {weight, span(weight, 1, K, vs)},
+                       {gate, span(gate, gate_rows, ldg, vs)},
+                       {scale, span(scale, mod_rows, ldm, vs)},
+                       {shift, span(shift, mod_rows, ldm, vs)}};
+  const Range out[4] = {{q, slab ? act_code_bytes(act, R, K) : 0},
+                        {s, slab ? act_scale_bytes(act, R, K) : 0},
+                        {residual_out, span(residual_out, M, ldo, es)},
+                        {y, span(y, M, ldy, 2)}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 7; ++i) {
+      // The new residual may take the old one's place, row by row.
+      if (o == 2 && i == 1 && residual_out == residual && ldo == ldr) continue;
+      if (overlap(out[o].p, out[o].n, in[i].p, in[i].n))
+        return fail(MX_ERR_INVALID_ARGUMENT, "an output overlaps an input");
+    }
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].n, out[i].p, out[i].n)) return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap");
+  }
+  if ((st = check_device()) != MX_OK) return st;
+  mx::BlockNormArgs a;
+  a.x = x;
+  a.ldx = ldx;
+  a.residual = residual;
+  a.ldr = ldr;
+  a.residual_scale = residual_scale;
+  a.eps = eps;
+  a.post_weight = post_weight;
+  a.gate = gate;
+  a.weight = weight;
+  a.scale = scale;
+  a.shift = shift;
+  a.gate_period = gate != nullptr ? M / gate_rows : 1;
+  a.ldg = gate != nullptr ? ldg : 0;
+  a.mod_period = mod ? M / mod_rows : 1;
+  a.ldm = mod ? ldm : 0;
+  a.M = M;
+  a.R = R;
+  a.K = K;
+  a.residual_out = residual_out;
+  a.ldo = ldo;
+  a.y = y;
+  a.ldy = ldy;
+  a.q = q;
+  a.s = s;
+  a.residual_f32 = rdtype == MX_DT_F32;
+  a.vectors_f32 = vdtype == MX_DT_F32;
+  a.post = post != 0;
+  a.layer = kind == MX_NORM_LAYER;
+  a.fp4 = slab ? act == MX_ACT_FP4 : 1;
+  (void)hipGetLastError();
+  return finish(mx::launch_block_norm_slab(a, (hipStream_t)stream), "block norm launch");
+}
+
 // ---------------------------------------------------------------------------
 // Mixture of experts.
 namespace {
@@ -1315,6 +1420,53 @@ int check_experts_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, i
 }  // namespace
 
 extern "C" {
+
+int mx_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scores,
+             int64_t groups, int64_t top_groups, int64_t k, int renorm, double scale, int32_t* ids, float* weights,
+             void* stream) {
+  int st;
+  if ((st = check_rows("T", T)) != MX_OK) return st;
+  if (dtype != MX_DT_BF16 && dtype != MX_DT_F32) return fail(MX_ERR_INVALID_ARGUMENT, "unknown logits dtype %d", dtype);
+  if (scores != MX_ROUTE_SOFTMAX && scores != MX_ROUTE_SIGMOID)
+    return fail(MX_ERR_INVALID_ARGUMENT, "unknown scores %d", scores);
+  if (E < 1 || ld < E) return fail(MX_ERR_INVALID_ARGUMENT, "E = %lld must be positive and at most ld = %lld", (long long)E, (long long)ld);
+  if (groups < 1 || E % groups != 0 || top_groups < 1 || top_groups > groups)
+    return fail(MX_ERR_INVALID_ARGUMENT, "groups = %lld must divide E = %lld, top_groups = %lld lie in 1 .. groups",
+                (long long)groups, (long long)E, (long long)top_groups);
+  if (k < 1 || k > top_groups * (E / groups))
+    return fail(MX_ERR_INVALID_ARGUMENT, "k = %lld must lie in 1 .. %lld", (long long)k, (long long)(top_groups * (E / groups)));
+  if (!std::isfinite(scale)) return fail(MX_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if (E > mx::kMaxExperts || k > kExpertsMaxK || groups > kExpertsMaxK || T > (int64_t(1) << 26))
+    return fail(MX_ERR_UNSUPPORTED, "E = %lld, k = %lld, groups = %lld, T = %lld: at most 1024, 64, 64 and 2^26",
+                (long long)E, (long long)k, (long long)groups, (long long)T);
+  if (T == 0) return MX_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return fail(MX_ERR_INVALID_ARGUMENT, "NULL pointer");
+  const uint64_t es = dtype == MX_DT_F32 ? 4 : 2;
+  if (!aligned(logits, es) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return fail(MX_ERR_INVALID_ARGUMENT, "buffers must be aligned to their elements");
+  const uint64_t lb = ((uint64_t)(T - 1) * ld + E) * es, ob = (uint64_t)T * k * 4;
+  if (overlap(ids, ob, logits, lb) || overlap(weights, ob, logits, lb) || overlap(ids, ob, bias, (uint64_t)E * 4) ||
+      overlap(weights, ob, bias, (uint64_t)E * 4) || overlap(ids, ob, weights, ob))
+    return fail(MX_ERR_INVALID_ARGUMENT, "outputs overlap an input or each other");
+  if ((st = check_device()) != MX_OK) return st;
+  mx::RouteArgs a;
+  a.logits = logits;
+  a.T = T;
+  a.ld = ld;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.factor = scale;
+  a.f32 = dtype == MX_DT_F32;
+  a.scores = scores;
+  a.E = (int)E;
+  a.groups = (int)groups;
+  a.top_groups = (int)top_groups;
+  a.k = (int)k;
+  a.renorm = renorm != 0;
+  (void)hipGetLastError();
+  return finish(mx::launch_route(a, (hipStream_t)stream), "route launch");
+}
 
 int64_t mx_fp4_experts_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int act) {
   if (check_experts_shape(T, k, E, H, I, act) != MX_OK) return -1;

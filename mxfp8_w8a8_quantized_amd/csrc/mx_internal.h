@@ -184,6 +184,29 @@ struct RmsNormArgs {
 };
 hipError_t launch_rmsnorm_slab(const RmsNormArgs& a, hipStream_t stream);
 
+// The norms around a block with its gate and scaled residual (mx_block_norm.hip).
+// K up to kNormMaxK; residual_out, y, q (with s) and the vectors may be null. The
+// vectors (f32 or bf16, all the same): post_weight and weight [K]; gate a row for
+// every gate_period rows of x, scale and shift one for every mod_period.
+struct BlockNormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* residual;
+  int64_t ldr;
+  double residual_scale, eps;
+  const void *post_weight, *gate, *weight, *scale, *shift;
+  int64_t gate_period, ldg, mod_period, ldm;
+  int64_t M, R, K;  // R = slab_rows(M)
+  void* residual_out;
+  int64_t ldo;
+  void* y;
+  int64_t ldy;
+  uint8_t* q;
+  uint8_t* s;
+  int residual_f32, vectors_f32, post, layer, fp4;
+};
+hipError_t launch_block_norm_slab(const BlockNormArgs& a, hipStream_t stream);
+
 // The experts' products on MXFP4 weights (mx_experts.hip): x bf16 [T][ldx], k
 // pairs (ids, weights) a token, up slabs of 2 I rows and K = H, down slabs of H
 // rows and K = I for each of E experts; y bf16 [T][H]. gate: 0 SiLU, 1 GELU-tanh.
@@ -217,6 +240,20 @@ inline int64_t experts_max_tiles(int64_t T, int64_t k, int64_t E) {
 }
 ExpertsWorkspace experts_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int fp4);
 hipError_t launch_fp4_experts(const ExpertsArgs& a, hipStream_t stream);
+
+// Routing to experts (mx_route.hip). logits f32 or bf16 [T][ld]; bias may be null;
+// scores: 0 softmax, 1 sigmoid; E <= kMaxExperts, groups divides E, groups and k
+// <= 64; ids and weights [T][k].
+struct RouteArgs {
+  const void* logits;
+  int64_t T, ld;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  double factor;
+  int f32, scores, E, groups, top_groups, k, renorm;
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 // Bytes of the library-owned scratch array of mx_linear_noalloc (per GPU).
 constexpr int64_t kScratchBytes = int64_t(64) << 20;
