@@ -9,68 +9,106 @@
 //
 // One pass over memory, as in mx_norm.hip: a row stays in registers through up to
 // three sums (of x^2, of h, of the squares), 7 bytes an element with a bf16
-// residual. Sums and products are f64, for the reason given there; the vectors
-// (weights, gate, scale, shift) come from the caches, once for each row.
+// residual.
+//
+// Products are f32: a conversion to f64 costs as much as four f32 operations, and
+// an element has up to nine of them (75348 x 5120 with gate, modulation and layer
+// norm: 1146 us in f64). Eight squares are added in f32, those sums in f64, so a
+// row's sum is off by at most 8 * 2^-24; a row whose squares leave f32's range is
+// summed again in f64 (SLOW below). The mean is subtracted in two parts. y is then
+// off by less than 2^-20 of its terms before it is rounded to 8 bits.
 #include "mx_internal.h"
 #include "mx_norm_device.h"
 
 namespace mx {
 namespace {
 
-struct Vectors {  // the vectors' rows for one row of x; null where there is none
-  const void *post, *gate, *weight, *scale, *shift;
+// A vector's row for one row of x: an empty resource where there is none, whose
+// loads give zeros without touching memory; `rest` is then added (1 for factors), so
+// that the code has no branches and one chunk's vectors are on their way while the
+// chunk before is computed (gate, scale and shift of 75348 x 5120: 698 to RESULT us).
+struct Vector {
+  __amdgpu_buffer_rsrc_t r;
+  float rest;
+};
+template <bool VF32>
+__device__ __forceinline__ Vector vector_of(const BlockNormArgs& p, const void* v, int64_t row, int64_t ld, float rest) {
+  constexpr int ES = VF32 ? 4 : 2;
+  return {make_rsrc(v == nullptr ? nullptr : (const uint8_t*)v + row * ld * ES, v == nullptr ? 0u : (uint32_t)p.K * ES),
+          v == nullptr ? rest : 0.f};
+}
+struct Vectors {
+  Vector post, gate, weight, scale, shift;
+};
+template <bool VF32>
+__device__ __forceinline__ Vectors vectors_of(const BlockNormArgs& p, int64_t row) {
+  const int64_t g = row / p.gate_period, m = row / p.mod_period;
+  return {vector_of<VF32>(p, p.post_weight, 0, 0, 1.f), vector_of<VF32>(p, p.gate, g, p.ldg, 1.f),
+          vector_of<VF32>(p, p.weight, 0, 0, 1.f), vector_of<VF32>(p, p.scale, m, p.ldm, 0.f),
+          vector_of<VF32>(p, p.shift, m, p.ldm, 0.f)};
+}
+
+// Eight consecutive values of a vector as loaded (past K zeros).
+template <bool VF32>
+struct Eight {
+  i32x4 w[VF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const Vector& v, int k) {
+    w[0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(v.r, k * (VF32 ? 4 : 2), 0, 0));
+    if constexpr (VF32) w[1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(v.r, k * 4 + 16, 0, 0));
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (VF32) return __uint_as_float((uint32_t)w[i >> 2][i & 3]);
+    return (i & 1) ? bf16_hi((uint32_t)w[0][i >> 1]) : bf16_lo((uint32_t)w[0][i >> 1]);
+  }
 };
 
-// Eight consecutive values of a vector.
-__device__ __forceinline__ void vector8(const void* v, int k, int f32, float (&out)[8]) {
-  if (f32) {
-    const f32x4 a = *(const f32x4*)((const float*)v + k), b = *(const f32x4*)((const float*)v + k + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out[i] = a[i];
-      out[4 + i] = b[i];
-    }
-  } else {
-    const i32x4 a = *(const i32x4*)((const uint16_t*)v + k);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out[2 * i] = bf16_lo((uint32_t)a[i]);
-      out[2 * i + 1] = bf16_hi((uint32_t)a[i]);
-    }
-  }
+// The squares' f32 sums cannot be relied on: too large, or so small that squares
+// vanished and eps does not hide it.
+__device__ __forceinline__ bool out_of_range(const BlockNormArgs& p, double sum) {
+  return !(sum < 1e38) || (sum < 1e-30 && p.eps * (double)p.K < 1e-20);
 }
-
-__device__ __forceinline__ const void* vector_row(const void* v, int64_t row, int64_t ld, int f32) {
-  return v == nullptr ? nullptr : (const uint8_t*)v + row * ld * (f32 ? 4 : 2);
-}
-__device__ __forceinline__ Vectors vectors_of(const BlockNormArgs& p, int64_t row) {
-  Vectors v;
-  v.post = p.post_weight;
-  v.weight = p.weight;
-  v.gate = vector_row(p.gate, row / p.gate_period, p.ldg, p.vectors_f32);
-  v.scale = vector_row(p.scale, row / p.mod_period, p.ldm, p.vectors_f32);
-  v.shift = vector_row(p.shift, row / p.mod_period, p.ldm, p.vectors_f32);
-  return v;
-}
-
 __device__ __forceinline__ double rstd_of(const BlockNormArgs& p, double sum) {
   return 1.0 / __builtin_sqrt(sum / (double)p.K + p.eps);
 }
 
-// Rounds f64 to f32; the asm keeps the rounding to bf16 that follows apart (merged,
-// the compiler spells the two out in ten operations an element).
-__device__ __forceinline__ float round_f32(double d) {
-  float f = (float)d;
-  asm volatile("" : "+v"(f));
-  return f;
+// Sums over a lane's elements value(c, i), chunk c < NCH with in(c), i < 8; SLOW in
+// f64.
+template <bool SLOW, bool SQUARES, int NCH, typename In, typename Value>
+__device__ __forceinline__ double sum_of(In&& in, Value&& value) {
+  double sum = 0.0;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    if constexpr (SLOW) {
+      double s = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double v = value(c, i);
+        s = SQUARES ? __builtin_fma(v, v, s) : s + v;
+      }
+      sum += in(c) ? s : 0.0;
+    } else {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = value(c, i);
+        s = SQUARES ? __builtin_fmaf(v, v, s) : s + v;
+      }
+      sum += (double)(in(c) ? s : 0.f);
+    }
+  }
+  return sum;
 }
 
+struct Statistics {
+  float mean, mean_low, rstd;  // mean + mean_low: the mean (0 for the RMS norm)
+};
+
 // The wave's part of row `row`: chunks first, first + step, ... (NCH of them) of
-// 512 elements, 8 per lane. Computes and stores h, and returns the row's mean (0
-// for the RMS norm) and 1 / sqrt(...). total(i, v): the row's i-th sum.
-template <int RES, int NCH, typename Total>
-__device__ __forceinline__ void make_h(const BlockNormArgs& p, const Vectors& vec, int64_t row, int first, int step,
-                                       int lane, Held<RES> (&h)[NCH], double& mean, double& rstd, Total&& total) {
+// 512 elements, 8 per lane. Computes and stores h, and returns the row's
+// statistics. total(i, v): the row's sum of its waves' i-th sums.
+template <int RES, bool VF32, int NCH, typename Total>
+__device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vectors& vec, int64_t row, int first, int step,
+                                             int lane, Held<RES> (&h)[NCH], Total&& total) {
   i32x4 xv[NCH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
@@ -93,139 +131,132 @@ __device__ __forceinline__ void make_h(const BlockNormArgs& p, const Vectors& ve
       if constexpr (RES == RES_F32) h[c].w[4 + u] = (uint32_t)rb[u];
     }
   }
-  double post = 1.0;
-  if (p.post) {
-    double sum = 0.0;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const double a = (double)bf16_lo((uint32_t)xv[c][u]), b = (double)bf16_hi((uint32_t)xv[c][u]);
-        sum = __builtin_fma(a, a, sum);
-        sum = __builtin_fma(b, b, sum);
-      }
-    post = rstd_of(p, total(0, sum));
+  auto hold_x = [&]() {  // as hold() below, of x
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         int w = xv[c][u];
-        asm volatile("" : "+v"(w));  // no f64 conversions kept from above
+        asm volatile("" : "+v"(w));
         xv[c][u] = w;
       }
+  };
+  // Words of a second, rare pass over the same elements: values of their own to the
+  // compiler, which would keep the first pass's conversions for it.
+  auto again = [](uint32_t w) {
+    uint32_t zero = 0;
+    asm volatile("" : "+v"(zero));
+    return w ^ zero;
+  };
+  auto h_again = [&](int c, int i) -> double {
+    if constexpr (RES == RES_F32) return (double)__uint_as_float(again(h[c].w[i]));
+    const uint32_t w = again(h[c].w[i >> 1]);
+    return (double)((i & 1) ? bf16_hi(w) : bf16_lo(w));
+  };
+  // Elements past K are zeros, but not the mean away from it.
+  auto all = [](int) { return true; };
+  auto in = [&](int c) { return (first + c * step) * 512 + 8 * lane < p.K; };
+  auto x_at = [&](int c, int i) { return (i & 1) ? bf16_hi((uint32_t)xv[c][i >> 1]) : bf16_lo((uint32_t)xv[c][i >> 1]); };
+  float post = 1.f;
+  if (p.post) {
+    double sum = total(0, sum_of<false, true, NCH>(all, x_at));
+    if (out_of_range(p, sum))
+      sum = total(1, sum_of<true, true, NCH>(all, [&](int c, int i) -> double {
+                    const uint32_t w = again((uint32_t)xv[c][i >> 1]);
+                    return (double)((i & 1) ? bf16_hi(w) : bf16_lo(w));
+                  }));
+    hold_x();
+    post = (float)rstd_of(p, sum);
   }
-  double sum = 0.0;
+  Eight<VF32> pw, ga;
+  pw.load(vec.post, first * 512 + 8 * lane);
+  ga.load(vec.gate, first * 512 + 8 * lane);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int k = (first + c * step) * 512 + 8 * lane;
-    if (k < p.K) {
-      double d[8];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        d[2 * u] = (double)bf16_lo((uint32_t)xv[c][u]);
-        d[2 * u + 1] = (double)bf16_hi((uint32_t)xv[c][u]);
-      }
-      if (p.post) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= post;
-        if (vec.post != nullptr) {
-          float g[8];
-          vector8(vec.post, k, p.vectors_f32, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] *= (double)g[i];
-        }
-      }
-      if (vec.gate != nullptr) {
-        float g[8];
-        vector8(vec.gate, k, p.vectors_f32, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] *= (double)g[i];
-      }
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = round_f32(__builtin_fma(p.residual_scale, (double)h[c].at(i), d[i]));
-      if constexpr (RES == RES_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[c].w[i] = __float_as_uint(f[i]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) h[c].w[u] = pack_bf16(f[2 * u], f[2 * u + 1]);
-      }
-      if (p.residual_out != nullptr) {
-        if constexpr (RES == RES_F32) {
-          float* o = (float*)p.residual_out + row * p.ldo + k;
-          *(i32x4*)o = i32x4{(int)h[c].w[0], (int)h[c].w[1], (int)h[c].w[2], (int)h[c].w[3]};
-          *(i32x4*)(o + 4) = i32x4{(int)h[c].w[4], (int)h[c].w[5], (int)h[c].w[6], (int)h[c].w[7]};
-        } else {
-          *(i32x4*)((uint16_t*)p.residual_out + row * p.ldo + k) =
-              i32x4{(int)h[c].w[0], (int)h[c].w[1], (int)h[c].w[2], (int)h[c].w[3]};
-        }
-      }
-    }
+    float d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const double v = (double)h[c].at(i);
-      sum = p.layer ? sum + v : __builtin_fma(v, v, sum);
+      d[i] = x_at(c, i) * post * (pw.at(i) + vec.post.rest);
+      d[i] *= ga.at(i) + vec.gate.rest;
+      d[i] = __builtin_fmaf(p.residual_scale, h[c].at(i), d[i]);
     }
-  }
-  mean = 0.0;
-  sum = total(1, sum);
-  if (p.layer) {
-    mean = sum / (double)p.K;
-    hold(h);
-    double sq = 0.0;
+    if (c + 1 < NCH) {
+      pw.load(vec.post, k + step * 512);
+      ga.load(vec.gate, k + step * 512);
+    }
+    if constexpr (RES == RES_F32) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      if ((first + c * step) * 512 + 8 * lane >= p.K) continue;
+      for (int i = 0; i < 8; ++i) h[c].w[i] = __float_as_uint(d[i]);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double v = (double)h[c].at(i) - mean;
-        sq = __builtin_fma(v, v, sq);
+      for (int u = 0; u < 4; ++u) h[c].w[u] = pack_bf16(d[2 * u], d[2 * u + 1]);
+    }
+    if (p.residual_out != nullptr && k < p.K) {
+      if constexpr (RES == RES_F32) {
+        float* o = (float*)p.residual_out + row * p.ldo + k;
+        *(i32x4*)o = i32x4{(int)h[c].w[0], (int)h[c].w[1], (int)h[c].w[2], (int)h[c].w[3]};
+        *(i32x4*)(o + 4) = i32x4{(int)h[c].w[4], (int)h[c].w[5], (int)h[c].w[6], (int)h[c].w[7]};
+      } else {
+        *(i32x4*)((uint16_t*)p.residual_out + row * p.ldo + k) =
+            i32x4{(int)h[c].w[0], (int)h[c].w[1], (int)h[c].w[2], (int)h[c].w[3]};
       }
     }
-    sum = total(2, sq);
   }
-  rstd = rstd_of(p, sum);
+  Statistics st = {0.f, 0.f, 0.f};
+  double m = 0.0;
+  if (p.layer) {
+    auto at = [&](int c, int i) { return h[c].at(i); };
+    hold(h);
+    m = total(2, sum_of<false, false, NCH>(all, at));
+    if (!(__builtin_fabs(m) < 1e38)) m = total(3, sum_of<true, false, NCH>(all, h_again));
+    m /= (double)p.K;
+    st.mean = (float)m;
+    st.mean_low = (float)(m - (double)st.mean);
+  }
   hold(h);
+  double sum = total(4, sum_of<false, true, NCH>(in, [&](int c, int i) { return h[c].at(i) - st.mean - st.mean_low; }));
+  if (out_of_range(p, sum))
+    sum = total(5, sum_of<true, true, NCH>(in, [&](int c, int i) { return h_again(c, i) - m; }));
+  hold(h);
+  st.rstd = (float)rstd_of(p, sum);
+  return st;
 }
 
+// The vectors of a chunk's y.
+template <bool VF32>
+struct After {
+  Eight<VF32> weight, scale, shift;
+  __device__ __forceinline__ void load(const Vectors& v, int k) {
+    weight.load(v.weight, k);
+    scale.load(v.scale, k);
+    shift.load(v.shift, k);
+  }
+};
+
 // The bf16 y of a lane's 8 elements at k, as packed pairs (zeros past K).
-template <int RES>
-__device__ __forceinline__ void make_y(const BlockNormArgs& p, const Vectors& vec, int64_t row, const Held<RES>& h, int k,
-                                       double mean, double rstd, uint32_t (&out)[4]) {
-  out[0] = out[1] = out[2] = out[3] = 0;
-  if (k >= p.K) return;
-  double d[8];
+template <int RES, bool VF32>
+__device__ __forceinline__ void make_y(const BlockNormArgs& p, const Vectors& vec, const After<VF32>& a, int64_t row,
+                                       const Held<RES>& h, int k, const Statistics& st, uint32_t (&out)[4]) {
+  float d[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) d[i] = ((double)h.at(i) - mean) * rstd;
-  float g[8];
-  if (vec.weight != nullptr) {
-    vector8(vec.weight, k, p.vectors_f32, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= (double)g[i];
+  for (int i = 0; i < 8; ++i) {
+    d[i] = (h.at(i) - st.mean - st.mean_low) * st.rstd * (a.weight.at(i) + vec.weight.rest);
+    d[i] = __builtin_fmaf(d[i], a.scale.at(i), d[i]) + a.shift.at(i);
   }
-  if (vec.scale != nullptr) {
-    vector8(vec.scale, k, p.vectors_f32, g);
+  const bool in = k < p.K;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] *= 1.0 + (double)g[i];
-  }
-  if (vec.shift != nullptr) {
-    vector8(vec.shift, k, p.vectors_f32, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] += (double)g[i];
-  }
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = round_f32(d[i]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-  if (p.y != nullptr)
+  for (int i = 0; i < 4; ++i) out[i] = in ? pack_bf16(d[2 * i], d[2 * i + 1]) : 0u;
+  if (p.y != nullptr && in)
     *(i32x4*)((uint16_t*)p.y + row * p.ldy + k) = i32x4{(int)out[0], (int)out[1], (int)out[2], (int)out[3]};
 }
 
+// Two blocks of 8 waves a CU where a row's registers allow it.
+constexpr int waves_wanted(int res, int nch) { return nch <= (res == RES_F32 ? 8 : 10) ? 4 : 2; }
+
 // Many rows: a block takes 8, a wave each; the codes pass through LDS.
-template <int RES, bool FP4, int NCH>
-__global__ __launch_bounds__(64 * kTileRows, 2) void block_norm_tile_kernel(BlockNormArgs p) {
+template <int RES, bool VF32, bool FP4, int NCH>
+__global__ __launch_bounds__(64 * kTileRows, waves_wanted(RES, NCH)) void block_norm_tile_kernel(BlockNormArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using St = Stage<FP4>;
   const int t = threadIdx.x, lane = t & 63, rl = t >> 6;
@@ -235,17 +266,20 @@ __global__ __launch_bounds__(64 * kTileRows, 2) void block_norm_tile_kernel(Bloc
   const int64_t row = r0 + rl;
   const bool real = row < p.M;
   Held<RES> h[NCH];
-  double mean = 0.0, rstd = 0.0;
-  Vectors vec = {nullptr, nullptr, nullptr, nullptr, nullptr};
+  Statistics stats = {0.f, 0.f, 0.f};
+  const Vectors vec = vectors_of<VF32>(p, real ? row : p.M - 1);
   if (real) {
-    vec = vectors_of(p, row);
-    make_h<RES, NCH>(p, vec, row, 0, 1, lane, h, mean, rstd, [](int, double v) { return wave_sum(v); });
+    stats = make_h<RES, VF32, NCH>(p, vec, row, 0, 1, lane, h, [](int, double v) { return wave_sum(v); });
   }
+  After<VF32> after;
+  after.load(vec, 8 * lane);
 #pragma unroll
   for (int ch = 0; ch < NCH; ++ch) {
     const int k = ch * 512 + 8 * lane;
     uint32_t v[4] = {0, 0, 0, 0};
-    if (real) make_y(p, vec, row, h[ch], k, mean, rstd, v);
+    if (real) make_y(p, vec, after, row, h[ch], k, stats, v);
+    if (ch + 1 < NCH) after.load(vec, k + 512);
+    __builtin_amdgcn_sched_barrier(0);
     if (p.q == nullptr) continue;
     if constexpr (FP4) {
       uint32_t sc;
@@ -286,9 +320,9 @@ __global__ __launch_bounds__(64 * kTileRows, 2) void block_norm_tile_kernel(Bloc
 
 // Few rows. Blocks 0 .. M-1: one row each, WPR waves. Blocks M ..: pad rows of one
 // slab.
-template <int RES, bool FP4, int WPR, int NCH>
+template <int RES, bool VF32, bool FP4, int WPR, int NCH>
 __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs p) {
-  __shared__ double part[3][WPR];
+  __shared__ double part[6][WPR];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int S = Stage<FP4>::slabs((int)p.K);
   if ((int64_t)blockIdx.x >= p.M) {
@@ -305,10 +339,9 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
     return;
   }
   const int64_t row = blockIdx.x;
-  const Vectors vec = vectors_of(p, row);
+  const Vectors vec = vectors_of<VF32>(p, row);
   Held<RES> h[NCH];
-  double mean, rstd;
-  make_h<RES, NCH>(p, vec, row, wave, WPR, lane, h, mean, rstd, [&](int i, double v) {
+  const Statistics stats = make_h<RES, VF32, NCH>(p, vec, row, wave, WPR, lane, h, [&](int i, double v) {
     v = wave_sum(v);
     if (lane == 0) part[i][wave] = v;
     __syncthreads();
@@ -317,12 +350,15 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
     for (int w = 0; w < WPR; ++w) sum += part[i][w];
     return sum;
   });
+  After<VF32> after;
+  after.load(vec, wave * 512 + 8 * lane);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int ch = wave + c * WPR;
     const int k = ch * 512 + 8 * lane;
     uint32_t v[4];
-    make_y(p, vec, row, h[c], k, mean, rstd, v);
+    make_y(p, vec, after, row, h[c], k, stats, v);
+    if (c + 1 < NCH) after.load(vec, k + WPR * 512);
     if (p.q == nullptr) continue;
     if constexpr (FP4) {
       uint32_t sc;
@@ -345,20 +381,20 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
   }
 }
 
-template <int RES, bool FP4, int NCH>
+template <int RES, bool VF32, bool FP4, int NCH>
 hipError_t launch_tile(const BlockNormArgs& p, hipStream_t st) {
   static std::atomic<uint64_t> configured{0};  // per instantiation
-  auto kern = block_norm_tile_kernel<RES, FP4, NCH>;
+  auto kern = block_norm_tile_kernel<RES, VF32, FP4, NCH>;
   const hipError_t e = allow_dynamic_lds((const void*)kern, Stage<FP4>::bytes(512 * NCH), configured);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(p.R / kTileRows)), dim3(64 * kTileRows), Stage<FP4>::bytes((int)p.K), st, p);
   return hipGetLastError();
 }
 
-template <int RES, bool FP4, int WPR, int NCH>
+template <int RES, bool VF32, bool FP4, int WPR, int NCH>
 hipError_t launch_row(const BlockNormArgs& p, hipStream_t st) {
   const unsigned blocks = (unsigned)(p.M + (p.q != nullptr && p.R > p.M ? Stage<FP4>::slabs((int)p.K) : 0));
-  hipLaunchKernelGGL((block_norm_row_kernel<RES, FP4, WPR, NCH>), dim3(blocks), dim3(64 * WPR), 0, st, p);
+  hipLaunchKernelGGL((block_norm_row_kernel<RES, VF32, FP4, WPR, NCH>), dim3(blocks), dim3(64 * WPR), 0, st, p);
   return hipGetLastError();
 }
 
@@ -366,29 +402,34 @@ hipError_t launch_row(const BlockNormArgs& p, hipStream_t st) {
 constexpr int64_t kTileMinRows = 32768;
 constexpr int64_t kTileMinRowsShort = 2048;  // K <= 2048
 
-template <int RES, bool FP4>
+template <int RES, bool VF32, bool FP4>
 hipError_t dispatch(const BlockNormArgs& p, hipStream_t st) {
   const int ch = (int)((p.K + 511) / 512);
   if (p.M >= (ch <= 4 ? kTileMinRowsShort : kTileMinRows)) {
-    if (ch <= 4) return launch_tile<RES, FP4, 4>(p, st);
-    if (ch <= 8) return launch_tile<RES, FP4, 8>(p, st);
-    if (ch <= 10) return launch_tile<RES, FP4, 10>(p, st);
+    if (ch <= 4) return launch_tile<RES, VF32, FP4, 4>(p, st);
+    if (ch <= 8) return launch_tile<RES, VF32, FP4, 8>(p, st);
+    if (ch <= 10) return launch_tile<RES, VF32, FP4, 10>(p, st);
     if constexpr (RES != RES_F32)  // an f32 row of 16 chunks does not fit the registers
-      if (ch <= 16) return launch_tile<RES, FP4, 16>(p, st);
+      if (ch <= 16) return launch_tile<RES, VF32, FP4, 16>(p, st);
   }
-  if (ch <= 8) return launch_row<RES, FP4, 4, 2>(p, st);
-  if (ch <= 12) return launch_row<RES, FP4, 4, 3>(p, st);
-  if (ch <= 16) return launch_row<RES, FP4, 4, 4>(p, st);
-  if (ch <= 24) return launch_row<RES, FP4, 8, 3>(p, st);
-  if (ch <= 32) return launch_row<RES, FP4, 8, 4>(p, st);
-  return launch_row<RES, FP4, 8, 16>(p, st);
+  if (ch <= 8) return launch_row<RES, VF32, FP4, 4, 2>(p, st);
+  if (ch <= 12) return launch_row<RES, VF32, FP4, 4, 3>(p, st);
+  if (ch <= 16) return launch_row<RES, VF32, FP4, 4, 4>(p, st);
+  if (ch <= 24) return launch_row<RES, VF32, FP4, 8, 3>(p, st);
+  if (ch <= 32) return launch_row<RES, VF32, FP4, 8, 4>(p, st);
+  return launch_row<RES, VF32, FP4, 8, 16>(p, st);
+}
+
+template <int RES, bool VF32>
+hipError_t dispatch(const BlockNormArgs& p, hipStream_t st) {
+  return p.fp4 ? dispatch<RES, VF32, true>(p, st) : dispatch<RES, VF32, false>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_block_norm_slab(const BlockNormArgs& a, hipStream_t stream) {
-  if (a.residual_f32) return a.fp4 ? dispatch<RES_F32, true>(a, stream) : dispatch<RES_F32, false>(a, stream);
-  return a.fp4 ? dispatch<RES_BF16, true>(a, stream) : dispatch<RES_BF16, false>(a, stream);
+  if (a.residual_f32) return a.vectors_f32 ? dispatch<RES_F32, true>(a, stream) : dispatch<RES_F32, false>(a, stream);
+  return a.vectors_f32 ? dispatch<RES_BF16, true>(a, stream) : dispatch<RES_BF16, false>(a, stream);
 }
 
 }  // namespace mx

@@ -193,7 +193,8 @@ struct BlockNormArgs {
   int64_t ldx;
   const void* residual;
   int64_t ldr;
-  double residual_scale, eps;
+  double eps;
+  float residual_scale;
   const void *post_weight, *gate, *weight, *scale, *shift;
   int64_t gate_period, ldg, mod_period, ldm;
   int64_t M, R, K;  // R = slab_rows(M)
