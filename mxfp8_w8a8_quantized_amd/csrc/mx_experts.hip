@@ -32,12 +32,15 @@ namespace mx {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int NT = 256;
 constexpr int MT = kExpertTile;  // pairs per tile
 constexpr int JB = 4;            // and their fragments of 32
 constexpr int PLAN_THREADS = 1024;
+constexpr int kPlanChunk = 4096;  // pairs
 
 template <int B, int E, typename F>
 __device__ __forceinline__ void static_for(F&& f) {
@@ -62,27 +65,40 @@ struct PrepareParams {
   int32_t* pos;   // pair -> sorted row, or -1
   ExpertTile* tiles;
   int32_t* n_tiles;
+  int chunks;
+  int32_t* counts;  // [chunks][kMaxExperts], with more than one chunk
 };
 
-// One workgroup: a histogram of the experts in LDS, its running sum and the tiles,
-// then a place for each pair. The order of an expert's pairs is that in which the
-// threads come; no output depends on it, since every row of a tile is computed
-// alike.
-__device__ __forceinline__ void make_plan(const PrepareParams& p) {
-  __shared__ int32_t count[kMaxExperts], next[kMaxExperts];
-  __shared__ int32_t part[2][PLAN_THREADS / 64];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int P = p.T * p.k;
-  for (int e = t; e < kMaxExperts; e += PLAN_THREADS) count[e] = 0;
+// The plan. A chunk is kPlanChunk pairs, one workgroup's: a histogram of the experts
+// in LDS gives each pair its place among the chunk's pairs of its expert. With one
+// chunk (PLACE follows at once) the running sum over the experts makes it a row;
+// with more, a second kernel first adds the histograms of the chunks before. The
+// order of an expert's pairs is that in which the threads come; no output depends
+// on it, since every row of a tile is computed alike.
+struct Pairs {
+  int32_t e[kPlanChunk / PLAN_THREADS], place[kPlanChunk / PLAN_THREADS];
+};
+__device__ __forceinline__ void count_chunk(const PrepareParams& p, int chunk, int32_t* count, Pairs& q) {
+  const int t = threadIdx.x, P = p.T * p.k;
+  count[t] = 0;
   __syncthreads();
-  for (int i = t; i < P; i += PLAN_THREADS) {
-    const int32_t e = p.ids[i];
-    if (e >= 0 && e < p.E) atomicAdd(&count[e], 1);
+#pragma unroll
+  for (int u = 0; u < kPlanChunk / PLAN_THREADS; ++u) {
+    const int i = chunk * kPlanChunk + u * PLAN_THREADS + t;
+    int32_t e = i < P ? p.ids[i] : -1;
+    if (e >= p.E) e = -1;
+    q.e[u] = e;
+    if (e >= 0) q.place[u] = atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  // A thread an expert: running sums of pairs and of tiles.
-  const int n = count[t], tiles = (n + MT - 1) / MT;
-  int sn = n, st = tiles;
+}
+// Thread e: expert e has n pairs, the chunk's begin at `before` among them. first[e]
+// becomes the chunk's first row of the expert; `tiles`: write them down.
+__device__ __forceinline__ void place_experts(const PrepareParams& p, int n, int before, bool tiles, int32_t* first) {
+  __shared__ int32_t part[2][PLAN_THREADS / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int nt = (n + MT - 1) / MT;
+  int sn = n, st = nt;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int un = __shfl_up(sn, off, 64), ut = __shfl_up(st, off, 64);
@@ -100,32 +116,72 @@ __device__ __forceinline__ void make_plan(const PrepareParams& p) {
     sn += part[0][w];
     st += part[1][w];
   }
-  const int first = sn - n;
-  next[t] = first;
-  for (int i = 0; i < tiles; ++i) p.tiles[st - tiles + i] = {t, first + i * MT, min(n - i * MT, MT), 0};
-  if (t == PLAN_THREADS - 1) *p.n_tiles = st;
+  first[t] = sn - n + before;
+  if (tiles) {
+    for (int i = 0; i < nt; ++i) p.tiles[st - nt + i] = {t, sn - n + i * MT, min(n - i * MT, MT), 0};
+    if (t == PLAN_THREADS - 1) *p.n_tiles = st;
+  }
   __syncthreads();
-  for (int i = t; i < P; i += PLAN_THREADS) {
-    const int32_t e = p.ids[i];
-    int r = -1;
-    if (e >= 0 && e < p.E) {
-      r = atomicAdd(&next[e], 1);
-      p.rows[r] = i;
-    }
+}
+__device__ __forceinline__ void place_pairs(const PrepareParams& p, int chunk, const int32_t* first, const Pairs& q) {
+  const int t = threadIdx.x, P = p.T * p.k;
+#pragma unroll
+  for (int u = 0; u < kPlanChunk / PLAN_THREADS; ++u) {
+    const int i = chunk * kPlanChunk + u * PLAN_THREADS + t;
+    if (i >= P) continue;
+    const int r = q.e[u] >= 0 ? first[q.e[u]] + q.place[u] : -1;
     p.pos[i] = r;
+    if (r >= 0) p.rows[r] = i;
   }
 }
 static_assert(kMaxExperts == PLAN_THREADS, "a thread an expert");
 
-// Workgroup 0 makes the plan; each wave of the others takes a token's row.
+// The chunks' second pass.
+__global__ __launch_bounds__(PLAN_THREADS) void place_kernel(PrepareParams p) {
+  __shared__ int32_t first[kMaxExperts];
+  const int t = threadIdx.x, chunk = blockIdx.x;
+  int n = 0, before = 0;
+  for (int c = 0; c < p.chunks; ++c) {
+    const int v = p.counts[c * kMaxExperts + t];
+    if (c < chunk) before += v;
+    n += v;
+  }
+  Pairs q;
+  const int P = p.T * p.k;
+#pragma unroll
+  for (int u = 0; u < kPlanChunk / PLAN_THREADS; ++u) {
+    const int i = chunk * kPlanChunk + u * PLAN_THREADS + t;
+    int32_t e = i < P ? p.ids[i] : -1;
+    if (e >= p.E) e = -1;
+    q.e[u] = e;
+    q.place[u] = e >= 0 ? p.pos[i] : 0;
+  }
+  place_experts(p, n, before, chunk == 0, first);
+  place_pairs(p, chunk, first, q);
+}
+
+// The first workgroups count a chunk of pairs each (the only one makes the plan);
+// each wave of the others takes a token's row.
 template <bool X8>
 __global__ __launch_bounds__(PLAN_THREADS) void prepare_kernel(PrepareParams p) {
-  if (blockIdx.x == 0) {
-    make_plan(p);
+  if ((int)blockIdx.x < p.chunks) {
+    __shared__ int32_t count[kMaxExperts];
+    const int t = threadIdx.x, chunk = blockIdx.x;
+    Pairs q;
+    count_chunk(p, chunk, count, q);
+    if (p.chunks == 1) {
+      place_experts(p, count[t], 0, true, count);
+      place_pairs(p, 0, count, q);
+    } else {
+      p.counts[chunk * kMaxExperts + t] = count[t];
+#pragma unroll
+      for (int u = 0; u < kPlanChunk / PLAN_THREADS; ++u)
+        if (q.e[u] >= 0) p.pos[chunk * kPlanChunk + u * PLAN_THREADS + t] = q.place[u];
+    }
     return;
   }
   const int lane = threadIdx.x & 63;
-  const int64_t row = ((int64_t)blockIdx.x - 1) * (PLAN_THREADS / 64) + (threadIdx.x >> 6);
+  const int64_t row = ((int64_t)blockIdx.x - p.chunks) * (PLAN_THREADS / 64) + (threadIdx.x >> 6);
   if (row >= p.T) return;
   const uint16_t* x = p.x + row * p.ldx;
   uint8_t* q = p.xq + row * p.pitch_q;
@@ -169,7 +225,9 @@ struct ProductParams {
   uint8_t* hq;  // up: h's codes and scales
   uint8_t* hs;
   uint32_t hpitch_q, hpitch_s;
-  float* o;  // down: [pairs][H]
+  uint16_t* o;  // down: f16 [pairs][H]
+  uint8_t* os;  // and the exponents of 32 columns
+  uint32_t opitch_s;
 };
 
 template <bool X8>
@@ -179,7 +237,7 @@ struct Shape {
   static constexpr int REGION = MT * ROW;
   static constexpr int NX = ROW * MT / 4096;    // row DMAs per wave and step
   static constexpr int L = NX + 3;              // loads per wave and step: rows, weights (2), their scales
-  static constexpr int XS_SLOT = MT * 32;       // scales of 8 steps
+  static constexpr int XS_SLOT = MT * 32;       // scales of 8 steps: [32 rows][4 steps][row][16]
   static constexpr int XS = D * REGION;
   static constexpr int LDS = XS + 2 * XS_SLOT;
   static constexpr int NB = X8 ? 2 : 1;         // 16-byte reads per fragment and MFMA
@@ -209,23 +267,26 @@ struct Source {
   int R, nsteps;
 };
 
+// 16 bytes a lane from `offset` into LDS, lane by lane from `to` on.
+__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 16, offset, 0, 0, 0);
+}
+
 // Loads of step j (past the last one zeros from an empty resource, so that every
 // step has the same number of them).
-template <bool X8>
-__device__ __forceinline__ void load_rows(const Source<X8>& S, uint8_t* smem, int j, int wave) {
+template <int V, bool X8>
+__device__ __forceinline__ void load_rows(const Source<X8>& S, uint8_t* smem, int j, int wave) {  // V = j % 8
   using Sh = Shape<X8>;
   const bool on = j < S.nsteps;
-  if (j % 8 == 0) {
+  if constexpr (V == 0) {
     const __amdgpu_buffer_rsrc_t r = make_rsrc(S.xs + (int64_t)j * 4, on ? S.xs_bytes - (uint32_t)j * 4u : 0u);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(smem + Sh::XS + (j / 8 % 2) * Sh::XS_SLOT + wave * 1024), 16,
-                                             S.xso, 0, 0, 0);
+    dma(r, smem + Sh::XS + (j / 8 % 2) * Sh::XS_SLOT + wave * 1024, S.xso);
   }
   const __amdgpu_buffer_rsrc_t r =
       make_rsrc(S.x + (int64_t)j * Sh::ROW, on ? S.x_bytes - (uint32_t)(j * Sh::ROW) : 0u);
-  uint8_t* reg = smem + (j % Sh::D) * Sh::REGION + wave * (Sh::NX * 1024);
+  uint8_t* reg = smem + (V % Sh::D) * Sh::REGION + wave * (Sh::NX * 1024);
 #pragma unroll
-  for (int i = 0; i < Sh::NX; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(reg + i * 1024), 16, S.xo[i], 0, 0, 0);
+  for (int i = 0; i < Sh::NX; ++i) dma(r, reg + i * 1024, S.xo[i]);
 }
 template <bool X8>
 __device__ __forceinline__ void load_weights(Weights& W, const Source<X8>& S, int j) {
@@ -240,11 +301,11 @@ __device__ __forceinline__ void load_weights(Weights& W, const Source<X8>& S, in
 // Fragments of MFMA set `s` of step j. Lane half h of the set takes group 2 h + s
 // of the step's four (mx_fp4_gemm.hip says why that is free); E4M3: 16 elements of
 // group s, then 16 of group 2 + s.
-template <bool X8, int s>
-__device__ __forceinline__ void read_half(Half<X8>& F, const uint8_t* smem, int j, int lane) {
+template <bool X8, int s, int D>
+__device__ __forceinline__ void read_half(Half<X8>& F, const uint8_t* smem, int lane) {  // D: the step's region
   using Sh = Shape<X8>;
   const int r32 = lane & 31, hi = lane >> 5, sw = Sh::swizzle(r32);
-  const uint8_t* row = smem + (j % Sh::D) * Sh::REGION + r32 * Sh::ROW;
+  const uint8_t* row = smem + D * Sh::REGION + r32 * Sh::ROW;
 #pragma unroll
   for (int f = 0; f < JB; ++f) {
     if constexpr (X8) {
@@ -255,12 +316,15 @@ __device__ __forceinline__ void read_half(Half<X8>& F, const uint8_t* smem, int 
     }
   }
 }
-template <bool X8>
-__device__ __forceinline__ void read_scales(int (&sb)[JB], const uint8_t* smem, int j, int lane) {
+// The rows' scales of the four steps from j on, V = j % 8: the 16 bytes of each row of
+// the four fragments in one conflict-free read (two bytes a row and step cost 15
+// cycles of bank conflicts each).
+template <bool X8, int V>
+__device__ __forceinline__ void read_scales(i32x4 (&q)[JB], const uint8_t* smem, int j, int lane) {
   using Sh = Shape<X8>;
-  const uint8_t* p = smem + Sh::XS + (j / 8 % 2) * Sh::XS_SLOT + (lane & 31) * 32 + (j % 8) * 4 + 2 * (lane >> 5);
+  const uint8_t* p = smem + Sh::XS + (j / 8 % 2) * Sh::XS_SLOT + V / 4 * 512 + (lane & 31) * 16;
 #pragma unroll
-  for (int f = 0; f < JB; ++f) sb[f] = *(const uint16_t*)(p + f * 1024);
+  for (int f = 0; f < JB; ++f) q[f] = *(const i32x4*)(p + f * 1024);
 }
 
 template <bool X8, int s>
@@ -280,10 +344,48 @@ __device__ __forceinline__ void mma_half(f32x16 (&acc)[JB], const Weights& W, co
   });
 }
 
-// acc = the wave's 32 weight rows x 128 pairs. Step j: MFMA set 0 while set 1's
-// fragments are read; one barrier, behind which step j + 1's rows are there and
-// every wave is done with step j's; set 1 while step j + 1's first fragments are
-// read and step j + D is sent for into the place of step j.
+// Step j, V = j % 8: MFMA set 0 while set 1's fragments are read; one barrier, behind
+// which step j + 1's rows are there and every wave is done with step j's; set 1 while
+// step j + 1's first fragments are read and step j + D is sent for into the place of
+// step j.
+template <int V, bool X8>
+__device__ __forceinline__ void step(f32x16 (&acc)[JB], Weights (&W)[Shape<X8>::D], Half<X8>& F0, Half<X8>& F1,
+                                     i32x4 (&q)[JB], const Source<X8>& S, uint8_t* smem, int j, int wave, int lane) {
+  using Sh = Shape<X8>;
+  // Lane half h: the scales of groups 2 h and 2 h + 1 in bytes 0 and 1.
+  int sb[JB];
+#pragma unroll
+  for (int f = 0; f < JB; ++f) sb[f] = (int)((uint32_t)q[f][V % 4] >> (lane >> 5 << 4));
+  constexpr int D = Sh::D, v = V, d = V % D, refill = (V + D) % 8;
+  read_half<X8, 1, d>(F1, smem, lane);
+  mma_half<X8, 0>(acc, W[d], F0, sb);
+  static_for<0, JB>([&](auto I) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (decltype(I)::value < 2) __builtin_amdgcn_sched_group_barrier(0x100, 2 * Sh::NB, 0);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+  // Younger loads than step j + 1's. The lgkmcnt(0) keeps the refill from
+  // overtaking another wave's reads.
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((D - 2) * Sh::L) : "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  read_half<X8, 0, (d + 1) % D>(F0, smem, lane);
+  if constexpr (V % 4 == 3) read_scales<X8, (V + 1) % 8>(q, smem, j + 1, lane);
+  load_rows<refill>(S, smem, j + D, wave);
+  load_weights(W[(d + D - 1) % D], S, j + D - 1);
+  mma_half<X8, 1>(acc, W[d], F1, sb);
+  static_for<0, JB>([&](auto I) {
+    constexpr int i = decltype(I)::value;
+    constexpr int loads = Sh::L + (refill == 0 ? 1 : 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, Sh::NB + (V % 4 == 3 ? 1 : 0), 0);
+    if constexpr (loads * (i + 1) / JB > loads * i / JB)
+      __builtin_amdgcn_sched_group_barrier(0x020, loads * (i + 1) / JB - loads * i / JB, 0);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// acc = the wave's 32 weight rows x 128 pairs.
 template <bool X8>
 __device__ __forceinline__ void product(f32x16 (&acc)[JB], const Source<X8>& S, uint8_t* smem, int wave, int lane) {
   using Sh = Shape<X8>;
@@ -291,7 +393,7 @@ __device__ __forceinline__ void product(f32x16 (&acc)[JB], const Source<X8>& S, 
   Weights W[D];
   static_for<0, D>([&](auto V) {
     constexpr int v = decltype(V)::value;
-    load_rows(S, smem, v, wave);
+    load_rows<v>(S, smem, v, wave);
     if constexpr (v > 0) load_weights(W[v - 1], S, v - 1);
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -305,35 +407,17 @@ __device__ __forceinline__ void product(f32x16 (&acc)[JB], const Source<X8>& S, 
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
   Half<X8> F0, F1;
-  int sb[2][JB];
-  read_half<X8, 0>(F0, smem, 0, lane);
-  read_scales<X8>(sb[0], smem, 0, lane);
-  // TAIL: the last nsteps % D steps, which load nothing more.
-  auto step = [&](auto V, auto TAIL, int j) {
-    constexpr int v = decltype(V)::value;
-    constexpr bool tail = decltype(TAIL)::value;
-    read_half<X8, 1>(F1, smem, j, lane);
-    mma_half<X8, 0>(acc, W[v], F0, sb[v & 1]);
-    __builtin_amdgcn_sched_barrier(0);
-    // Younger loads than step j + 1's. The lgkmcnt(0) keeps the refill from
-    // overtaking another wave's reads.
-    constexpr int younger = !tail ? D - 2 : D - 2 > v ? D - 2 - v : 0;
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(younger * Sh::L) : "memory");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    read_half<X8, 0>(F0, smem, j + 1, lane);
-    read_scales<X8>(sb[(v + 1) & 1], smem, j + 1, lane);
-    if constexpr (!tail) {
-      load_rows(S, smem, j + D, wave);
-      load_weights(W[(v + D - 1) % D], S, j + D - 1);
-    }
-    mma_half<X8, 1>(acc, W[v], F1, sb[v & 1]);
-    __builtin_amdgcn_sched_barrier(0);
-  };
+  i32x4 q[JB];
+  read_half<X8, 0, 0>(F0, smem, lane);
+  read_scales<X8, 0>(q, smem, 0, lane);
   int j = 0;
-  for (; j + D <= S.nsteps; j += D) static_for<0, D>([&](auto V) { step(V, std::false_type{}, j + decltype(V)::value); });
-  static_for<0, D - 1>([&](auto V) {
-    if (j + decltype(V)::value < S.nsteps) step(V, std::true_type{}, j + decltype(V)::value);
+  for (; j + 8 <= S.nsteps; j += 8)
+    static_for<0, 8>([&](auto V) {
+      step<decltype(V)::value>(acc, W, F0, F1, q, S, smem, j + decltype(V)::value, wave, lane);
+    });
+  static_for<0, 7>([&](auto V) {
+    if (j + decltype(V)::value < S.nsteps)
+      step<decltype(V)::value>(acc, W, F0, F1, q, S, smem, j + decltype(V)::value, wave, lane);
   });
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -435,19 +519,42 @@ __device__ __forceinline__ void store_h(const f32x16 (&acc)[JB], const ProductPa
   if (t < count) *(uint16_t*)(p.hs + (int64_t)(m0 + t) * p.hpitch_s + n0 / 32) = *(const uint16_t*)(scales + 2 * t);
 }
 
-__device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductParams& p, int m0, int count, int n0,
-                                        int wave, int lane) {
+// The tile's outputs o as f16 with a power of two for each 32 columns of a row: 2^-12
+// of a value at most is lost (f32 would be 2^-24, and twice the bytes written here
+// and read by the sum; bf16 2^-9, as much as y's own rounding). The largest of the
+// 32 is brought to [2^14, 2^15); values under 2^-28 of it lose bits. A lane holds 16
+// of a group's 32, lane ^ 32 the others.
+__device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductParams& p, uint8_t* smem, int m0, int count,
+                                        int n0, int wave, int lane) {
+  constexpr int PITCH = 2 * MT + 16;
+  uint8_t* scales = smem + MT * PITCH;  // [row][4]
   const int r32 = lane & 31, hi = lane >> 5;
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
-    if (32 * j + r32 >= count) continue;
-    float* o = p.o + (int64_t)(m0 + 32 * j + r32) * p.H;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, __builtin_fabsf(acc[j][i]));
+    const uint32_t b = __float_as_uint(m);
+    const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t e = min(max(max((uint32_t)sw[0], (uint32_t)sw[1]) >> 23, 15u), 254u);
+    const float f = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
+    uint8_t* row = smem + (32 * j + r32) * PITCH + 64 * wave + 8 * hi;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 32 * wave + 8 * q + 4 * hi;
-      if (n < p.H) *(f32x4*)(o + n) = f32x4{acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+      const f16x2 a = {(_Float16)(acc[j][4 * q] * f), (_Float16)(acc[j][4 * q + 1] * f)};
+      const f16x2 c = {(_Float16)(acc[j][4 * q + 2] * f), (_Float16)(acc[j][4 * q + 3] * f)};
+      *(i32x2*)(row + 16 * q) = i32x2{__builtin_bit_cast(int, a), __builtin_bit_cast(int, c)};
     }
+    if (hi == 0) scales[(32 * j + r32) * 4 + wave] = (uint8_t)e;
   }
+  __syncthreads();
+  const int t = threadIdx.x;
+  for (int u = t; u < count * 16; u += NT) {
+    const int r = u >> 4, c = u & 15;
+    if (n0 + 8 * c < p.H)
+      *(i32x4*)(p.o + (int64_t)(m0 + r) * p.H + n0 + 8 * c) = *(const i32x4*)(smem + r * PITCH + 16 * c);
+  }
+  if (t < count) *(uint32_t*)(p.os + (int64_t)(m0 + t) * p.opitch_s + n0 / 32) = *(const uint32_t*)(scales + 4 * t);
 }
 
 // Tiles in groups of 4 along the pairs x all weight tiles, of which each XCD takes
@@ -502,35 +609,41 @@ __global__ __launch_bounds__(NT, 2) void product_kernel(ProductParams p) {
     const int r = (wave * Sh::NX + i) * (64 / LPR) + lane / LPR;
     S.xo[i] = source_row(r) * p.pitch_q + (uint32_t)(((lane % LPR) ^ Sh::swizzle(r)) * 16);
   }
-  S.xso = source_row(32 * wave + (lane >> 1)) * p.pitch_s + (uint32_t)(lane & 1) * 16u;
+  S.xso = source_row(32 * wave + (lane & 31)) * p.pitch_s + (uint32_t)(lane >> 5) * 16u;
 
   f32x16 acc[JB];
   product(acc, S, smem, wave, lane);
   if constexpr (UP)
     store_h<X8, ACT>(acc, p, smem, tile.first, tile.count, n0, wave, lane);
   else
-    store_o(acc, p, tile.first, tile.count, n0, wave, lane);
+    store_o(acc, p, smem, tile.first, tile.count, n0, wave, lane);
 }
 
 // ---------------------------------------------------------------------------
-// (4) y[t] = bf16(sum_j w[t][j] o[pos[t][j]]), four columns a thread.
+// (4) y[t] = bf16(sum_j w[t][j] o[pos[t][j]]), eight columns a thread.
 
-__global__ __launch_bounds__(NT) void combine_kernel(const float* __restrict__ o, const int32_t* __restrict__ pos,
-                                                     const float* __restrict__ weights, int k, int H, int blocks_row,
+__global__ __launch_bounds__(NT) void combine_kernel(const uint16_t* __restrict__ o, const uint8_t* __restrict__ os,
+                                                     uint32_t opitch_s, const int32_t* __restrict__ pos,
+                                                     const float* __restrict__ weights, int k, int H, int64_t pieces,
                                                      uint16_t* __restrict__ y) {
-  const int64_t t = blockIdx.x / (uint32_t)blocks_row;
-  const int n = (int)(blockIdx.x - (uint32_t)t * (uint32_t)blocks_row) * (4 * NT) + 4 * (int)threadIdx.x;
-  if (n >= H) return;
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t u = (int64_t)blockIdx.x * NT + threadIdx.x;
+  if (u >= pieces) return;
+  const int64_t t = u / (uint32_t)(H / 8);
+  const int n = (int)(u - t * (H / 8)) * 8;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
   for (int j = 0; j < k; ++j) {
     const int r = pos[t * k + j];
     if (r < 0) continue;
-    const float w = weights[t * k + j];
-    const f32x4 a = *(const f32x4*)(o + (int64_t)r * H + n);
+    const uint32_t e = os[(int64_t)r * opitch_s + n / 32];
+    const f16x8 a = *(const f16x8*)(o + (int64_t)r * H + n);
+    const float w = weights[t * k + j], f = __uint_as_float((e - 14u) << 23);  // 2^(e - 127 - 14)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w, a[i], v[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(w, (float)a[i] * f, v[i]);
   }
-  *(i32x2*)(y + t * H + n) = i32x2{(int)pack_bf16(v[0], v[1]), (int)pack_bf16(v[2], v[3])};
+  *(i32x4*)(y + t * H + n) = i32x4{(int)pack_bf16(v[0], v[1]), (int)pack_bf16(v[2], v[3]), (int)pack_bf16(v[4], v[5]),
+                                   (int)pack_bf16(v[6], v[7])};
 }
 
 template <bool UP, bool X8, int ACT>
@@ -563,10 +676,16 @@ hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) 
   q.pos = (int32_t*)(base + w.pos);
   q.tiles = (ExpertTile*)(base + w.tiles);
   q.n_tiles = (int32_t*)(base + w.n_tiles);
-  const unsigned blocks = 1u + (unsigned)((a.T + PLAN_THREADS / 64 - 1) / (PLAN_THREADS / 64));
+  q.chunks = (int)w.chunks;
+  q.counts = (int32_t*)(base + w.counts);
+  const unsigned blocks = (unsigned)(w.chunks + (a.T + PLAN_THREADS / 64 - 1) / (PLAN_THREADS / 64));
   hipLaunchKernelGGL(prepare_kernel<X8>, dim3(blocks), dim3(PLAN_THREADS), 0, st, q);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (w.chunks > 1) {
+    hipLaunchKernelGGL(place_kernel, dim3((unsigned)w.chunks), dim3(PLAN_THREADS), 0, st, q);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
 
   ProductParams p;
   p.x = q.xq;
@@ -590,7 +709,9 @@ hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) 
   p.hs = base + w.hs;
   p.hpitch_q = w.hpitch_q;
   p.hpitch_s = w.hpitch_s;
-  p.o = (float*)(base + w.o);
+  p.o = (uint16_t*)(base + w.o);
+  p.os = base + w.os;
+  p.opitch_s = w.opitch_s;
   e = a.gate == 1 ? launch_product<true, X8, 1>(p, max_tiles, st) : launch_product<true, X8, 0>(p, max_tiles, st);
   if (e != hipSuccess) return e;
 
@@ -606,9 +727,9 @@ hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) 
   e = launch_product<false, X8, 0>(p, max_tiles, st);
   if (e != hipSuccess) return e;
 
-  const int blocks_row = (int)((a.H + 4 * NT - 1) / (4 * NT));
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)(a.T * blocks_row)), dim3(NT), 0, st, p.o, q.pos, a.weights, (int)a.k,
-                     (int)a.H, blocks_row, (uint16_t*)a.y);
+  const int64_t pieces = a.T * (a.H / 8);
+  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)((pieces + NT - 1) / NT)), dim3(NT), 0, st, p.o, p.os, p.opitch_s, q.pos,
+                     a.weights, (int)a.k, (int)a.H, pieces, (uint16_t*)a.y);
   return hipGetLastError();
 }
 
@@ -632,11 +753,15 @@ ExpertsWorkspace experts_workspace(int64_t T, int64_t k, int64_t E, int64_t H, i
   w.xs = take(T * w.xpitch_s);
   w.hq = take(P * w.hpitch_q);
   w.hs = take(P * w.hpitch_s);
-  w.o = take(P * H * 4);
+  w.opitch_s = (uint32_t)((H + 127) / 128 * 4);
+  w.o = take(P * H * 2);
+  w.os = take(P * w.opitch_s);
   w.rows = take(P * 4);
   w.pos = take(P * 4);
   w.tiles = take(w.max_tiles * (int64_t)sizeof(ExpertTile));
   w.n_tiles = take(4);
+  w.chunks = (P + kPlanChunk - 1) / kPlanChunk;
+  w.counts = take(w.chunks > 1 ? w.chunks * kMaxExperts * 4 : 0);
   w.bytes = at;
   return w;
 }

@@ -231,9 +231,9 @@ struct ExpertsArgs {
   void* workspace;
 };
 struct ExpertsWorkspace {  // offsets of its parts
-  int64_t xq, xs, hq, hs, o, rows, pos, tiles, n_tiles, bytes;
-  uint32_t xpitch_q, xpitch_s, hpitch_q, hpitch_s;
-  int64_t max_tiles;
+  int64_t xq, xs, hq, hs, o, os, rows, pos, tiles, n_tiles, counts, bytes;
+  uint32_t xpitch_q, xpitch_s, hpitch_q, hpitch_s, opitch_s;
+  int64_t max_tiles, chunks;
 };
 // The most tiles that T k pairs of E experts can take.
 inline int64_t experts_max_tiles(int64_t T, int64_t k, int64_t E) {
