@@ -23,32 +23,16 @@
 // (a 16-row block of their slab is in lane order), the pairs' rows through LDS.
 // In the up product a wave's 32 rows are 16 of Wg and the 16 of Wu for the same
 // columns of h, so that both factors of an element meet in one lane.
-#include <type_traits>
-
-#include "mx_fp4_device.h"
-#include "mx_internal.h"
+#include "mx_experts_device.h"
 
 namespace mx {
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int NT = 256;
 constexpr int MT = kExpertTile;  // pairs per tile
 constexpr int JB = 4;            // and their fragments of 32
 constexpr int PLAN_THREADS = 1024;
 constexpr int kPlanChunk = 4096;  // pairs
-
-template <int B, int E, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (B < E) {
-    f(std::integral_constant<int, B>{});
-    static_for<B + 1, E>(f);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // (1) Plan and tokens' codes.
@@ -207,29 +191,6 @@ __global__ __launch_bounds__(PLAN_THREADS) void prepare_kernel(PrepareParams p) 
 // ---------------------------------------------------------------------------
 // (2), (3) Products.
 
-struct ProductParams {
-  const uint8_t* x;   // codes of tokens (up) or of h (down)
-  const uint8_t* xs;
-  uint32_t pitch_q, pitch_s;
-  uint32_t x_bytes, xs_bytes;  // up: of the whole operand
-  const uint8_t* wq;
-  const uint8_t* ws;
-  int R;             // padded weight rows
-  int k;
-  int nsteps;
-  int I, H;
-  int tiles_n;
-  const int32_t* rows;
-  const ExpertTile* tiles;
-  const int32_t* n_tiles;
-  uint8_t* hq;  // up: h's codes and scales
-  uint8_t* hs;
-  uint32_t hpitch_q, hpitch_s;
-  uint16_t* o;  // down: f16 [pairs][H]
-  uint8_t* os;  // and the exponents of 32 columns
-  uint32_t opitch_s;
-};
-
 template <bool X8>
 struct Shape {
   static constexpr int D = X8 ? 4 : 8;          // steps in flight
@@ -266,11 +227,6 @@ struct Source {
   uint32_t wo, wso;
   int R, nsteps;
 };
-
-// 16 bytes a lane from `offset` into LDS, lane by lane from `to` on.
-__device__ __forceinline__ void dma(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 16, offset, 0, 0, 0);
-}
 
 // Loads of step j (past the last one zeros from an empty resource, so that every
 // step has the same number of them).
@@ -419,45 +375,12 @@ __device__ __forceinline__ void product(f32x16 (&acc)[JB], const Source<X8>& S, 
     if (j + decltype(V)::value < S.nsteps)
       step<decltype(V)::value>(acc, W, F0, F1, q, S, smem, j + decltype(V)::value, wave, lane);
   });
+  // The last MFMAs' results are read 20 wait states after them at the earliest; the
+  // compiler counts the scheduling directives above among its own.
+  asm volatile("s_nop 15\n\ts_nop 7" : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3]));
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-}
-
-// E4M3 codes of two bf16 pairs under scale code `scode` (as quantize8_bf16).
-__device__ __forceinline__ uint32_t e4m3_encode4_bf16(uint32_t x0, uint32_t x1, uint32_t scode) {
-  const float sv = scale_value(scode);
-  const uint32_t lim = ((scode + 8u) << 7) | 0x60u;  // bf16 bits of 448 * 2^e
-  const u16x2 lim_u = {(unsigned short)(lim | 0x8000u), (unsigned short)(lim | 0x8000u)};
-  const i16x2 lim_i = {(short)lim, (short)lim};
-  const u16x2 a0 = __builtin_elementwise_min(__builtin_bit_cast(u16x2, x0), lim_u);
-  const u16x2 a1 = __builtin_elementwise_min(__builtin_bit_cast(u16x2, x1), lim_u);
-  const i16x2 c0 = __builtin_elementwise_min(__builtin_bit_cast(i16x2, a0), lim_i);
-  const i16x2 c1 = __builtin_elementwise_min(__builtin_bit_cast(i16x2, a1), lim_i);
-  s16x2 r = {0, 0};
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, c0), sv, false);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2, c1), sv, true);
-  return scode == 0xFFu ? 0x7F7F7F7Fu : __builtin_bit_cast(uint32_t, r);
-}
-__device__ __forceinline__ uint32_t e2m1_encode4_bf16(uint32_t x0, uint32_t x1, uint32_t scode) {
-  const float sv = scale_value(scode);
-  uint32_t r = 0;
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x0), sv, 0);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x1), sv, 1);
-  return scode == 0xFFu ? 0x7777u : r;
-}
-
-// act(g) of the gated product: SiLU g / (1 + exp(-g)) on the hardware's exp2 and
-// reciprocal (about 1 ulp each; the product is rounded to bf16 next), or GELU.
-template <int ACT>
-__device__ __forceinline__ float activation(float g) {
-  if constexpr (ACT == 1) return epilogue<1>(g);
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const bf16x2 p = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, p);
 }
 
 // Codes of the tile's 64 columns of h. Lane: pair 32 j + r32; registers 4 q + r
@@ -519,11 +442,7 @@ __device__ __forceinline__ void store_h(const f32x16 (&acc)[JB], const ProductPa
   if (t < count) *(uint16_t*)(p.hs + (int64_t)(m0 + t) * p.hpitch_s + n0 / 32) = *(const uint16_t*)(scales + 2 * t);
 }
 
-// The tile's outputs o as f16 with a power of two for each 32 columns of a row: 2^-12
-// of a value at most is lost (f32 would be 2^-24, and twice the bytes written here
-// and read by the sum; bf16 2^-9, as much as y's own rounding). The largest of the
-// 32 is brought to [2^14, 2^15); values under 2^-28 of it lose bits. A lane holds 16
-// of a group's 32, lane ^ 32 the others.
+// o of the tile's 128 columns.
 __device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductParams& p, uint8_t* smem, int m0, int count,
                                         int n0, int wave, int lane) {
   constexpr int PITCH = 2 * MT + 16;
@@ -531,20 +450,8 @@ __device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductPa
   const int r32 = lane & 31, hi = lane >> 5;
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, __builtin_fabsf(acc[j][i]));
-    const uint32_t b = __float_as_uint(m);
-    const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const uint32_t e = min(max(max((uint32_t)sw[0], (uint32_t)sw[1]) >> 23, 15u), 254u);
-    const float f = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
-    uint8_t* row = smem + (32 * j + r32) * PITCH + 64 * wave + 8 * hi;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f16x2 a = {(_Float16)(acc[j][4 * q] * f), (_Float16)(acc[j][4 * q + 1] * f)};
-      const f16x2 c = {(_Float16)(acc[j][4 * q + 2] * f), (_Float16)(acc[j][4 * q + 3] * f)};
-      *(i32x2*)(row + 16 * q) = i32x2{__builtin_bit_cast(int, a), __builtin_bit_cast(int, c)};
-    }
+    const uint32_t e = o_exponent(acc[j]);
+    store_o16(smem + (32 * j + r32) * PITCH + 64 * wave + 8 * hi, acc[j], e);
     if (hi == 0) scales[(32 * j + r32) * 4 + wave] = (uint8_t)e;
   }
   __syncthreads();
@@ -557,22 +464,13 @@ __device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductPa
   if (t < count) *(uint32_t*)(p.os + (int64_t)(m0 + t) * p.opitch_s + n0 / 32) = *(const uint32_t*)(scales + 4 * t);
 }
 
-// Tiles in groups of 4 along the pairs x all weight tiles, of which each XCD takes
-// a contiguous range, as in mx_fp4_gemm.hip; the number of tiles is known on the
-// device only, and workgroups past it end at once.
 template <bool UP, bool X8, int ACT>
 __global__ __launch_bounds__(NT, 2) void product_kernel(ProductParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using Sh = Shape<X8>;
-  const int tiles_m = *p.n_tiles;
-  const uint32_t total = (uint32_t)tiles_m * (uint32_t)p.tiles_n;
-  if (blockIdx.x >= total) return;
-  constexpr int GM = 4;
-  const int lid = (int)xcd_order(blockIdx.x, total);
-  const int group = lid / (GM * p.tiles_n), gm = min(tiles_m - group * GM, GM);
-  const int in_group = lid - group * GM * p.tiles_n;
-  const ExpertTile tile = p.tiles[group * GM + in_group % gm];
-  const int tn = in_group / gm;
+  ExpertTile tile;
+  int tn;
+  if (!find_tile(p, tile, tn)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, hi = lane >> 5;
@@ -656,6 +554,9 @@ hipError_t launch_product(const ProductParams& p, int64_t max_tiles, hipStream_t
   return hipGetLastError();
 }
 
+// Tiles of 256 weight rows where an expert has many pairs.
+bool large_tiles(const ExpertsArgs& a) { return a.T * a.k >= 64 * a.E; }
+
 template <bool X8>
 hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) {
   uint8_t* base = (uint8_t*)a.workspace;
@@ -712,7 +613,10 @@ hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) 
   p.o = (uint16_t*)(base + w.o);
   p.os = base + w.os;
   p.opitch_s = w.opitch_s;
-  e = a.gate == 1 ? launch_product<true, X8, 1>(p, max_tiles, st) : launch_product<true, X8, 0>(p, max_tiles, st);
+  const bool large = large_tiles(a);
+  e = large         ? launch_experts_tile(p, true, X8, a.gate, max_tiles, st)
+      : a.gate == 1 ? launch_product<true, X8, 1>(p, max_tiles, st)
+                    : launch_product<true, X8, 0>(p, max_tiles, st);
   if (e != hipSuccess) return e;
 
   p.x = p.hq;
@@ -724,7 +628,7 @@ hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) 
   p.R = (int)slab_rows(a.H);
   p.nsteps = (int)fp4_slabs(a.I);
   p.tiles_n = (int)((a.H + MT - 1) / MT);
-  e = launch_product<false, X8, 0>(p, max_tiles, st);
+  e = large ? launch_experts_tile(p, false, X8, 0, max_tiles, st) : launch_product<false, X8, 0>(p, max_tiles, st);
   if (e != hipSuccess) return e;
 
   const int64_t pieces = a.T * (a.H / 8);

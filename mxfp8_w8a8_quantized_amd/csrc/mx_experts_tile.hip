@@ -1,0 +1,425 @@
+// The experts' products on large tiles: 256 weight rows x 128 pairs a workgroup, four
+// waves of 128 x 64 (mx_experts.hip says what the products are, and has the tiles of
+// 128 rows that read few pairs' weights faster).
+//
+// What bounds the 128-row tiles when an expert has many pairs is the path of the loads:
+// about 25 cycles of a CU for each 1 KB that a wave asks for, so 17 KB for the 512
+// cycles of MFMA of a 128 x 128 step. Here a step takes 24 KB (32 with MXFP8 tokens) for
+// twice the MFMAs, both operands through LDS, on the pipeline of mx_fp4_gemm.hip: a
+// ring of four regions, a quarter of a refill issued by each wave, fragments of step j
+// + 1 read between the MFMAs of step j, one barrier a step crossed while MFMAs issued
+// ahead of it run.
+//
+// The pairs' rows are gathered: 64 (MXFP4) or 128 bytes of a row and step, in LDS with
+// 16-byte chunk c of row r at c ^ swizzle(r). Scales come for four steps at a time: the
+// weights' as one slot a step, the rows' 16 bytes a row. In the up product a wave's
+// first 64 weight rows are Wg's and the other 64 Wu's for the same columns of h, so
+// that fragments 0 and 2, 1 and 3 hold both factors of an element, and 32 columns of h
+// lie in one fragment.
+#include "mx_experts_device.h"
+
+namespace mx {
+namespace {
+
+constexpr int NT = 256;
+constexpr int MT = kExpertTile;  // pairs per tile
+constexpr int BN = 256;          // weight rows
+constexpr int IA = 4, JB = 2;    // fragments of 32 x 32 per wave
+constexpr int RING = 4;
+constexpr int SW_SLOT = 4 * BN;  // weight scales of a step
+constexpr int SX_SLOT = 16 * MT; // rows' scales of four steps
+
+template <bool X8>
+struct Shape {
+  static constexpr int ROW = X8 ? 128 : 64;             // bytes of a row's step
+  static constexpr int XB = MT * ROW / 4096;            // row DMAs per wave and step
+  static constexpr int CL = IA + XB;                    // and with the weights'
+  static constexpr int R_X = 64 * BN;                   // rows within a region
+  static constexpr int REGION = R_X + MT * ROW;
+  static constexpr int SW = RING * REGION;              // eight steps of weight scales
+  static constexpr int SX = SW + 8 * SW_SLOT;           // eight steps of the rows'
+  static constexpr int LDS = SX + 2 * SX_SLOT;
+  static constexpr int NM = 2 * IA * JB;                // MFMAs per wave and step
+  static constexpr int NBH = X8 ? 2 * JB : JB;          // 16-byte row reads per MFMA set
+  static constexpr int H = IA + NBH;
+  static constexpr int NC = 2 * H;
+  static constexpr int NR = NC + IA + JB;               // and the scale pairs
+  static constexpr int PRE = X8 ? 3 : 4;                // MFMAs ahead of the barrier
+  static constexpr int SETUP = X8 ? 11 : 6;             // set-up instructions behind each
+  static constexpr int RS = (NM - PRE) * 10 / 13;       // MFMAs after it that carry reads
+  static constexpr int DS = X8 ? (NM - PRE) * 9 / 13 : (NM - PRE) * 18 / 26 + 1;  // and loads
+  __device__ static int swizzle(int r) { return X8 ? (r >> 1) & 7 : (r >> 2) & 3; }
+  static_assert(LDS <= 163840, "LDS");
+};
+
+template <bool X8>
+struct Source {
+  const uint8_t *x, *xs, *w, *ws;
+  uint32_t x_bytes, xs_bytes;
+  uint32_t xo[Shape<X8>::XB], xso, wo[IA], wso;  // the lane's offsets
+  int R, nsteps;
+};
+
+// Loads of a step: past the last one from empty resources, so that every step has the
+// same number of them.
+template <class Sh>
+struct LoadRes {
+  __amdgpu_buffer_rsrc_t w, x;
+  uint8_t* reg;
+};
+template <bool X8>
+__device__ __forceinline__ LoadRes<Shape<X8>> load_res(const Source<X8>& S, uint8_t* smem, int j, int rg) {
+  using Sh = Shape<X8>;
+  const bool on = j < S.nsteps;
+  return {make_rsrc(S.w + (int64_t)j * S.R * 64, on ? (uint32_t)S.R * 64u : 0u),
+          make_rsrc(S.x + (int64_t)j * Sh::ROW, on ? S.x_bytes - (uint32_t)(j * Sh::ROW) : 0u), smem + rg * Sh::REGION};
+}
+// Code piece D of a step: one KB, weights and rows in turn while there are both.
+template <int D, bool X8>
+__device__ __forceinline__ void load_piece(const LoadRes<Shape<X8>>& L, const Source<X8>& S, int wave) {
+  using Sh = Shape<X8>;
+  constexpr int XB = Sh::XB, both = IA < XB ? IA : XB;
+  constexpr bool W = D < 2 * both ? D % 2 == 0 : IA > XB;
+  constexpr int u = D < 2 * both ? D / 2 : D - both;
+  if constexpr (W)
+    dma(L.w, L.reg + (wave * IA + u) * 1024, S.wo[u]);
+  else
+    dma(L.x, L.reg + Sh::R_X + (wave * XB + u) * 1024, S.xo[u]);
+}
+// Scales of steps s .. s + 3 (s a multiple of 4): a wave takes the weights' of one step
+// and half of the rows (waves 2 and 3 the same halves as 0 and 1).
+struct ScaleRes {
+  __amdgpu_buffer_rsrc_t w, x;
+  uint8_t *wto, *xto;
+};
+template <bool X8>
+__device__ __forceinline__ ScaleRes scale_res(const Source<X8>& S, uint8_t* smem, int s, int wave) {
+  using Sh = Shape<X8>;
+  const int st = s + wave;
+  return {make_rsrc(S.ws + (int64_t)st * S.R * 4, st < S.nsteps ? (uint32_t)S.R * 4u : 0u),
+          make_rsrc(S.xs + (int64_t)s * 4, s < S.nsteps ? S.xs_bytes - (uint32_t)s * 4u : 0u),
+          smem + Sh::SW + (st & 7) * SW_SLOT, smem + Sh::SX + ((s >> 2) & 1) * SX_SLOT + (wave & 1) * 1024};
+}
+
+template <bool X8>
+struct Frags {
+  i32x4 a[IA][2];              // [fragment][MFMA of the step]
+  i32x4 b[JB][2][X8 ? 2 : 1];  // and, of an E4M3 operand, its two halves
+  int sa[IA], sb[JB];          // byte s: the scale for MFMA s
+};
+struct FragAddr {
+  const uint8_t *a, *sa, *sb;
+  const uint8_t *b[2][2];  // [MFMA of the step][half]
+};
+template <bool X8>
+__device__ __forceinline__ FragAddr frag_addr(const uint8_t* smem, int j, int rg, int wn, int wm, int lane) {
+  using Sh = Shape<X8>;
+  const int r32 = lane & 31, hi = lane >> 5, sw = Sh::swizzle(r32);
+  const uint8_t* reg = smem + rg * Sh::REGION;
+  const uint8_t* row = reg + Sh::R_X + (wm * 32 * JB + r32) * Sh::ROW;
+  FragAddr A;
+  A.a = reg + wn * (2048 * IA) + (r32 >> 4) * 1024 + (r32 & 15) * 16 + 512 * hi;
+  A.sa = smem + Sh::SW + (j & 7) * SW_SLOT + (wn * 32 * IA + r32) * 4 + 2 * hi;
+  A.sb = smem + Sh::SX + ((j >> 2) & 1) * SX_SLOT + (wm * 32 * JB + r32) * 16 + (j & 3) * 4 + 2 * hi;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    A.b[s][0] = row + (((X8 ? 2 * s + hi : 2 * hi + s) ^ sw) << 4);
+    A.b[s][1] = X8 ? row + (((4 + 2 * s + hi) ^ sw) << 4) : A.b[s][0];
+  }
+  return A;
+}
+// Read piece r: the fragments' 16-byte parts in the order the MFMAs take them, then
+// the scales.
+template <int R, bool X8>
+__device__ __forceinline__ void read_piece(Frags<X8>& F, const FragAddr& A) {
+  using Sh = Shape<X8>;
+  if constexpr (R < Sh::NC) {
+    constexpr int s = R / Sh::H, r = R % Sh::H;
+    constexpr int both = Sh::NBH < IA ? Sh::NBH : IA;
+    constexpr bool isA = r < 2 * both ? r % 2 == 0 : IA > Sh::NBH;
+    constexpr int f = r < 2 * both ? r / 2 : r - both;
+    if constexpr (isA)
+      F.a[f][s] = *(const i32x4*)(A.a + f * 2048 + s * 256);
+    else if constexpr (X8)
+      F.b[f / 2][s][f % 2] = *(const i32x4*)(A.b[s][f % 2] + (f / 2) * 32 * Sh::ROW);
+    else
+      F.b[f][s][0] = *(const i32x4*)(A.b[s][0] + f * 32 * Sh::ROW);
+  } else if constexpr (R < Sh::NC + IA) {
+    F.sa[R - Sh::NC] = *(const uint16_t*)(A.sa + 32 * 4 * (R - Sh::NC));
+  } else {
+    F.sb[R - Sh::NC - IA] = *(const uint16_t*)(A.sb + 32 * 16 * (R - Sh::NC - IA));
+  }
+}
+
+template <int B, int E, bool X8>
+__device__ __forceinline__ void mma(f32x16 (&acc)[IA][JB], const Frags<X8>& F) {
+  static_for<B, E>([&](auto T) {
+    constexpr int s = decltype(T)::value / (IA * JB), u = decltype(T)::value % (IA * JB), i = u / JB, j = u % JB;
+    const i32x8 a = {F.a[i][s][0], F.a[i][s][1], F.a[i][s][2], F.a[i][s][3], 0, 0, 0, 0};
+    const i32x4& b0 = F.b[j][s][0];
+    if constexpr (X8) {
+      const i32x4& b1 = F.b[j][s][1];
+      const i32x8 b = {b0[0], b0[1], b0[2], b0[3], b1[0], b1[1], b1[2], b1[3]};
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 0, s, F.sa[i], s, F.sb[j]);
+    } else {
+      const i32x8 b = {b0[0], b0[1], b0[2], b0[3], 0, 0, 0, 0};
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 4, 4, s, F.sa[i], s, F.sb[j]);
+    }
+  });
+}
+
+// Reads [r0, r1) and loads [d0, d1) issued with the I-th MFMA after the barrier; SC:
+// two of scales first.
+template <class Sh, bool SC, int I>
+struct Slot {
+  static constexpr int N = Sh::CL + (SC ? 2 : 0);
+  static constexpr int r0 = I < Sh::RS ? Sh::NR * I / Sh::RS : Sh::NR, r1 = I < Sh::RS ? Sh::NR * (I + 1) / Sh::RS : Sh::NR;
+  static constexpr int d0 = I < Sh::DS ? N * I / Sh::DS : N, d1 = I < Sh::DS ? N * (I + 1) / Sh::DS : N;
+};
+
+// Step j, V = j % 4 (and its ring region).
+template <int V, bool X8>
+__device__ __forceinline__ void step(f32x16 (&acc)[IA][JB], Frags<X8>& cur, Frags<X8>& nxt, const Source<X8>& S,
+                                     uint8_t* smem, int j, int wave, int wn, int wm, int lane) {
+  using Sh = Shape<X8>;
+  constexpr int NM = Sh::NM, PRE = Sh::PRE;
+  constexpr bool SC = V == 0;
+  __builtin_amdgcn_sched_barrier(0);
+  const FragAddr A = frag_addr<X8>(smem, j + 1, (V + 1) % RING, wn, wm, lane);
+  const LoadRes<Sh> L = load_res<X8>(S, smem, j + RING, V);
+  ScaleRes C;
+  if constexpr (SC) C = scale_res<X8>(S, smem, j + RING, wave);
+  mma<0, PRE>(acc, cur);
+  static_for<0, PRE>([&](auto) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
+    __builtin_amdgcn_sched_group_barrier(0x006, Sh::SETUP, 0);  // set-up VALU / SALU
+  });
+  __builtin_amdgcn_sched_barrier(0);
+  // Younger loads than step j + 1's: the codes of RING - 2 steps (those of scales, left
+  // out, only make the wait stricter). The lgkmcnt(0) keeps a wave's refill from
+  // overtaking another wave's last reads of the region.
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((RING - 2) * Sh::CL) : "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  static_for<0, NM - PRE>([&](auto I) {
+    using SL = Slot<Sh, SC, decltype(I)::value>;
+    static_for<SL::r0, SL::r1>([&](auto R) { read_piece<decltype(R)::value>(nxt, A); });
+    static_for<SL::d0, SL::d1>([&](auto D) {
+      constexpr int d = decltype(D)::value - (SC ? 2 : 0);
+      if constexpr (d == -2)
+        dma(C.w, C.wto, S.wso);
+      else if constexpr (d == -1)
+        dma(C.x, C.xto, S.xso);
+      else
+        load_piece<d, X8>(L, S, wave);
+    });
+  });
+  mma<PRE, NM>(acc, cur);
+  static_for<0, NM - PRE>([&](auto I) {
+    using SL = Slot<Sh, SC, decltype(I)::value>;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (SL::r1 > SL::r0) __builtin_amdgcn_sched_group_barrier(0x100, SL::r1 - SL::r0, 0);
+    if constexpr (SL::d1 > SL::d0) __builtin_amdgcn_sched_group_barrier(0x020, SL::d1 - SL::d0, 0);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Codes of the tile's 128 columns of h: the wave's 64 columns x 64 pairs.
+template <bool X8, int ACT>
+__device__ __forceinline__ void store_h(const f32x16 (&acc)[IA][JB], const ProductParams& p, uint8_t* smem,
+                                        const ExpertTile& tile, int n0, int wn, int wm, int lane) {
+  constexpr int W = X8 ? 128 : 64;  // bytes of a row's codes
+  constexpr int PITCH = W + 16;     // in LDS
+  uint8_t* scales = smem + MT * PITCH;  // [row][4]
+  const int r32 = lane & 31, hi = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int m = wm * 32 * JB + 32 * j + r32;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t v[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float h[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = activation<ACT>(acc[i][j][4 * q + r]) * acc[i + 2][j][4 * q + r];
+        v[2 * q] = pack_bf16(h[0], h[1]);
+        v[2 * q + 1] = pack_bf16(h[2], h[3]);
+      }
+      const uint32_t b = bf16_amax_bits(v);
+      const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+      const uint32_t E = max((uint32_t)sw[0], (uint32_t)sw[1]) >> 7;
+      const bool real = n0 + 64 * wn + 32 * i < p.I;  // columns past I: zero codes and scales
+      const uint32_t sc = X8 ? scale_code_from_exponent(E) : fp4_scale_code(E);
+      uint8_t* row = smem + m * PITCH;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 64 * wn + 32 * i + 8 * q + 4 * hi;
+        if constexpr (X8)
+          *(uint32_t*)(row + col) = real ? e4m3_encode4_bf16(v[2 * q], v[2 * q + 1], sc) : 0u;
+        else
+          *(uint16_t*)(row + col / 2) = (uint16_t)(real ? e2m1_encode4_bf16(v[2 * q], v[2 * q + 1], sc) : 0u);
+      }
+      if (hi == 0) scales[m * 4 + 2 * wn + i] = (uint8_t)(real ? sc : 0u);
+    }
+  }
+  __syncthreads();
+  constexpr int PIECES = W / 16;
+  const int t = threadIdx.x;
+  for (int u = t; u < tile.count * PIECES; u += NT) {
+    const int r = u / PIECES, c = u % PIECES;
+    *(i32x4*)(p.hq + (int64_t)(tile.first + r) * p.hpitch_q + n0 * W / 128 + 16 * c) =
+        *(const i32x4*)(smem + r * PITCH + 16 * c);
+  }
+  if (t < tile.count)
+    *(uint32_t*)(p.hs + (int64_t)(tile.first + t) * p.hpitch_s + n0 / 32) = *(const uint32_t*)(scales + 4 * t);
+}
+
+// o of the tile's 256 columns (mx_experts.hip has its form): the wave's 128 x 64 pairs.
+__device__ __forceinline__ void store_o(const f32x16 (&acc)[IA][JB], const ProductParams& p, uint8_t* smem,
+                                        const ExpertTile& tile, int n0, int wn, int wm, int lane) {
+  constexpr int PITCH = 2 * BN + 16;
+  uint8_t* scales = smem + MT * PITCH;  // [row][8]
+  const int r32 = lane & 31, hi = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < JB; ++j) {
+    const int m = wm * 32 * JB + 32 * j + r32;
+#pragma unroll
+    for (int i = 0; i < IA; ++i) {
+      const uint32_t e = o_exponent(acc[i][j]);
+      store_o16(smem + m * PITCH + 2 * (wn * 32 * IA + 32 * i) + 8 * hi, acc[i][j], e);
+      if (hi == 0) scales[m * 8 + wn * IA + i] = (uint8_t)e;
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  for (int u = t; u < tile.count * 32; u += NT) {
+    const int r = u >> 5, c = u & 31;
+    if (n0 + 8 * c < p.H)
+      *(i32x4*)(p.o + (int64_t)(tile.first + r) * p.H + n0 + 8 * c) = *(const i32x4*)(smem + r * PITCH + 16 * c);
+  }
+  // (Rows of exponents are whole multiples of 4; the second four may be past them.)
+  for (int u = t; u < tile.count * 2; u += NT)
+    if ((uint32_t)(n0 / 32 + (u & 1) * 4) < p.opitch_s)
+      *(uint32_t*)(p.os + (int64_t)(tile.first + (u >> 1)) * p.opitch_s + n0 / 32 + (u & 1) * 4) =
+          *(const uint32_t*)(scales + 4 * u);
+}
+
+template <bool UP, bool X8, int ACT>
+__global__ __launch_bounds__(NT, 1) void tile_kernel(ProductParams p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  using Sh = Shape<X8>;
+  ExpertTile tile;
+  int tn;
+  if (!find_tile(p, tile, tn)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave & 1, wm = wave >> 1;
+
+  Source<X8> S;
+  S.nsteps = p.nsteps;
+  S.R = p.R;
+  S.w = p.wq + (int64_t)tile.expert * p.nsteps * p.R * 64;
+  S.ws = p.ws + (int64_t)tile.expert * p.nsteps * p.R * 4;
+  const int n0 = tn * (UP ? BN / 2 : BN);
+  // Weight row of the tile's row r (rows past the slab's read zeros).
+  auto weight_row = [&](int r) {
+    return UP ? n0 + (r >> 7) * 64 + (r & 63) + ((r >> 6) & 1) * p.I : n0 + r;
+  };
+#pragma unroll
+  for (int u = 0; u < IA; ++u) S.wo[u] = (uint32_t)(weight_row((wave * IA + u) * 16) / 16 * 1024 + lane * 16);
+  S.wso = (uint32_t)weight_row(4 * lane) * 4u;
+  // The pairs' rows: rows past the tile's count repeat its last one.
+  if constexpr (UP) {
+    S.x = p.x;
+    S.xs = p.xs;
+    S.x_bytes = p.x_bytes;
+    S.xs_bytes = p.xs_bytes;
+  } else {
+    S.x = p.x + (int64_t)tile.first * p.pitch_q;
+    S.xs = p.xs + (int64_t)tile.first * p.pitch_s;
+    S.x_bytes = (uint32_t)tile.count * p.pitch_q;
+    S.xs_bytes = (uint32_t)tile.count * p.pitch_s;
+  }
+  auto source_row = [&](int r) -> uint32_t {
+    const int c = min(r, tile.count - 1);
+    return UP ? (uint32_t)p.rows[tile.first + c] / (uint32_t)p.k : (uint32_t)c;
+  };
+  constexpr int LPR = Sh::ROW / 16;  // lanes per row
+#pragma unroll
+  for (int i = 0; i < Sh::XB; ++i) {
+    const int r = (wave * Sh::XB + i) * (64 / LPR) + lane / LPR;
+    S.xo[i] = source_row(r) * p.pitch_q + (uint32_t)(((lane % LPR) ^ Sh::swizzle(r)) * 16);
+  }
+  S.xso = source_row(64 * (wave & 1) + lane) * p.pitch_s;
+
+  // The ring's first loads in the order the loop would have issued them.
+  {
+    const ScaleRes C = scale_res<X8>(S, smem, 0, wave);
+    dma(C.w, C.wto, S.wso);
+    dma(C.x, C.xto, S.xso);
+  }
+  static_for<0, RING>([&](auto J) {
+    constexpr int j = decltype(J)::value;
+    const LoadRes<Sh> L = load_res<X8>(S, smem, j, j);
+    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, X8>(L, S, wave); });
+  });
+  f32x16 acc[IA][JB];
+#pragma unroll
+  for (int i = 0; i < IA; ++i)
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+      asm volatile("" : "+a"(acc[i][j]));  // written here, inside the first loads' latency
+    }
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((RING - 1) * Sh::CL) : "memory");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  Frags<X8> F[2];
+  const FragAddr A0 = frag_addr<X8>(smem, 0, 0, wn, wm, lane);
+  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value>(F[0], A0); });
+  int j = 0;
+  for (; j + RING <= S.nsteps; j += RING)
+    static_for<0, RING>([&](auto V) {
+      constexpr int v = decltype(V)::value;
+      step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
+    });
+  static_for<0, RING - 1>([&](auto V) {
+    constexpr int v = decltype(V)::value;
+    if (j + v < S.nsteps) step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
+  });
+  __builtin_amdgcn_sched_barrier(0);
+  // The last MFMAs' results are read 20 wait states after them at the earliest; the
+  // compiler counts the scheduling directives above among its own.
+#pragma unroll
+  for (int i = 0; i < IA; ++i) asm volatile("s_nop 15\n\ts_nop 7" : "+a"(acc[i][0]), "+a"(acc[i][1]));
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  if constexpr (UP)
+    store_h<X8, ACT>(acc, p, smem, tile, n0, wn, wm, lane);
+  else
+    store_o(acc, p, smem, tile, n0, wn, wm, lane);
+}
+
+template <bool UP, bool X8, int ACT>
+hipError_t launch(ProductParams p, int64_t max_tiles, hipStream_t st) {
+  static std::atomic<uint64_t> configured{0};  // per instantiation
+  auto kern = tile_kernel<UP, X8, ACT>;
+  const hipError_t e = allow_dynamic_lds((const void*)kern, Shape<X8>::LDS, configured);
+  if (e != hipSuccess) return e;
+  p.tiles_n = UP ? (p.I + 127) / 128 : (p.H + BN - 1) / BN;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(max_tiles * p.tiles_n)), dim3(NT), Shape<X8>::LDS, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_experts_tile(const ProductParams& p, bool up, bool fp8, int gate, int64_t max_tiles, hipStream_t stream) {
+  if (!up) return fp8 ? launch<false, true, 0>(p, max_tiles, stream) : launch<false, false, 0>(p, max_tiles, stream);
+  if (fp8) return gate == 1 ? launch<true, true, 1>(p, max_tiles, stream) : launch<true, true, 0>(p, max_tiles, stream);
+  return gate == 1 ? launch<true, false, 1>(p, max_tiles, stream) : launch<true, false, 0>(p, max_tiles, stream);
+}
+
+}  // namespace mx
