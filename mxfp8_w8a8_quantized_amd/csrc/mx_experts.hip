@@ -451,7 +451,11 @@ __device__ __forceinline__ void store_o(const f32x16 (&acc)[JB], const ProductPa
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
     const uint32_t e = o_exponent(acc[j]);
-    store_o16(smem + (32 * j + r32) * PITCH + 64 * wave + 8 * hi, acc[j], e);
+    uint32_t c[8];
+    o_pack(acc[j], e, c);
+    uint8_t* row = smem + (32 * j + r32) * PITCH + 64 * wave + 8 * hi;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *(i32x2*)(row + 16 * q) = i32x2{(int)c[2 * q], (int)c[2 * q + 1]};
     if (hi == 0) scales[(32 * j + r32) * 4 + wave] = (uint8_t)e;
   }
   __syncthreads();

@@ -104,13 +104,13 @@ __device__ __forceinline__ uint32_t o_exponent(const f32x16& a) {
   const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
   return min(max(max((uint32_t)sw[0], (uint32_t)sw[1]) >> 23, 15u), 254u);
 }
-__device__ __forceinline__ void store_o16(uint8_t* to, const f32x16& a, uint32_t e) {
+// The lane's 16 columns 8 q + 4 hi .. + 3 (q = 0 .. 3), two dwords for each q.
+__device__ __forceinline__ void o_pack(const f32x16& a, uint32_t e, uint32_t (&c)[8]) {
   const float f = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const f16x2 x = {(_Float16)(a[4 * q] * f), (_Float16)(a[4 * q + 1] * f)};
-    const f16x2 y = {(_Float16)(a[4 * q + 2] * f), (_Float16)(a[4 * q + 3] * f)};
-    *(i32x2*)(to + 16 * q) = i32x2{__builtin_bit_cast(int, x), __builtin_bit_cast(int, y)};
+  for (int q = 0; q < 8; ++q) {
+    const f16x2 x = {(_Float16)(a[2 * q] * f), (_Float16)(a[2 * q + 1] * f)};
+    c[q] = __builtin_bit_cast(uint32_t, x);
   }
 }
 

@@ -26,6 +26,7 @@ constexpr int MT = kExpertTile;  // pairs per tile
 constexpr int BN = 256;          // weight rows
 constexpr int IA = 4, JB = 2;    // fragments of 32 x 32 per wave
 constexpr int RING = 4;
+constexpr int64_t kWorkgroups = 256;  // a multiple of the 8 XCDs
 constexpr int SW_SLOT = 4 * BN;  // weight scales of a step
 constexpr int SX_SLOT = 16 * MT; // rows' scales of four steps
 
@@ -224,17 +225,40 @@ __device__ __forceinline__ void step(f32x16 (&acc)[IA][JB], Frags<X8>& cur, Frag
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Codes of the tile's 128 columns of h: the wave's 64 columns x 64 pairs.
+// A workgroup's tile: its pairs, and its first column of h (up) or of o.
+struct Where {
+  ExpertTile pairs;
+  int n0;
+  bool any;
+};
+
+// Buffer stores past a resource's end are dropped: rows past the tile's count are past
+// it, columns past the operand's are sent there.
+constexpr uint32_t kDrop = 0x80000000u;
+
+// The upper 32 lanes of a change places with the lower 32 of b.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = s[0];
+  b = s[1];
+}
+
+// Codes of the tile's 128 columns of h, straight from the registers: lane r32 + 32 hi
+// of a fragment holds columns 8 q + 4 hi .. + 3 (q = 0 .. 3) of row r32; two swaps leave
+// it columns 16 hi .. + 15.
 template <bool X8, int ACT>
-__device__ __forceinline__ void store_h(const f32x16 (&acc)[IA][JB], const ProductParams& p, uint8_t* smem,
-                                        const ExpertTile& tile, int n0, int wn, int wm, int lane) {
-  constexpr int W = X8 ? 128 : 64;  // bytes of a row's codes
-  constexpr int PITCH = W + 16;     // in LDS
-  uint8_t* scales = smem + MT * PITCH;  // [row][4]
+__device__ __forceinline__ void store_h(const f32x16 (&acc)[IA][JB], const ProductParams& p, const Where& t, int wn, int wm,
+                                        int lane) {
   const int r32 = lane & 31, hi = lane >> 5;
+  const __amdgpu_buffer_rsrc_t rq =
+      make_rsrc(p.hq + (int64_t)t.pairs.first * p.hpitch_q, (uint32_t)t.pairs.count * p.hpitch_q);
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc(p.hs + (int64_t)t.pairs.first * p.hpitch_s, (uint32_t)t.pairs.count * p.hpitch_s);
+  const int n = t.n0 + 64 * wn;
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
-    const int m = wm * 32 * JB + 32 * j + r32;
+    const uint32_t m = (uint32_t)(wm * 32 * JB + 32 * j + r32);
+    uint32_t scales = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t v[8];
@@ -246,161 +270,204 @@ __device__ __forceinline__ void store_h(const f32x16 (&acc)[IA][JB], const Produ
         v[2 * q] = pack_bf16(h[0], h[1]);
         v[2 * q + 1] = pack_bf16(h[2], h[3]);
       }
-      const uint32_t b = bf16_amax_bits(v);
-      const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-      const uint32_t E = max((uint32_t)sw[0], (uint32_t)sw[1]) >> 7;
-      const bool real = n0 + 64 * wn + 32 * i < p.I;  // columns past I: zero codes and scales
+      uint32_t b = bf16_amax_bits(v), b2 = b;
+      swap32(b, b2);
+      const uint32_t E = max(b, b2) >> 7;
+      const bool real = n + 32 * i < p.I;  // columns past I: zero codes and scales
       const uint32_t sc = X8 ? scale_code_from_exponent(E) : fp4_scale_code(E);
-      uint8_t* row = smem + m * PITCH;
+      scales |= (real ? sc : 0u) << (8 * i);
+      uint32_t c[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int col = 64 * wn + 32 * i + 8 * q + 4 * hi;
-        if constexpr (X8)
-          *(uint32_t*)(row + col) = real ? e4m3_encode4_bf16(v[2 * q], v[2 * q + 1], sc) : 0u;
-        else
-          *(uint16_t*)(row + col / 2) = (uint16_t)(real ? e2m1_encode4_bf16(v[2 * q], v[2 * q + 1], sc) : 0u);
+        c[q] = X8 ? e4m3_encode4_bf16(v[2 * q], v[2 * q + 1], sc) : e2m1_encode4_bf16(v[2 * q], v[2 * q + 1], sc);
+        c[q] = real ? c[q] : 0u;
       }
-      if (hi == 0) scales[m * 4 + 2 * wn + i] = (uint8_t)(real ? sc : 0u);
+      swap32(c[0], c[2]);
+      swap32(c[1], c[3]);
+      const uint32_t col = (uint32_t)(n + 32 * i + 16 * hi);
+      if constexpr (X8)
+        __builtin_amdgcn_raw_buffer_store_b128(i32x4{(int)c[0], (int)c[2], (int)c[1], (int)c[3]}, rq, m * p.hpitch_q + col, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b64(i32x2{(int)(c[0] | (c[2] << 16)), (int)(c[1] | (c[3] << 16))}, rq,
+                                              m * p.hpitch_q + col / 2, 0, 0);
     }
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)scales, rs, hi == 0 ? m * p.hpitch_s + (uint32_t)n / 32 : kDrop, 0, 0);
   }
-  __syncthreads();
-  constexpr int PIECES = W / 16;
-  const int t = threadIdx.x;
-  for (int u = t; u < tile.count * PIECES; u += NT) {
-    const int r = u / PIECES, c = u % PIECES;
-    *(i32x4*)(p.hq + (int64_t)(tile.first + r) * p.hpitch_q + n0 * W / 128 + 16 * c) =
-        *(const i32x4*)(smem + r * PITCH + 16 * c);
-  }
-  if (t < tile.count)
-    *(uint32_t*)(p.hs + (int64_t)(tile.first + t) * p.hpitch_s + n0 / 32) = *(const uint32_t*)(scales + 4 * t);
 }
 
-// o of the tile's 256 columns (mx_experts.hip has its form): the wave's 128 x 64 pairs.
-__device__ __forceinline__ void store_o(const f32x16 (&acc)[IA][JB], const ProductParams& p, uint8_t* smem,
-                                        const ExpertTile& tile, int n0, int wn, int wm, int lane) {
-  constexpr int PITCH = 2 * BN + 16;
-  uint8_t* scales = smem + MT * PITCH;  // [row][8]
+// o of the tile's 256 columns (mx_experts_device.h has its form), likewise: a lane's
+// columns 8 q + 4 hi .. + 3 become 8 hi .. + 7 and 16 + 8 hi .. + 7.
+__device__ __forceinline__ void store_o(const f32x16 (&acc)[IA][JB], const ProductParams& p, const Where& t, int wn, int wm,
+                                        int lane) {
   const int r32 = lane & 31, hi = lane >> 5;
+  const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.o + (int64_t)t.pairs.first * p.H, (uint32_t)(t.pairs.count * p.H * 2));
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc(p.os + (int64_t)t.pairs.first * p.opitch_s, (uint32_t)t.pairs.count * p.opitch_s);
+  const int n = t.n0 + 32 * IA * wn;
 #pragma unroll
   for (int j = 0; j < JB; ++j) {
-    const int m = wm * 32 * JB + 32 * j + r32;
+    const uint32_t m = (uint32_t)(wm * 32 * JB + 32 * j + r32);
+    uint32_t exponents = 0;
 #pragma unroll
     for (int i = 0; i < IA; ++i) {
       const uint32_t e = o_exponent(acc[i][j]);
-      store_o16(smem + m * PITCH + 2 * (wn * 32 * IA + 32 * i) + 8 * hi, acc[i][j], e);
-      if (hi == 0) scales[m * 8 + wn * IA + i] = (uint8_t)e;
+      exponents |= e << (8 * i);
+      uint32_t c[8];
+      o_pack(acc[i][j], e, c);
+      const uint32_t at = n + 32 * i < p.H ? (m * (uint32_t)p.H + (uint32_t)(n + 32 * i + 8 * hi)) * 2 : kDrop;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        swap32(c[4 * u], c[4 * u + 2]);
+        swap32(c[4 * u + 1], c[4 * u + 3]);
+        __builtin_amdgcn_raw_buffer_store_b128(
+            i32x4{(int)c[4 * u], (int)c[4 * u + 1], (int)c[4 * u + 2], (int)c[4 * u + 3]}, ro, at + 32 * u, 0, 0);
+      }
     }
+    const uint32_t g = (uint32_t)n / 32;
+    __builtin_amdgcn_raw_buffer_store_b32(exponents, rs, hi == 0 && g < p.opitch_s ? m * p.opitch_s + g : kDrop, 0, 0);
   }
-  __syncthreads();
-  const int t = threadIdx.x;
-  for (int u = t; u < tile.count * 32; u += NT) {
-    const int r = u >> 5, c = u & 31;
-    if (n0 + 8 * c < p.H)
-      *(i32x4*)(p.o + (int64_t)(tile.first + r) * p.H + n0 + 8 * c) = *(const i32x4*)(smem + r * PITCH + 16 * c);
-  }
-  // (Rows of exponents are whole multiples of 4; the second four may be past them.)
-  for (int u = t; u < tile.count * 2; u += NT)
-    if ((uint32_t)(n0 / 32 + (u & 1) * 4) < p.opitch_s)
-      *(uint32_t*)(p.os + (int64_t)(tile.first + (u >> 1)) * p.opitch_s + n0 / 32 + (u & 1) * 4) =
-          *(const uint32_t*)(scales + 4 * u);
 }
 
+// Workgroups stay for several tiles (256 of them, a CU each), so that a tile's first
+// loads are on their way while the output of the one before is written: RESULT
 template <bool UP, bool X8, int ACT>
 __global__ __launch_bounds__(NT, 1) void tile_kernel(ProductParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using Sh = Shape<X8>;
-  ExpertTile tile;
-  int tn;
-  if (!find_tile(p, tile, tn)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave & 1, wm = wave >> 1;
 
+  // Tiles in groups of 4 along the pairs x all weight tiles; each XCD has a contiguous
+  // range of them, its workgroups take them in turn. Their number is known on the
+  // device only.
+  const int tiles_m = *p.n_tiles;
+  const uint32_t total = (uint32_t)tiles_m * (uint32_t)p.tiles_n, xcd = blockIdx.x & 7;
+  const uint32_t first = xcd * (total >> 3) + min(xcd, total & 7), end = first + (total >> 3) + (xcd < (total & 7) ? 1 : 0);
+  uint32_t lid = first + (blockIdx.x >> 3);
+  auto next_tile = [&]() -> Where {
+    if (lid >= end) return {{0, 0, 0, 0}, 0, false};
+    constexpr int GM = 4;
+    const int group = (int)lid / (GM * p.tiles_n), gm = min(tiles_m - group * GM, GM);
+    const int in_group = (int)lid - group * GM * p.tiles_n;
+    lid += gridDim.x >> 3;
+    return {p.tiles[group * GM + in_group % gm], in_group / gm * (UP ? BN / 2 : BN), true};
+  };
+  // Rows of the operand that the lane's DMAs take (rows past the tile's count repeat
+  // its last one), and the scales'.
+  constexpr int LPR = Sh::ROW / 16;  // lanes per row
+  struct Rows {
+    uint32_t x[Sh::XB], s;
+  };
+  auto rows_of = [&](const Where& t) -> Rows {
+    auto source = [&](int r) -> uint32_t {
+      const int c = min(r, t.pairs.count - 1);
+      return UP ? (uint32_t)p.rows[t.pairs.first + c] : (uint32_t)c;
+    };
+    Rows R;
+#pragma unroll
+    for (int i = 0; i < Sh::XB; ++i) R.x[i] = source((wave * Sh::XB + i) * (64 / LPR) + lane / LPR);
+    R.s = source(64 * (wave & 1) + lane);
+    return R;
+  };
   Source<X8> S;
   S.nsteps = p.nsteps;
   S.R = p.R;
-  S.w = p.wq + (int64_t)tile.expert * p.nsteps * p.R * 64;
-  S.ws = p.ws + (int64_t)tile.expert * p.nsteps * p.R * 4;
-  const int n0 = tn * (UP ? BN / 2 : BN);
-  // Weight row of the tile's row r (rows past the slab's read zeros).
-  auto weight_row = [&](int r) {
-    return UP ? n0 + (r >> 7) * 64 + (r & 63) + ((r >> 6) & 1) * p.I : n0 + r;
-  };
+  auto start = [&](const Where& t, const Rows& R) {  // the ring's first loads, as the loop would have issued them
+    S.w = p.wq + (int64_t)t.pairs.expert * p.nsteps * p.R * 64;
+    S.ws = p.ws + (int64_t)t.pairs.expert * p.nsteps * p.R * 4;
+    // Weight row of the tile's row r (rows past the slab's read zeros).
+    auto weight_row = [&](int r) {
+      return UP ? t.n0 + (r >> 7) * 64 + (r & 63) + ((r >> 6) & 1) * p.I : t.n0 + r;
+    };
 #pragma unroll
-  for (int u = 0; u < IA; ++u) S.wo[u] = (uint32_t)(weight_row((wave * IA + u) * 16) / 16 * 1024 + lane * 16);
-  S.wso = (uint32_t)weight_row(4 * lane) * 4u;
-  // The pairs' rows: rows past the tile's count repeat its last one.
-  if constexpr (UP) {
-    S.x = p.x;
-    S.xs = p.xs;
-    S.x_bytes = p.x_bytes;
-    S.xs_bytes = p.xs_bytes;
-  } else {
-    S.x = p.x + (int64_t)tile.first * p.pitch_q;
-    S.xs = p.xs + (int64_t)tile.first * p.pitch_s;
-    S.x_bytes = (uint32_t)tile.count * p.pitch_q;
-    S.xs_bytes = (uint32_t)tile.count * p.pitch_s;
-  }
-  auto source_row = [&](int r) -> uint32_t {
-    const int c = min(r, tile.count - 1);
-    return UP ? (uint32_t)p.rows[tile.first + c] / (uint32_t)p.k : (uint32_t)c;
-  };
-  constexpr int LPR = Sh::ROW / 16;  // lanes per row
+    for (int u = 0; u < IA; ++u) S.wo[u] = (uint32_t)(weight_row((wave * IA + u) * 16) / 16 * 1024 + lane * 16);
+    S.wso = (uint32_t)weight_row(4 * lane) * 4u;
+    if constexpr (UP) {
+      S.x = p.x;
+      S.xs = p.xs;
+      S.x_bytes = p.x_bytes;
+      S.xs_bytes = p.xs_bytes;
+    } else {
+      S.x = p.x + (int64_t)t.pairs.first * p.pitch_q;
+      S.xs = p.xs + (int64_t)t.pairs.first * p.pitch_s;
+      S.x_bytes = (uint32_t)t.pairs.count * p.pitch_q;
+      S.xs_bytes = (uint32_t)t.pairs.count * p.pitch_s;
+    }
 #pragma unroll
-  for (int i = 0; i < Sh::XB; ++i) {
-    const int r = (wave * Sh::XB + i) * (64 / LPR) + lane / LPR;
-    S.xo[i] = source_row(r) * p.pitch_q + (uint32_t)(((lane % LPR) ^ Sh::swizzle(r)) * 16);
-  }
-  S.xso = source_row(64 * (wave & 1) + lane) * p.pitch_s;
-
-  // The ring's first loads in the order the loop would have issued them.
-  {
+    for (int i = 0; i < Sh::XB; ++i) {
+      const int r = (wave * Sh::XB + i) * (64 / LPR) + lane / LPR;
+      S.xo[i] = (UP ? R.x[i] / (uint32_t)p.k : R.x[i]) * p.pitch_q + (uint32_t)(((lane % LPR) ^ Sh::swizzle(r)) * 16);
+    }
+    S.xso = (UP ? R.s / (uint32_t)p.k : R.s) * p.pitch_s;
     const ScaleRes C = scale_res<X8>(S, smem, 0, wave);
     dma(C.w, C.wto, S.wso);
     dma(C.x, C.xto, S.xso);
-  }
-  static_for<0, RING>([&](auto J) {
-    constexpr int j = decltype(J)::value;
-    const LoadRes<Sh> L = load_res<X8>(S, smem, j, j);
-    static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, X8>(L, S, wave); });
-  });
-  f32x16 acc[IA][JB];
-#pragma unroll
-  for (int i = 0; i < IA; ++i)
-#pragma unroll
-    for (int j = 0; j < JB; ++j) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-      asm volatile("" : "+a"(acc[i][j]));  // written here, inside the first loads' latency
-    }
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((RING - 1) * Sh::CL) : "memory");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  Frags<X8> F[2];
-  const FragAddr A0 = frag_addr<X8>(smem, 0, 0, wn, wm, lane);
-  static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value>(F[0], A0); });
-  int j = 0;
-  for (; j + RING <= S.nsteps; j += RING)
-    static_for<0, RING>([&](auto V) {
-      constexpr int v = decltype(V)::value;
-      step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
+    static_for<0, RING>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      const LoadRes<Sh> L = load_res<X8>(S, smem, j, j);
+      static_for<0, Sh::CL>([&](auto D) { load_piece<decltype(D)::value, X8>(L, S, wave); });
     });
-  static_for<0, RING - 1>([&](auto V) {
-    constexpr int v = decltype(V)::value;
-    if (j + v < S.nsteps) step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
-  });
-  __builtin_amdgcn_sched_barrier(0);
-  // The last MFMAs' results are read 20 wait states after them at the earliest; the
-  // compiler counts the scheduling directives above among its own.
+  };
+
+  Where tile = next_tile();
+  if (!tile.any) return;
+  start(tile, rows_of(tile));
+  Where next = next_tile();
+  Rows next_rows = rows_of(next.any ? next : tile);
+  while (true) {
+    f32x16 acc[IA][JB];
 #pragma unroll
-  for (int i = 0; i < IA; ++i) asm volatile("s_nop 15\n\ts_nop 7" : "+a"(acc[i][0]), "+a"(acc[i][1]));
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  if constexpr (UP)
-    store_h<X8, ACT>(acc, p, smem, tile, n0, wn, wm, lane);
-  else
-    store_o(acc, p, smem, tile, n0, wn, wm, lane);
+    for (int i = 0; i < IA; ++i)
+#pragma unroll
+      for (int j = 0; j < JB; ++j) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+        asm volatile("" : "+a"(acc[i][j]));  // written here, inside the first loads' latency
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    // (The rows' loads and the stores of the tile before are younger than these loads, and
+    // waited for as well.)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((RING - 1) * Sh::CL) : "memory");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    Frags<X8> F[2];
+    const FragAddr A0 = frag_addr<X8>(smem, 0, 0, wn, wm, lane);
+    static_for<0, Sh::NR>([&](auto R) { read_piece<decltype(R)::value>(F[0], A0); });
+    int j = 0;
+    for (; j + RING <= S.nsteps; j += RING)
+      static_for<0, RING>([&](auto V) {
+        constexpr int v = decltype(V)::value;
+        step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
+      });
+    static_for<0, RING - 1>([&](auto V) {
+      constexpr int v = decltype(V)::value;
+      if (j + v < S.nsteps) step<v>(acc, F[v % 2], F[(v + 1) % 2], S, smem, j + v, wave, wn, wm, lane);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+    // The last MFMAs' results are read 20 wait states after them at the earliest; the
+    // compiler counts the scheduling directives above among its own.
+#pragma unroll
+    for (int i = 0; i < IA; ++i) asm volatile("s_nop 15\n\ts_nop 7" : "+a"(acc[i][0]), "+a"(acc[i][1]));
+    // Every wave's last loads have landed and its last reads are done.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    const Where done = tile;
+    const bool more = next.any;
+    if (more) {
+      tile = next;
+      const Rows rows = next_rows;
+      next = next_tile();
+      next_rows = rows_of(next.any ? next : tile);
+      start(tile, rows);
+    }
+    if constexpr (UP)
+      store_h<X8, ACT>(acc, p, done, wn, wm, lane);
+    else
+      store_o(acc, p, done, wn, wm, lane);
+    if (!more) break;
+  }
 }
 
 template <bool UP, bool X8, int ACT>
@@ -410,7 +477,8 @@ hipError_t launch(ProductParams p, int64_t max_tiles, hipStream_t st) {
   const hipError_t e = allow_dynamic_lds((const void*)kern, Shape<X8>::LDS, configured);
   if (e != hipSuccess) return e;
   p.tiles_n = UP ? (p.I + 127) / 128 : (p.H + BN - 1) / BN;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(max_tiles * p.tiles_n)), dim3(NT), Shape<X8>::LDS, st, p);
+  const int64_t tiles = (max_tiles * p.tiles_n + 7) / 8 * 8;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles < kWorkgroups ? tiles : kWorkgroups)), dim3(NT), Shape<X8>::LDS, st, p);
   return hipGetLastError();
 }
 
