@@ -561,6 +561,9 @@ hipError_t launch_product(const ProductParams& p, int64_t max_tiles, hipStream_t
 // Tiles of 256 weight rows where an expert has many pairs.
 bool large_tiles(const ExpertsArgs& a) { return a.T * a.k >= 64 * a.E; }
 
+// A few tokens.
+bool few(const ExpertsArgs& a) { return a.T <= kFewTokens && a.T * a.k <= kFewPairs; }
+
 template <bool X8>
 hipError_t run(const ExpertsArgs& a, const ExpertsWorkspace& w, hipStream_t st) {
   uint8_t* base = (uint8_t*)a.workspace;
@@ -676,6 +679,31 @@ ExpertsWorkspace experts_workspace(int64_t T, int64_t k, int64_t E, int64_t H, i
 
 hipError_t launch_fp4_experts(const ExpertsArgs& a, hipStream_t stream) {
   const ExpertsWorkspace w = experts_workspace(a.T, a.k, a.E, a.H, a.I, a.fp4);
+  if (few(a)) {
+    FewParams p;
+    p.x = (const uint16_t*)a.x;
+    p.ldx = a.ldx;
+    p.ids = a.ids;
+    p.weights = a.weights;
+    p.T = (int)a.T;
+    p.k = (int)a.k;
+    p.E = (int)a.E;
+    p.H = (int)a.H;
+    p.I = (int)a.I;
+    p.RU = (int)slab_rows(2 * a.I);
+    p.RD = (int)slab_rows(a.H);
+    p.up_q = a.up_q;
+    p.up_s = a.up_s;
+    p.down_q = a.down_q;
+    p.down_s = a.down_s;
+    p.hq = (uint8_t*)a.workspace + w.hq;
+    p.hs = (uint8_t*)a.workspace + w.hs;
+    p.hpitch_q = w.hpitch_q;
+    p.hpitch_s = w.hpitch_s;
+    p.y = (uint16_t*)a.y;
+    p.tiles_n = 0;
+    return launch_experts_few(p, !a.fp4, a.gate, stream);
+  }
   return a.fp4 ? run<false>(a, w, stream) : run<true>(a, w, stream);
 }
 

@@ -35,6 +35,24 @@ struct ProductParams {
 // else o; gate: 0 SiLU, 1 GELU-tanh.
 hipError_t launch_experts_tile(const ProductParams& p, bool up, bool fp8, int gate, int64_t max_tiles, hipStream_t stream);
 
+// At most kFewTokens tokens with at most kFewPairs pairs (mx_experts_few.hip); h is
+// indexed by pair.
+constexpr int kFewTokens = 16, kFewPairs = 128;
+struct FewParams {
+  const uint16_t* x;
+  int64_t ldx;
+  const int32_t* ids;
+  const float* weights;
+  int T, k, E, H, I, RU, RD;  // RU, RD: padded rows of the weights
+  const uint8_t *up_q, *up_s, *down_q, *down_s;
+  uint8_t* hq;
+  uint8_t* hs;
+  uint32_t hpitch_q, hpitch_s;
+  uint16_t* y;
+  int tiles_n;
+};
+hipError_t launch_experts_few(const FewParams& p, bool fp8, int gate, hipStream_t stream);
+
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
