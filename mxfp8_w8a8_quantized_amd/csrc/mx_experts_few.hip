@@ -158,6 +158,7 @@ constexpr int DEPTH = 4;  // steps in flight a wave
 template <bool X8>
 __global__ __launch_bounds__(64 * DW, 4) void few_down_kernel(FewParams p) {
   __shared__ int32_t id[kPairs], lowest[kMaxExperts];
+  __shared__ float weight[kPairs];
   __shared__ int32_t expert[kPairs];            // of a slot
   __shared__ int32_t pair_of[kPairs][kTokens];  // a token's first pair of the slot's expert, or -1
   __shared__ float weight_of[kPairs][kTokens];
@@ -171,6 +172,7 @@ __global__ __launch_bounds__(64 * DW, 4) void few_down_kernel(FewParams p) {
   int e = -1;
   if (t < P) {
     e = p.ids[t];
+    weight[t] = p.weights[t];
     if (e >= p.E) e = -1;
     id[t] = e;
     if (e >= 0) lowest[e] = kPairs;
@@ -198,7 +200,7 @@ __global__ __launch_bounds__(64 * DW, 4) void few_down_kernel(FewParams p) {
     for (int j = tok * p.k; j < (tok + 1) * p.k; ++j)
       if (id[j] == e) {
         if (j < t) again = true;
-        w += p.weights[j];
+        w += weight[j];
       }
     if (!again) {
       pair_of[lowest[e]][tok] = t;
