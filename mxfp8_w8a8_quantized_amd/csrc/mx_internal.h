@@ -253,6 +253,7 @@ struct RouteArgs {
   float* weights;
   double factor;
   int f32, scores, E, groups, top_groups, k, renorm;
+  int vector;  // set by the launch: rows are read four logits at a time
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 

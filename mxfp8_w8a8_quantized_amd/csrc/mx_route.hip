@@ -10,14 +10,16 @@
 //   their sum if asked, times a factor
 //
 // A choice next to a tie is decided by its last bits, so scores that decide are
-// computed in f64 and rounded once; without a bias the order of the scores is that
-// of the logits and no score of a loser is computed at all (but for the sum of an
-// unnormalised softmax, in f32). Weights are computed in f64 for the k chosen.
+// computed in f64 (to 2^-42; see fast_exp2) and rounded once; without a bias the order
+// of the scores is that of the logits and no score of a loser is computed at all (but
+// for the sum of an unnormalised softmax, in f32). Weights are computed in f64 for the
+// k chosen.
 //
-// A team of L = 16 lanes (64 from 257 experts on) takes a token, expert i L + l
-// in lane l, so a wave takes four tokens and its maxima need four DPP steps. A round
-// of the choice is a maximum of order-preserving integer keys over the lanes' own
-// best, a minimum of the indices that have it, and a new scan by the lane that won.
+// A team of L = 16 lanes (64 from 257 experts on) takes a token, lane l experts l NE ..
+// + NE - 1, so a wave takes four tokens and its maxima need four DPP steps. A round of
+// the choice is a maximum of order-preserving integer keys over the lanes' best ones; the
+// lowest lane that has it takes its lowest expert with that key out and finds its next
+// best. Bound by VALU work: RESULT
 #include "mx_fp4_device.h"
 #include "mx_internal.h"
 
@@ -56,10 +58,6 @@ __device__ __forceinline__ uint32_t team_max(uint32_t v) {
   }
   return v;
 }
-template <int L>
-__device__ __forceinline__ uint32_t team_min(uint32_t v) {
-  return ~team_max<L>(~v);
-}
 template <int L, typename F>
 __device__ __forceinline__ F team_sum(F v) {
 #pragma unroll
@@ -67,13 +65,40 @@ __device__ __forceinline__ F team_sum(F v) {
   return v;
 }
 
+__device__ __forceinline__ float sane(float l) { return l != l ? -__builtin_inff() : fminf(l, kF32Max); }
 __device__ __forceinline__ float logit(const RouteArgs& p, int64_t t, int e) {
-  float l;
-  if (p.f32)
-    l = ((const float*)p.logits)[t * p.ld + e];
-  else
-    l = __uint_as_float((uint32_t)((const uint16_t*)p.logits)[t * p.ld + e] << 16);
-  return l != l ? -__builtin_inff() : fminf(l, kF32Max);
+  if (p.f32) return sane(((const float*)p.logits)[t * p.ld + e]);
+  return sane(__uint_as_float((uint32_t)((const uint16_t*)p.logits)[t * p.ld + e] << 16));
+}
+
+// 2^t for t <= 1000 to about 2^-42: 2^round(t) times the Taylor polynomial of degree 11
+// of the rest (|f| <= 1/2: the next term is (ln 2 / 2)^12 / 12! = 2^-47 of it). Below
+// f64's range the result is 0. The coefficients stay in scalar registers: left to
+// itself the compiler moves each constant anew before each use.
+struct Exp2 {
+  double k[12];
+  __device__ __forceinline__ Exp2() {
+    k[0] = 1.0;
+#pragma unroll
+    for (int i = 1; i < 12; ++i) k[i] = k[i - 1] * 0.693147180559945309417 / i;
+#pragma unroll
+    for (int i = 0; i < 12; ++i) asm volatile("" : "+s"(k[i]));
+  }
+  __device__ __forceinline__ double operator()(double t) const {
+    const double n = __builtin_rint(t), f = t - n;
+    double r = k[11];
+#pragma unroll
+    for (int i = 10; i >= 0; --i) r = __builtin_fma(r, f, k[i]);
+    return __builtin_amdgcn_ldexp(r, (int)n);
+  }
+};
+constexpr double kLog2e = 1.44269504088896340736;
+
+// 1 / d for d in [1, 2^1001): the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double fast_reciprocal(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
 }
 
 template <int L, int NE>
@@ -83,16 +108,38 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, team = lane / L, l = lane % L;
   const int64_t token = ((int64_t)blockIdx.x * kWaves + wave) * TEAMS + team;
   const int64_t t = token < p.T ? token : p.T - 1;  // the last waves repeat the last token
-  const int E = p.E, k = p.k;
+  const int E = p.E, k = p.k, e0 = l * NE;
 
   float v[NE];
   uint32_t key[NE];
+  if (p.vector) {  // rows of whole, aligned 16-byte pieces
 #pragma unroll
-  for (int i = 0; i < NE; ++i) v[i] = i * L + l < E ? logit(p, t, i * L + l) : -__builtin_inff();
+    for (int i = 0; i < NE; i += 4) {
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+      if (e0 + i < E) {
+        if (p.f32) {
+          const f32x4 q = *(const f32x4*)((const float*)p.logits + t * p.ld + e0 + i);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) f[u] = q[u];
+        } else {
+          const i32x2 q = *(const i32x2*)((const uint16_t*)p.logits + t * p.ld + e0 + i);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            f[u] = __uint_as_float((u & 1) ? (uint32_t)q[u >> 1] & 0xFFFF0000u : (uint32_t)q[u >> 1] << 16);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[i + u] = e0 + i < E ? sane(f[u]) : -__builtin_inff();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) v[i] = e0 + i < E ? logit(p, t, e0 + i) : -__builtin_inff();
+  }
 
   // Softmax: the largest logit, and the sum where it is needed.
   const bool softmax = p.scores == 0;
   double top = 0.0, sum = 1.0;
+  const Exp2 exp2_of;
   if (softmax) {
     uint32_t m = kNone;
 #pragma unroll
@@ -103,7 +150,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
     if (p.bias != nullptr) {
       sum = 0.0;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) sum += exp((double)v[i] - top);
+      for (int i = 0; i < NE; ++i)
+        sum += exp2_of(fmax(((double)v[i] - top) * kLog2e, -2000.0));
       sum = team_sum<L>(sum);
     } else if (!p.renorm) {
       float s = 0.f;
@@ -113,106 +161,139 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
     }
     if (!any) sum = 1.0;
   }
-  auto score = [&](float x) {
-    return softmax ? exp((double)x - top) / sum : 1.0 / (1.0 + exp(-(double)x));
-  };
+  if (p.bias != nullptr) {
+    const double scale = 1.0 / sum;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = i * L + l;
-    float c = v[i];
-    if (p.bias != nullptr && e < E && c > -__builtin_inff()) {
-      c = (float)(score(c) + (double)p.bias[e]);
-      if (c != c) c = -__builtin_inff();
+    for (int i = 0; i < NE; ++i) {
+      // (Masked logits give a score of 0 here and their own key below.)
+      const double x = (double)v[i];
+      const double s = softmax ? exp2_of(fmax((x - top) * kLog2e, -2000.0)) * scale
+                               : fast_reciprocal(1.0 + exp2_of(fmin(fmax(x * -kLog2e, -2000.0), 1000.0)));
+      const float c = (float)(s + (double)p.bias[e0 + i < E ? e0 + i : 0]);
+      v[i] = v[i] > -__builtin_inff() && c == c ? c : -__builtin_inff();
     }
-    key[i] = e < E ? key_of(c) : kNone;
   }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) key[i] = e0 + i < E ? key_of(v[i]) : kNone;
 
   if (p.groups > 1) {
     const int size = E / p.groups;
-    uint32_t* tab = table[wave][team];
+    auto score_of = [&](uint32_t b1, uint32_t b2) {
+      float c = value_of(b1);
+      if (p.bias != nullptr && b2 > kMasked) c += value_of(b2);
+      return c != c ? kMasked : key_of(c);
+    };
+    // A round takes the best group that is left, the lowest of equal ones.
+    if (size >= NE && size % NE == 0 && ((size / NE) & (size / NE - 1)) == 0) {
+      // Groups of 1, 2, 4, ... whole lanes: the two highest by lane, then across them.
+      const int lanes = size / NE;
+      uint32_t b1 = kMasked, b2 = kMasked;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) tab[i * L + l] = key[i];
-    __syncthreads();
-    uint32_t group[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      group[s] = kNone;
-      const int g = s * L + l;
-      if (g < p.groups) {
-        uint32_t b1 = kMasked, b2 = kMasked;
-        int at = l % size;  // lanes start at different banks
-        for (int i = 0; i < size; ++i) {
-          const uint32_t x = tab[g * size + at];
-          at = at + 1 == size ? 0 : at + 1;
-          b2 = max(b2, min(b1, x));
-          b1 = max(b1, x);
+      for (int i = 0; i < NE; ++i) {
+        b2 = max(b2, min(b1, key[i]));
+        b1 = max(b1, key[i]);
+      }
+      for (int off = 1; off < lanes; off <<= 1) {
+        const uint32_t o1 = (uint32_t)__shfl_xor((int)b1, off, 64), o2 = (uint32_t)__shfl_xor((int)b2, off, 64);
+        b2 = max(min(b1, o1), max(b2, o2));
+        b1 = max(b1, o1);
+      }
+      uint32_t group = e0 < E ? score_of(b1, b2) : kNone;  // of the lane's group
+      const uint32_t mine = (uint32_t)(l / lanes);
+      bool kept = false;
+      for (int r = 0; r < p.top_groups; ++r) {
+        const uint32_t b = team_max<L>(group);
+        const uint64_t has = __ballot(group == b) >> (team * L);
+        if ((uint32_t)__builtin_ctzll(has) / (uint32_t)lanes == mine) {
+          kept = true;
+          group = kNone;
         }
-        float c = value_of(b1);
-        if (p.bias != nullptr && b2 > kMasked) c += value_of(b2);
-        group[s] = c != c ? kMasked : key_of(c);
       }
-    }
-    uint64_t kept = 0;
-    for (int r = 0; r < p.top_groups; ++r) {
-      uint32_t b = kNone;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) b = max(b, group[s]);
-      b = team_max<L>(b);
-      uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-      for (int s = KS - 1; s >= 0; --s)
-        if (group[s] == b) at = (uint32_t)(s * L + l);
-      at = team_min<L>(at);
-      kept |= uint64_t(1) << at;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        if (at == (uint32_t)(s * L + l)) group[s] = kNone;
-    }
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = i * L + l;
-      if (e < E && !((kept >> (e / size)) & 1)) key[i] = kMasked;
-    }
-  }
-
-  // The choice. Output j is kept by lane j % L.
-  uint32_t best, at;
-  auto scan = [&]() {
-    best = kNone;
-    at = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = (uint32_t)(i * L + l);
-      }
-  };
-  scan();
-  uint32_t chosen[KS], with[KS];
-#pragma unroll
-  for (int s = 0; s < KS; ++s) chosen[s] = with[s] = 0;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t b = team_max<L>(best);
-    const uint32_t e = team_min<L>(best == b ? at : 0xFFFFFFFFu);
-#pragma unroll
-    for (int s = 0; s < KS; ++s)
-      if (s * L + l == j) {
-        chosen[s] = e;
-        with[s] = b;
-      }
-    if (at == e) {
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if ((uint32_t)(i * L + l) == e) key[i] = kNone;
-      scan();
+        if (e0 + i < E && !kept) key[i] = kMasked;
+    } else {
+      uint32_t* tab = table[wave][team];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) tab[e0 + i] = key[i];
+      __syncthreads();
+      uint32_t group[KS];  // of groups s L + l
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        group[s] = kNone;
+        const int g = s * L + l;
+        if (g < p.groups) {
+          uint32_t b1 = kMasked, b2 = kMasked;
+#pragma unroll 4
+          for (int i = 0; i < size; ++i) {
+            const uint32_t x = tab[g * size + i];
+            b2 = max(b2, min(b1, x));
+            b1 = max(b1, x);
+          }
+          group[s] = score_of(b1, b2);
+        }
+      }
+      uint64_t kept = 0;
+      for (int r = 0; r < p.top_groups; ++r) {
+        uint32_t b = kNone;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) b = max(b, group[s]);
+        b = team_max<L>(b);
+        int at = -1;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint64_t has = (__ballot(group[s] == b) >> (team * L)) & (L == 64 ? ~uint64_t(0) : (uint64_t(1) << (L & 63)) - 1);
+          if (at < 0 && has != 0) at = s * L + __builtin_ctzll(has);
+        }
+        kept |= uint64_t(1) << at;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          if (at == s * L + l) group[s] = kNone;
+      }
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1)) key[i] = kMasked;
+      __syncthreads();  // the table is written again below
     }
   }
 
+  // The choice: output j in the table.
+  uint32_t* out = table[wave][team];
+  uint32_t best = kNone;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) best = max(best, key[i]);
+  for (int j = 0; j < k; ++j) {
+    const uint32_t b = team_max<L>(best);
+    const uint64_t has = __ballot(best == b) >> (team * L);
+    if (l == (int)__builtin_ctzll(has)) {
+      int at = 0;
+      bool found = false;
+      best = kNone;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const bool hit = key[i] == b && !found;
+        key[i] = hit ? kNone : key[i];
+        at = hit ? i : at;
+        found = found || hit;
+        best = max(best, key[i]);
+      }
+      out[j] = (uint32_t)(e0 + at) | (b > kMasked ? 0u : 0x80000000u);
+    }
+  }
+  __syncthreads();
+
+  // Output s L + l in this lane.
   double w[KS], total = 0.0;
+  uint32_t chosen[KS];
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
-    const bool live = s * L + l < k && with[s] > kMasked;
-    w[s] = live ? score(logit(p, t, (int)chosen[s])) : 0.0;
+    const int j = s * L + l;
+    chosen[s] = j < k ? out[j] : 0x80000000u;
+    w[s] = 0.0;
+    if (!(chosen[s] >> 31)) {
+      const double x = (double)logit(p, t, (int)chosen[s]);
+      w[s] = softmax ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
+    }
     total += w[s];
   }
   if (p.renorm) {
@@ -225,7 +306,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
   for (int s = 0; s < KS; ++s) {
     const int j = s * L + l;
     if (j < k) {
-      p.ids[t * k + j] = (int32_t)chosen[s];
+      p.ids[t * k + j] = (int32_t)(chosen[s] & 0x7FFFFFFFu);
       p.weights[t * k + j] = (float)(w[s] * p.factor);
     }
   }
@@ -240,7 +321,10 @@ hipError_t launch(const RouteArgs& p, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& p, hipStream_t stream) {
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+  RouteArgs p = a;
+  const int es = p.f32 ? 4 : 2;
+  p.vector = p.E % 4 == 0 && (p.ld * es) % (4 * es) == 0 && (uintptr_t)p.logits % (uintptr_t)(4 * es) == 0;
   if (p.E <= 64) return launch<16, 4>(p, stream);
   if (p.E <= 128) return launch<16, 8>(p, stream);
   if (p.E <= 256) return launch<16, 16>(p, stream);
