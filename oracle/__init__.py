@@ -8,7 +8,8 @@ here imports the product package.
 Everything is plain numpy in float64 (float32 where the pages fix FP32
 scales). ``oracle/mx_oracle.py`` is the MXFP8 scheme, ``oracle/pc_oracle.py``
 the per-output-channel FP8 scheme; each function cites the passage it follows.
-``oracle/fp4_oracle.py`` is the MXFP4 scheme and the RMS norm.
+``oracle/fp4_oracle.py`` is the MXFP4 scheme and the RMS norm, ``oracle/moe_oracle.py``
+routing, the experts' products and the norms around a block.
 """
 
 from .mx_oracle import (  # noqa: F401
@@ -41,4 +42,12 @@ from .fp4_oracle import (  # noqa: F401
     pack_rows,
     quantize_fp4,
     rmsnorm_ref,
+)
+from .moe_oracle import (  # noqa: F401
+    activation_values,
+    block_h_ref,
+    block_y_ref,
+    experts_ref,
+    route_ref,
+    silu,
 )
