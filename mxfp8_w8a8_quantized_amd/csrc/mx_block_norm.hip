@@ -7,35 +7,46 @@
 //       h / sqrt(mean(h^2) + eps), or (h - mean h) / sqrt(var h + eps)
 //   q, s = the MX quantization of y (MXFP8 or MXFP4), where a slab is wanted
 //
-// One pass over memory, as in mx_norm.hip: a row stays in registers through up to
-// three sums (of x^2, of h, of the squares), 7 bytes an element with a bf16
-// residual.
+// One pass over memory: a row stays in registers through up to three sums (of x^2,
+// of h and h^2, and for an f32 residual of the squares around the mean), 7 bytes an
+// element with a bf16 residual and MXFP8 codes. Few rows take a block each, many are
+// tiled, a wave a row, with the codes passing through LDS.
 //
-// Products are f32: a conversion to f64 costs as much as four f32 operations, and
-// an element has up to nine of them (75348 x 5120 with gate, modulation and layer
-// norm: 1146 us in f64). Eight squares are added in f32, those sums in f64, so a
-// row's sum is off by at most 8 * 2^-24; a row whose squares leave f32's range is
-// summed again in f64 (SLOW below). The mean is subtracted in two parts. y is then
-// off by less than 2^-20 of its terms before it is rounded to 8 bits.
+// Sums and products are f64, each result rounded to f32 and then to its type: y is
+// next rounded to few bits, where a sum off in its last f32 bit moves a code. What
+// bounds it is the memory (5.2 TB/s would take 521 us for 75348 x 5120, bf16
+// residual), then the 37 to 45 vector operations an element, a quarter of them
+// conversions to f64. Measured there: RMS norm 656 us, with post norm 720, layer
+// norm 628, with gate and modulation 651 (4.1 TB/s; 842 before the rows' resources
+// lay in scalar registers and the options' choices were made once a chunk, 673 with
+// f32 products, which move one code in 1e4). 4096 x 5120: 39 us; one row: 5 us.
 #include "mx_internal.h"
 #include "mx_norm_device.h"
 
 namespace mx {
 namespace {
 
-// A vector's row for one row of x: an empty resource where there is none, whose
-// loads give zeros without touching memory; `rest` is then added (1 for factors), so
-// that the code has no branches and one chunk's vectors are on their way while the
-// chunk before is computed (gate, scale and shift of 75348 x 5120: 698 to RESULT us).
+// A vector's row for one row of x. Where there is none, its neutral values are
+// loaded instead, from the same eight for all k (mask 0), so that the code has no
+// branches and one chunk's vectors are on their way while the chunk before is
+// computed.
 struct Vector {
   __amdgpu_buffer_rsrc_t r;
-  float rest;
+  int mask;
 };
+// 1, -0 (which changes no sum, not a zero's sign either) and 0; f32, then bf16.
+__device__ const uint32_t kNeutral[3][2][8] = {
+    {{0x3F800000, 0x3F800000, 0x3F800000, 0x3F800000, 0x3F800000, 0x3F800000, 0x3F800000, 0x3F800000},
+     {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80}},
+    {{0x80000000, 0x80000000, 0x80000000, 0x80000000, 0x80000000, 0x80000000, 0x80000000, 0x80000000},
+     {0x80008000, 0x80008000, 0x80008000, 0x80008000}},
+    {{0, 0, 0, 0, 0, 0, 0, 0}, {0, 0, 0, 0}}};
+enum Neutral { ONE, NO_TERM, ZERO };
 template <bool VF32>
-__device__ __forceinline__ Vector vector_of(const BlockNormArgs& p, const void* v, int64_t row, int64_t ld, float rest) {
+__device__ __forceinline__ Vector vector_of(const BlockNormArgs& p, const void* v, int64_t row, int64_t ld, Neutral n) {
   constexpr int ES = VF32 ? 4 : 2;
-  return {make_rsrc(v == nullptr ? nullptr : (const uint8_t*)v + row * ld * ES, v == nullptr ? 0u : (uint32_t)p.K * ES),
-          v == nullptr ? rest : 0.f};
+  if (v == nullptr) return {make_rsrc(kNeutral[n][VF32 ? 0 : 1], 32u), 0};
+  return {make_rsrc((const uint8_t*)v + row * ld * ES, (uint32_t)p.K * ES), -1};
 }
 struct Vectors {
   Vector post, gate, weight, scale, shift;
@@ -43,9 +54,9 @@ struct Vectors {
 template <bool VF32>
 __device__ __forceinline__ Vectors vectors_of(const BlockNormArgs& p, int64_t row) {
   const int64_t g = row / p.gate_period, m = row / p.mod_period;
-  return {vector_of<VF32>(p, p.post_weight, 0, 0, 1.f), vector_of<VF32>(p, p.gate, g, p.ldg, 1.f),
-          vector_of<VF32>(p, p.weight, 0, 0, 1.f), vector_of<VF32>(p, p.scale, m, p.ldm, 0.f),
-          vector_of<VF32>(p, p.shift, m, p.ldm, 0.f)};
+  return {vector_of<VF32>(p, p.post_weight, 0, 0, ONE), vector_of<VF32>(p, p.gate, g, p.ldg, ONE),
+          vector_of<VF32>(p, p.weight, 0, 0, ONE), vector_of<VF32>(p, p.scale, m, p.ldm, ZERO),
+          vector_of<VF32>(p, p.shift, m, p.ldm, NO_TERM)};
 }
 
 // Eight consecutive values of a vector as loaded (past K zeros).
@@ -53,59 +64,49 @@ template <bool VF32>
 struct Eight {
   i32x4 w[VF32 ? 2 : 1];
   __device__ __forceinline__ void load(const Vector& v, int k) {
+    k &= v.mask;
     w[0] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(v.r, k * (VF32 ? 4 : 2), 0, 0));
     if constexpr (VF32) w[1] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(v.r, k * 4 + 16, 0, 0));
   }
-  __device__ __forceinline__ float at(int i) const {
+  __device__ __forceinline__ double at(int i) const {
     if constexpr (VF32) return __uint_as_float((uint32_t)w[i >> 2][i & 3]);
     return (i & 1) ? bf16_hi((uint32_t)w[0][i >> 1]) : bf16_lo((uint32_t)w[0][i >> 1]);
   }
 };
 
-// The squares' f32 sums cannot be relied on: too large, or so small that squares
-// vanished and eps does not hide it.
-__device__ __forceinline__ bool out_of_range(const BlockNormArgs& p, double sum) {
-  return !(sum < 1e38) || (sum < 1e-30 && p.eps * (double)p.K < 1e-20);
-}
 __device__ __forceinline__ double rstd_of(const BlockNormArgs& p, double sum) {
   return 1.0 / __builtin_sqrt(sum / (double)p.K + p.eps);
 }
 
-// Sums over a lane's elements value(c, i), chunk c < NCH with in(c), i < 8; SLOW in
-// f64.
-template <bool SLOW, bool SQUARES, int NCH, typename In, typename Value>
-__device__ __forceinline__ double sum_of(In&& in, Value&& value) {
-  double sum = 0.0;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    if constexpr (SLOW) {
-      double s = 0.0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double v = value(c, i);
-        s = SQUARES ? __builtin_fma(v, v, s) : s + v;
-      }
-      sum += in(c) ? s : 0.0;
-    } else {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = value(c, i);
-        s = SQUARES ? __builtin_fmaf(v, v, s) : s + v;
-      }
-      sum += (double)(in(c) ? s : 0.f);
-    }
-  }
-  return sum;
+// Rounds f64 to f32; the asm keeps the rounding to bf16 that follows apart (merged,
+// the compiler spells the two out in ten operations an element).
+__device__ __forceinline__ float round_f32(double d) {
+  float f = (float)d;
+  asm volatile("" : "+v"(f));
+  return f;
+}
+
+// A value that is the same in all lanes, in scalar registers.
+__device__ __forceinline__ double uniform(double v) {
+  const i32x2 w = __builtin_bit_cast(i32x2, v);
+  return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readfirstlane(w[0]), __builtin_amdgcn_readfirstlane(w[1])});
 }
 
 struct Statistics {
-  float mean, mean_low, rstd;  // mean + mean_low: the mean (0 for the RMS norm)
+  double mean, rstd;  // the mean is 0 for the RMS norm
 };
 
 // The wave's part of row `row`: chunks first, first + step, ... (NCH of them) of
 // 512 elements, 8 per lane. Computes and stores h, and returns the row's
-// statistics. total(i, v): the row's sum of its waves' i-th sums.
+// statistics. total(i, v): the row's sums of its waves' i-th sums v, in all lanes.
+//
+// The sums of h and h^2 are taken as h is made. For bf16 h the variance is their
+// difference: a value other than the largest is at least 2^-8 of it away, so a
+// variance that is not 0 is at least 2^-16 / K of the mean square. Where it is that
+// small all values but a few are the same, the sums of their 16-bit squares are
+// exact, and the mean's rounding, 2^-53 of the mean square, is 2^-21 of the variance
+// at the largest K, 65536. Values that are all the same leave exactly 0. f32 h is
+// summed again, around its mean.
 template <int RES, bool VF32, int NCH, typename Total>
 __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vectors& vec, int64_t row, int first, int step,
                                              int lane, Held<RES> (&h)[NCH], Total&& total) {
@@ -131,56 +132,50 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
       if constexpr (RES == RES_F32) h[c].w[4 + u] = (uint32_t)rb[u];
     }
   }
-  auto hold_x = [&]() {  // as hold() below, of x
+  // Elements past K are zeros, but not the mean away from it.
+  auto in = [&](int c) { return (first + c * step) * 512 + 8 * lane < p.K; };
+  auto x_at = [&](int c, int i) -> double {
+    return (i & 1) ? bf16_hi((uint32_t)xv[c][i >> 1]) : bf16_lo((uint32_t)xv[c][i >> 1]);
+  };
+  double post = 1.0;
+  if (p.post) {
+    double sum[1] = {0.0};
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c) {
+      double s = x_at(c, 0) * x_at(c, 0);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) s = __builtin_fma(x_at(c, i), x_at(c, i), s);
+      sum[0] += s;
+      // The conversions are made again below rather than kept.
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         int w = xv[c][u];
         asm volatile("" : "+v"(w));
         xv[c][u] = w;
       }
-  };
-  // Words of a second, rare pass over the same elements: values of their own to the
-  // compiler, which would keep the first pass's conversions for it.
-  auto again = [](uint32_t w) {
-    uint32_t zero = 0;
-    asm volatile("" : "+v"(zero));
-    return w ^ zero;
-  };
-  auto h_again = [&](int c, int i) -> double {
-    if constexpr (RES == RES_F32) return (double)__uint_as_float(again(h[c].w[i]));
-    const uint32_t w = again(h[c].w[i >> 1]);
-    return (double)((i & 1) ? bf16_hi(w) : bf16_lo(w));
-  };
-  // Elements past K are zeros, but not the mean away from it.
-  auto all = [](int) { return true; };
-  auto in = [&](int c) { return (first + c * step) * 512 + 8 * lane < p.K; };
-  auto x_at = [&](int c, int i) { return (i & 1) ? bf16_hi((uint32_t)xv[c][i >> 1]) : bf16_lo((uint32_t)xv[c][i >> 1]); };
-  float post = 1.f;
-  if (p.post) {
-    double sum = total(0, sum_of<false, true, NCH>(all, x_at));
-    if (out_of_range(p, sum))
-      sum = total(1, sum_of<true, true, NCH>(all, [&](int c, int i) -> double {
-                    const uint32_t w = again((uint32_t)xv[c][i >> 1]);
-                    return (double)((i & 1) ? bf16_hi(w) : bf16_lo(w));
-                  }));
-    hold_x();
-    post = (float)rstd_of(p, sum);
+    }
+    total(0, sum);
+    post = rstd_of(p, sum[0]);
   }
+  const double alpha = p.residual_scale;
+  double sums[2] = {0.0, 0.0};  // of h, of h^2
   Eight<VF32> pw, ga;
   pw.load(vec.post, first * 512 + 8 * lane);
   ga.load(vec.gate, first * 512 + 8 * lane);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int k = (first + c * step) * 512 + 8 * lane;
+    double g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = ga.at(i);
+    if (p.post) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] *= post * pw.at(i);
+    }
     float d[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d[i] = x_at(c, i) * post * (pw.at(i) + vec.post.rest);
-      d[i] *= ga.at(i) + vec.gate.rest;
-      d[i] = __builtin_fmaf(p.residual_scale, h[c].at(i), d[i]);
-    }
+    for (int i = 0; i < 8; ++i)
+      d[i] = round_f32(__builtin_fma(alpha, (double)h[c].at(i), x_at(c, i) * g[i]));
     if (c + 1 < NCH) {
       pw.load(vec.post, k + step * 512);
       ga.load(vec.gate, k + step * 512);
@@ -202,24 +197,42 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
             i32x4{(int)h[c].w[0], (int)h[c].w[1], (int)h[c].w[2], (int)h[c].w[3]};
       }
     }
+    double s = h[c].at(0), s2 = s * s;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const double v = h[c].at(i);
+      s += v;
+      s2 = __builtin_fma(v, v, s2);
+    }
+    sums[0] += s;
+    sums[1] += s2;
   }
-  Statistics st = {0.f, 0.f, 0.f};
-  double m = 0.0;
+  hold(h);
+  total(1, sums);
+  Statistics st = {0.0, 0.0};
   if (p.layer) {
-    auto at = [&](int c, int i) { return h[c].at(i); };
-    hold(h);
-    m = total(2, sum_of<false, false, NCH>(all, at));
-    if (!(__builtin_fabs(m) < 1e38)) m = total(3, sum_of<true, false, NCH>(all, h_again));
-    m /= (double)p.K;
-    st.mean = (float)m;
-    st.mean_low = (float)(m - (double)st.mean);
+    st.mean = uniform(sums[0] / (double)p.K);
+    if constexpr (RES == RES_F32) {
+      double sum[1] = {0.0};
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const double v = (double)h[c].at(i) - st.mean;
+          s = __builtin_fma(v, v, s);
+        }
+        sum[0] += in(c) ? s : 0.0;
+      }
+      hold(h);
+      total(3, sum);
+      sums[1] = sum[0];
+    } else {
+      const double var = __builtin_fma(-sums[0], st.mean, sums[1]);
+      sums[1] = var < 0.0 ? 0.0 : var;  // NaN stays
+    }
   }
-  hold(h);
-  double sum = total(4, sum_of<false, true, NCH>(in, [&](int c, int i) { return h[c].at(i) - st.mean - st.mean_low; }));
-  if (out_of_range(p, sum))
-    sum = total(5, sum_of<true, true, NCH>(in, [&](int c, int i) { return h_again(c, i) - m; }));
-  hold(h);
-  st.rstd = (float)rstd_of(p, sum);
+  st.rstd = uniform(rstd_of(p, sums[1]));
   return st;
 }
 
@@ -236,13 +249,23 @@ struct After {
 
 // The bf16 y of a lane's 8 elements at k, as packed pairs (zeros past K).
 template <int RES, bool VF32>
-__device__ __forceinline__ void make_y(const BlockNormArgs& p, const Vectors& vec, const After<VF32>& a, int64_t row,
+__device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32>& a, int64_t row,
                                        const Held<RES>& h, int k, const Statistics& st, uint32_t (&out)[4]) {
+  double g[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] = st.rstd;
+  if (p.weight != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= a.weight.at(i);
+  }
+  if (p.scale != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= 1.0 + a.scale.at(i);
+  }
   float d[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    d[i] = (h.at(i) - st.mean - st.mean_low) * st.rstd * (a.weight.at(i) + vec.weight.rest);
-    d[i] = __builtin_fmaf(d[i], a.scale.at(i), d[i]) + a.shift.at(i);
+    d[i] = round_f32(__builtin_fma((double)h.at(i) - st.mean, g[i], a.shift.at(i)));
   }
   const bool in = k < p.K;
 #pragma unroll
@@ -251,25 +274,26 @@ __device__ __forceinline__ void make_y(const BlockNormArgs& p, const Vectors& ve
     *(i32x4*)((uint16_t*)p.y + row * p.ldy + k) = i32x4{(int)out[0], (int)out[1], (int)out[2], (int)out[3]};
 }
 
-// Two blocks of 8 waves a CU where a row's registers allow it.
-constexpr int waves_wanted(int res, int nch) { return nch <= (res == RES_F32 ? 8 : 10) ? 4 : 2; }
-
-// Many rows: a block takes 8, a wave each; the codes pass through LDS.
+// Many rows: a block takes 8, a wave each; the codes pass through LDS. Two blocks a
+// CU.
 template <int RES, bool VF32, bool FP4, int NCH>
-__global__ __launch_bounds__(64 * kTileRows, waves_wanted(RES, NCH)) void block_norm_tile_kernel(BlockNormArgs p) {
+__global__ __launch_bounds__(64 * kTileRows, 4) void block_norm_tile_kernel(BlockNormArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using St = Stage<FP4>;
-  const int t = threadIdx.x, lane = t & 63, rl = t >> 6;
+  // The wave's number in a scalar register: its row and the resources follow.
+  const int t = threadIdx.x, lane = t & 63, rl = __builtin_amdgcn_readfirstlane(t >> 6);
   const int S = St::slabs((int)p.K);
   uint8_t* sc_lds = smem + S * St::kCodes;
   const int64_t r0 = (int64_t)xcd_order(blockIdx.x, gridDim.x) * kTileRows;
   const int64_t row = r0 + rl;
   const bool real = row < p.M;
   Held<RES> h[NCH];
-  Statistics stats = {0.f, 0.f, 0.f};
+  Statistics stats = {0.0, 0.0};
   const Vectors vec = vectors_of<VF32>(p, real ? row : p.M - 1);
   if (real) {
-    stats = make_h<RES, VF32, NCH>(p, vec, row, 0, 1, lane, h, [](int, double v) { return wave_sum(v); });
+    stats = make_h<RES, VF32, NCH>(p, vec, row, 0, 1, lane, h, [](int, auto& v) {
+      for (double& s : v) s = wave_sum(s);
+    });
   }
   After<VF32> after;
   after.load(vec, 8 * lane);
@@ -277,7 +301,7 @@ __global__ __launch_bounds__(64 * kTileRows, waves_wanted(RES, NCH)) void block_
   for (int ch = 0; ch < NCH; ++ch) {
     const int k = ch * 512 + 8 * lane;
     uint32_t v[4] = {0, 0, 0, 0};
-    if (real) make_y(p, vec, after, row, h[ch], k, stats, v);
+    if (real) make_y(p, after, row, h[ch], k, stats, v);
     if (ch + 1 < NCH) after.load(vec, k + 512);
     __builtin_amdgcn_sched_barrier(0);
     if (p.q == nullptr) continue;
@@ -322,7 +346,7 @@ __global__ __launch_bounds__(64 * kTileRows, waves_wanted(RES, NCH)) void block_
 // slab.
 template <int RES, bool VF32, bool FP4, int WPR, int NCH>
 __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs p) {
-  __shared__ double part[6][WPR];
+  __shared__ double part[4][WPR];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int S = Stage<FP4>::slabs((int)p.K);
   if ((int64_t)blockIdx.x >= p.M) {
@@ -341,14 +365,17 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
   const int64_t row = blockIdx.x;
   const Vectors vec = vectors_of<VF32>(p, row);
   Held<RES> h[NCH];
-  const Statistics stats = make_h<RES, VF32, NCH>(p, vec, row, wave, WPR, lane, h, [&](int i, double v) {
-    v = wave_sum(v);
-    if (lane == 0) part[i][wave] = v;
+  const Statistics stats = make_h<RES, VF32, NCH>(p, vec, row, wave, WPR, lane, h, [&](int i, auto& v) {
+    for (double& s : v) {
+      s = wave_sum(s);
+      if (lane == 0) part[i + (&s - v)][wave] = s;
+    }
     __syncthreads();
-    double sum = 0.0;
+    for (double& s : v) {
+      s = 0.0;
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) sum += part[i][w];
-    return sum;
+      for (int w = 0; w < WPR; ++w) s += part[i + (&s - v)][w];
+    }
   });
   After<VF32> after;
   after.load(vec, wave * 512 + 8 * lane);
@@ -357,7 +384,7 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
     const int ch = wave + c * WPR;
     const int k = ch * 512 + 8 * lane;
     uint32_t v[4];
-    make_y(p, vec, after, row, h[c], k, stats, v);
+    make_y(p, after, row, h[c], k, stats, v);
     if (c + 1 < NCH) after.load(vec, k + WPR * 512);
     if (p.q == nullptr) continue;
     if constexpr (FP4) {
@@ -398,19 +425,24 @@ hipError_t launch_row(const BlockNormArgs& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Rows from which the tiled form is taken, as in mx_norm.hip.
+// The tiled form writes whole lines of codes and shares no sums; the row form has
+// more rows on their way. Measured, tiled and row form, in us, the layer norm with
+// gate and modulation: K = 2048, 1024 rows 10.0 and 9.3, 2048 rows 11.0 and 14.5,
+// 32768 rows 126 and 166 (f32 residual 161 and 193); K = 4096, 16384 rows 140 and
+// 118, 32768 rows 238 and 242, 65536 rows 445 and 470; K = 5120, 16384 rows 163 and
+// 159, 65536 rows 590 and 635. Longer rows and f32 residuals beyond 2048 do not
+// leave enough registers (K = 8192, 65536 rows 1130 and 915; f32, K = 4096, 32768
+// rows 379 and 350).
 constexpr int64_t kTileMinRows = 32768;
 constexpr int64_t kTileMinRowsShort = 2048;  // K <= 2048
 
 template <int RES, bool VF32, bool FP4>
 hipError_t dispatch(const BlockNormArgs& p, hipStream_t st) {
   const int ch = (int)((p.K + 511) / 512);
-  if (p.M >= (ch <= 4 ? kTileMinRowsShort : kTileMinRows)) {
-    if (ch <= 4) return launch_tile<RES, VF32, FP4, 4>(p, st);
-    if (ch <= 8) return launch_tile<RES, VF32, FP4, 8>(p, st);
-    if (ch <= 10) return launch_tile<RES, VF32, FP4, 10>(p, st);
-    if constexpr (RES != RES_F32)  // an f32 row of 16 chunks does not fit the registers
-      if (ch <= 16) return launch_tile<RES, VF32, FP4, 16>(p, st);
+  if (ch <= 4 && p.M >= kTileMinRowsShort) return launch_tile<RES, VF32, FP4, 4>(p, st);
+  if constexpr (RES == RES_BF16) {
+    if (ch <= 8 && p.M >= kTileMinRows) return launch_tile<RES, VF32, FP4, 8>(p, st);
+    if (ch <= 10 && p.M >= kTileMinRows) return launch_tile<RES, VF32, FP4, 10>(p, st);
   }
   if (ch <= 8) return launch_row<RES, VF32, FP4, 4, 2>(p, st);
   if (ch <= 12) return launch_row<RES, VF32, FP4, 4, 3>(p, st);
