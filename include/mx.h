@@ -700,9 +700,12 @@ typedef enum { MX_GATE_SILU = 0, MX_GATE_GELU_TANH = 1 } mx_gate;
  *   y[t][n] = bf16_rne( sum_j w_j o_j )
  * with xhat the MX quantization of x (act: MXFP8 or MXFP4, the rule of
  * mx_quantize_act / mx_fp4_quantize_act_slab, for ahat too). Sums are FP32; the
- * products are added as in mx_fp4_linear_slab, the pairs in the order of j. A
- * pair whose id is outside 0 .. E-1 is skipped, whatever its weight (a token
- * with none gives a row of zeros); an expert may occur twice in a token's list.
+ * products are added as in mx_fp4_linear_slab, the pairs in the order of j (up to
+ * 16 tokens with at most 128 pairs: in that of the experts' first pairs in ids,
+ * the weights of an expert that occurs twice added first). With more, o_j is kept
+ * as 11-bit values with a power of two for each 32 columns. A pair whose id is
+ * outside 0 .. E-1 is skipped, whatever its weight (a token with none gives a row
+ * of zeros); an expert may occur twice in a token's list.
  * x: bf16 [T][ldx]; ids: int32 [T][k]; weights: f32 [T][k]; up: one MXFP4 slab
  * of 2 I rows and K = H (mx_fp4_quantize_weight_slab; the gate's rows first)
  * for each expert, up_q uint8 [E][ceil(H/128)][R/16][4][16][16], up_s uint8

@@ -15,6 +15,10 @@
 // other, the (expert, 128-K) steps in ranges over 8 waves; a token's column of an
 // expert's product is multiplied by its weight and added to the token's sum, so no o
 // goes through memory and nothing is left to combine.
+//
+// Bound by the memory. Measured with MXFP8 tokens: 1 token, E = 64, k = 8, H = 5120, I =
+// 2048: up 17.2 us (84 MB of codes, 4.9 TB/s), down 15.7 (42 MB, 2.7 TB/s: the waves'
+// ranges are 16 steps long); 13 tokens, k = 4, H = 4096, I = 1408: 43 and 26.5.
 #include "mx_experts_device.h"
 #include "mx_fp4_few_device.h"
 

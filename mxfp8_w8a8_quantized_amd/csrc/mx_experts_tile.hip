@@ -16,6 +16,12 @@
 // first 64 weight rows are Wg's and the other 64 Wu's for the same columns of h, so
 // that fragments 0 and 2, 1 and 3 hold both factors of an element, and 32 columns of h
 // lie in one fragment.
+//
+// Measured, 8192 tokens, E = 32, k = 4, H = 5120, I = 2048 with MXFP4 tokens: up 441 us
+// (3.1 PFLOP/s), down 315 (2.2). The up product without its stores takes 402 us, with
+// weights that stay in the L2 as well 365, without any loads 243: it is bound by the
+// memory's latency behind a ring of three steps, then by the stores' own time. 4001
+// tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 500 (2.1), down 311 (1.7).
 #include "mx_experts_device.h"
 
 namespace mx {
@@ -329,7 +335,8 @@ __device__ __forceinline__ void store_o(const f32x16 (&acc)[IA][JB], const Produ
 }
 
 // Workgroups stay for several tiles (256 of them, a CU each), so that a tile's first
-// loads are on their way while the output of the one before is written: RESULT
+// loads are on their way while the output of the one before is written
+// (the MXFP4 case above: up 446 to 441 us, down 331 to 315).
 template <bool UP, bool X8, int ACT>
 __global__ __launch_bounds__(NT, 1) void tile_kernel(ProductParams p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];

