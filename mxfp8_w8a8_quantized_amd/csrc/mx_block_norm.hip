@@ -15,11 +15,11 @@
 // Sums and products are f64, each result rounded to f32 and then to its type: y is
 // next rounded to few bits, where a sum off in its last f32 bit moves a code. What
 // bounds it is the memory (5.2 TB/s would take 521 us for 75348 x 5120, bf16
-// residual), then the 37 to 45 vector operations an element, a quarter of them
-// conversions to f64. Measured there: RMS norm 656 us, with post norm 720, layer
-// norm 628, with gate and modulation 651 (4.1 TB/s; 842 before the rows' resources
-// lay in scalar registers and the options' choices were made once a chunk, 673 with
-// f32 products, which move one code in 1e4). 4096 x 5120: 39 us; one row: 5 us.
+// residual), with gate, post norm or modulation the 37 to 45 vector operations an
+// element, a quarter of them conversions to f64. Measured there: RMS norm 550 us, layer
+// norm 546, with gate and modulation 640 (4.2 TB/s), RMS norm behind a post norm 725;
+// f32 products take 673 with gate and modulation, and move one code in 1e4.
+// 4096 x 5120: 39 us; one row: 5 us.
 #include "mx_internal.h"
 #include "mx_norm_device.h"
 
@@ -92,6 +92,13 @@ __device__ __forceinline__ double uniform(double v) {
   return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readfirstlane(w[0]), __builtin_amdgcn_readfirstlane(w[1])});
 }
 
+// What goes before h and what follows the norm, where a kernel is built for it: a
+// branch on an option costs the tiled form up to a tenth, the neutral values of what
+// is not there as much again (75348 x 5120, RMS norm with a weight: 666 us with both,
+// 546 without; layer norm with gate and modulation 663 and 639).
+enum Pre { PRE_ANY = -1, PRE_NONE, PRE_GATE, PRE_POST };  // PRE_POST: with or without a gate
+enum Mod { MOD_ANY = -1, MOD_NONE, MOD_SOME };
+
 struct Statistics {
   double mean, rstd;  // the mean is 0 for the RMS norm
 };
@@ -107,7 +114,7 @@ struct Statistics {
 // exact, and the mean's rounding, 2^-53 of the mean square, is 2^-21 of the variance
 // at the largest K, 65536. Values that are all the same leave exactly 0. f32 h is
 // summed again, around its mean.
-template <int RES, bool VF32, int NCH, typename Total>
+template <int RES, bool VF32, int PRE, int NCH, typename Total>
 __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vectors& vec, int64_t row, int first, int step,
                                              int lane, Held<RES> (&h)[NCH], Total&& total) {
   i32x4 xv[NCH];
@@ -138,7 +145,8 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
     return (i & 1) ? bf16_hi((uint32_t)xv[c][i >> 1]) : bf16_lo((uint32_t)xv[c][i >> 1]);
   };
   double post = 1.0;
-  if (p.post) {
+  const bool with_post = PRE == PRE_ANY ? p.post : PRE == PRE_POST;
+  if (with_post) {
     double sum[1] = {0.0};
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
@@ -160,15 +168,15 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
   const double alpha = p.residual_scale;
   double sums[2] = {0.0, 0.0};  // of h, of h^2
   Eight<VF32> pw, ga;
-  pw.load(vec.post, first * 512 + 8 * lane);
-  ga.load(vec.gate, first * 512 + 8 * lane);
+  if constexpr (PRE != PRE_NONE) ga.load(vec.gate, first * 512 + 8 * lane);
+  if constexpr (PRE == PRE_ANY || PRE == PRE_POST) pw.load(vec.post, first * 512 + 8 * lane);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int k = (first + c * step) * 512 + 8 * lane;
     double g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = ga.at(i);
-    if (p.post) {
+    for (int i = 0; i < 8; ++i) g[i] = PRE == PRE_NONE ? 1.0 : ga.at(i);
+    if (with_post) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] *= post * pw.at(i);
     }
@@ -177,8 +185,8 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
     for (int i = 0; i < 8; ++i)
       d[i] = round_f32(__builtin_fma(alpha, (double)h[c].at(i), x_at(c, i) * g[i]));
     if (c + 1 < NCH) {
-      pw.load(vec.post, k + step * 512);
-      ga.load(vec.gate, k + step * 512);
+      if constexpr (PRE != PRE_NONE) ga.load(vec.gate, k + step * 512);
+      if constexpr (PRE == PRE_ANY || PRE == PRE_POST) pw.load(vec.post, k + step * 512);
     }
     if constexpr (RES == RES_F32) {
 #pragma unroll
@@ -237,19 +245,21 @@ __device__ __forceinline__ Statistics make_h(const BlockNormArgs& p, const Vecto
 }
 
 // The vectors of a chunk's y.
-template <bool VF32>
+template <bool VF32, int MOD>
 struct After {
   Eight<VF32> weight, scale, shift;
   __device__ __forceinline__ void load(const Vectors& v, int k) {
     weight.load(v.weight, k);
-    scale.load(v.scale, k);
-    shift.load(v.shift, k);
+    if constexpr (MOD != MOD_NONE) {
+      scale.load(v.scale, k);
+      shift.load(v.shift, k);
+    }
   }
 };
 
 // The bf16 y of a lane's 8 elements at k, as packed pairs (zeros past K).
-template <int RES, bool VF32>
-__device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32>& a, int64_t row,
+template <int RES, bool VF32, int MOD>
+__device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32, MOD>& a, int64_t row,
                                        const Held<RES>& h, int k, const Statistics& st, uint32_t (&out)[4]) {
   double g[8];
 #pragma unroll
@@ -258,14 +268,14 @@ __device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32>
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] *= a.weight.at(i);
   }
-  if (p.scale != nullptr) {
+  if (MOD != MOD_NONE && p.scale != nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] *= 1.0 + a.scale.at(i);
   }
   float d[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    d[i] = round_f32(__builtin_fma((double)h.at(i) - st.mean, g[i], a.shift.at(i)));
+    d[i] = round_f32(__builtin_fma((double)h.at(i) - st.mean, g[i], MOD == MOD_NONE ? -0.0 : a.shift.at(i)));
   }
   const bool in = k < p.K;
 #pragma unroll
@@ -276,7 +286,7 @@ __device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32>
 
 // Many rows: a block takes 8, a wave each; the codes pass through LDS. Two blocks a
 // CU.
-template <int RES, bool VF32, bool FP4, int NCH>
+template <int RES, bool VF32, int PRE, int MOD, bool FP4, int NCH>
 __global__ __launch_bounds__(64 * kTileRows, 4) void block_norm_tile_kernel(BlockNormArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   using St = Stage<FP4>;
@@ -291,11 +301,11 @@ __global__ __launch_bounds__(64 * kTileRows, 4) void block_norm_tile_kernel(Bloc
   Statistics stats = {0.0, 0.0};
   const Vectors vec = vectors_of<VF32>(p, real ? row : p.M - 1);
   if (real) {
-    stats = make_h<RES, VF32, NCH>(p, vec, row, 0, 1, lane, h, [](int, auto& v) {
+    stats = make_h<RES, VF32, PRE, NCH>(p, vec, row, 0, 1, lane, h, [](int, auto& v) {
       for (double& s : v) s = wave_sum(s);
     });
   }
-  After<VF32> after;
+  After<VF32, MOD> after;
   after.load(vec, 8 * lane);
 #pragma unroll
   for (int ch = 0; ch < NCH; ++ch) {
@@ -365,7 +375,7 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
   const int64_t row = blockIdx.x;
   const Vectors vec = vectors_of<VF32>(p, row);
   Held<RES> h[NCH];
-  const Statistics stats = make_h<RES, VF32, NCH>(p, vec, row, wave, WPR, lane, h, [&](int i, auto& v) {
+  const Statistics stats = make_h<RES, VF32, PRE_ANY, NCH>(p, vec, row, wave, WPR, lane, h, [&](int i, auto& v) {
     for (double& s : v) {
       s = wave_sum(s);
       if (lane == 0) part[i + (&s - v)][wave] = s;
@@ -377,7 +387,7 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
       for (int w = 0; w < WPR; ++w) s += part[i + (&s - v)][w];
     }
   });
-  After<VF32> after;
+  After<VF32, MOD_ANY> after;
   after.load(vec, wave * 512 + 8 * lane);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
@@ -408,14 +418,25 @@ __global__ __launch_bounds__(64 * WPR) void block_norm_row_kernel(BlockNormArgs 
   }
 }
 
-template <int RES, bool VF32, bool FP4, int NCH>
+template <int RES, bool VF32, int PRE, int MOD, bool FP4, int NCH>
 hipError_t launch_tile(const BlockNormArgs& p, hipStream_t st) {
   static std::atomic<uint64_t> configured{0};  // per instantiation
-  auto kern = block_norm_tile_kernel<RES, VF32, FP4, NCH>;
+  auto kern = block_norm_tile_kernel<RES, VF32, PRE, MOD, FP4, NCH>;
   const hipError_t e = allow_dynamic_lds((const void*)kern, Stage<FP4>::bytes(512 * NCH), configured);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(p.R / kTileRows)), dim3(64 * kTileRows), Stage<FP4>::bytes((int)p.K), st, p);
   return hipGetLastError();
+}
+
+template <int RES, bool VF32, bool FP4, int NCH>
+hipError_t launch_tile(const BlockNormArgs& p, hipStream_t st) {
+  const bool mod = p.scale != nullptr || p.shift != nullptr;
+  if (p.post) return mod ? launch_tile<RES, VF32, PRE_POST, MOD_SOME, FP4, NCH>(p, st)
+                         : launch_tile<RES, VF32, PRE_POST, MOD_NONE, FP4, NCH>(p, st);
+  if (p.gate != nullptr) return mod ? launch_tile<RES, VF32, PRE_GATE, MOD_SOME, FP4, NCH>(p, st)
+                                    : launch_tile<RES, VF32, PRE_GATE, MOD_NONE, FP4, NCH>(p, st);
+  return mod ? launch_tile<RES, VF32, PRE_NONE, MOD_SOME, FP4, NCH>(p, st)
+             : launch_tile<RES, VF32, PRE_NONE, MOD_NONE, FP4, NCH>(p, st);
 }
 
 template <int RES, bool VF32, bool FP4, int WPR, int NCH>

@@ -20,7 +20,7 @@
 // Measured, 8192 tokens, E = 32, k = 4, H = 5120, I = 2048 with MXFP4 tokens: up 441 us
 // (3.1 PFLOP/s), down 315 (2.2). The up product without its stores takes 402 us, with
 // weights that stay in the L2 as well 365, without any loads 243: it is bound by the
-// memory's latency behind a ring of three steps, then by the stores' own time. 4001
+// path of the loads (a ring of five or six regions changes nothing), then by the stores' own time. 4001
 // tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 500 (2.1), down 311 (1.7).
 #include "mx_experts_device.h"
 
