@@ -24,6 +24,7 @@ HIP_FLAGS = [
     "-target-feature",
     "-Xclang",
     "-packed-fp32-ops",
+    "-parallel-jobs=8",  # sources at a time
 ]
 
 
