@@ -17,11 +17,12 @@
 // that fragments 0 and 2, 1 and 3 hold both factors of an element, and 32 columns of h
 // lie in one fragment.
 //
-// Measured, 8192 tokens, E = 32, k = 4, H = 5120, I = 2048 with MXFP4 tokens: up 441 us
-// (3.1 PFLOP/s), down 315 (2.2). The up product without its stores takes 402 us, with
+// Measured, 8192 tokens, E = 32, k = 4, H = 5120, I = 2048 with MXFP4 tokens: up 431 us
+// (3.2 PFLOP/s), down 309 (2.2). The up product without its stores takes 402 us, with
 // weights that stay in the L2 as well 365, without any loads 243: it is bound by the
-// path of the loads (a ring of five or six regions changes nothing), then by the stores' own time. 4001
-// tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 500 (2.1), down 311 (1.7).
+// loads' bytes (five or six regions, eight waves of 64 x 64, other groupings of the
+// tiles take the same time), then by the stores. 4001 tokens, E = 64, k = 8, H = 4096
+// with MXFP8 tokens: up 485 (2.2), down 310 (1.7).
 #include "mx_experts_device.h"
 
 namespace mx {
