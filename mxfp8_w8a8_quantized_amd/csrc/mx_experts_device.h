@@ -109,9 +109,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, p);
 }
 
-// o is kept as f16 with a power of two for each 32 columns of a row: 2^-12 of a value at
+// o is kept as f16 with a power of two for each 32 columns of a row: 2^-11 of a value at
 // most is lost (f32 would be 2^-24, and twice the bytes written here and read by the
-// sum; bf16 2^-9, as much as y's own rounding). The largest of the 32 is brought to
+// sum; bf16 2^-8, as much as y's own rounding). The largest of the 32 is brought to
 // [2^14, 2^15); values under 2^-28 of it lose bits. `e` is its biased f32 exponent, in
 // 15 .. 254. A lane holds 16 of a fragment's 32 columns of a pair, lane ^ 32 the others.
 __device__ __forceinline__ uint32_t o_exponent(const f32x16& a) {
