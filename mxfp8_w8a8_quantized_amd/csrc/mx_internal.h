@@ -253,7 +253,8 @@ struct RouteArgs {
   float* weights;
   double factor;
   int f32, scores, E, groups, top_groups, k, renorm;
-  int vector;  // set by the launch: rows are read four logits at a time
+  // Set by the launch: rows, and the bias, are read four values at a time.
+  int vector, vector_bias;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 

@@ -10,18 +10,18 @@
 //   their sum if asked, times a factor
 //
 // A choice next to a tie is decided by its last bits, so scores that decide are
-// computed in f64 (to 2^-42; see fast_exp2) and rounded once; without a bias the order
+// computed in f64 (to 2^-42; see Exp2) and rounded once; without a bias the order
 // of the scores is that of the logits and no score of a loser is computed at all (but
 // for the sum of an unnormalised softmax, in f32). Weights are computed in f64 for the
 // k chosen.
 //
 // A team of L = 16 lanes (64 from 257 experts on) takes a token, lane l experts l NE ..
-// + NE - 1, so a wave takes four tokens and its maxima need four DPP steps. A round of
-// the choice is a maximum of order-preserving integer keys over the lanes' best ones; the
-// lowest lane that has it takes its lowest expert with that key out and finds its next
-// best. A few tokens take a launch's time. Many are bound by VALU work, the scores'
+// + NE - 1, so a wave takes four tokens and its maxima need four DPP steps. A lane sorts
+// its keys (order-preserving integers) once; a round of the choice is a maximum over the
+// lanes' first ones, which the lowest lane that has it takes out. Which expert of the lane
+// it was is looked up at the end. A few tokens take a launch's time. Many are bound by VALU work, the scores'
 // f64 exponentials and the rounds in equal parts: 32001 tokens x 256 experts, k = 8 of
-// 4 out of 8 groups, sigmoid with a bias, 33 us; the logits alone would take 7.
+// 4 out of 8 groups, sigmoid with a bias, 27 us; the logits alone would take 7.
 #include "mx_fp4_device.h"
 #include "mx_internal.h"
 
@@ -73,40 +73,65 @@ __device__ __forceinline__ float logit(const RouteArgs& p, int64_t t, int e) {
   return sane(__uint_as_float((uint32_t)((const uint16_t*)p.logits)[t * p.ld + e] << 16));
 }
 
-// 2^t for t <= 1000 to about 2^-42: 2^round(t) times the Taylor polynomial of degree 11
-// of the rest (|f| <= 1/2: the next term is (ln 2 / 2)^12 / 12! = 2^-47 of it). Below
-// f64's range the result is 0. The coefficients stay in scalar registers: left to
+// 2^t for t <= 1000 to 2^-44: 2^round(t) times 1 + f q(f) of the rest f, |f| <= 1/2,
+// where q interpolates (2^f - 1) / f in the nine Chebyshev nodes (2^0 is 1 exactly).
+// Below f64's range the result is 0. The coefficients stay in scalar registers: left to
 // itself the compiler moves each constant anew before each use.
 struct Exp2 {
-  double k[12];
+  double k[10] = {1.0,
+                  0x1.62e42fefa39efp-1,
+                  0x1.ebfbdff823cedp-3,
+                  0x1.c6b08d7047e52p-5,
+                  0x1.3b2ab7181b755p-7,
+                  0x1.5d87fe86fe88ep-10,
+                  0x1.4308ac85aa947p-13,
+                  0x1.ffcb9515a8016p-17,
+                  0x1.63d136366db24p-20,
+                  0x1.b63880a30e9ffp-24};
   __device__ __forceinline__ Exp2() {
-    k[0] = 1.0;
 #pragma unroll
-    for (int i = 1; i < 12; ++i) k[i] = k[i - 1] * 0.693147180559945309417 / i;
-#pragma unroll
-    for (int i = 0; i < 12; ++i) asm volatile("" : "+s"(k[i]));
+    for (int i = 0; i < 10; ++i) asm volatile("" : "+s"(k[i]));
   }
   __device__ __forceinline__ double operator()(double t) const {
     const double n = __builtin_rint(t), f = t - n;
-    double r = k[11];
+    double r = k[9];
 #pragma unroll
-    for (int i = 10; i >= 0; --i) r = __builtin_fma(r, f, k[i]);
+    for (int i = 8; i >= 0; --i) r = __builtin_fma(r, f, k[i]);
     return __builtin_amdgcn_ldexp(r, (int)n);
   }
 };
 constexpr double kLog2e = 1.44269504088896340736;
 
-// 1 / d for d in [1, 2^1001): the hardware's estimate and two Newton steps.
+// 1 / d for d in [1, 2^1001): the hardware's estimate (off by 2^-24.3 at most, measured)
+// and a Newton step.
 __device__ __forceinline__ double fast_reciprocal(double d) {
-  double r = __builtin_amdgcn_rcp(d);
-  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  const double r = __builtin_amdgcn_rcp(d);
   return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+
+// Falling order (Batcher's odd-even merges of runs of 1, 2, 4, ...).
+template <int N>
+__device__ __forceinline__ void sort_falling(uint32_t (&a)[N]) {
+#pragma unroll
+  for (int run = 1; run < N; run *= 2)
+#pragma unroll
+    for (int d = run; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = d % run; i + d < N; i += 2 * d)
+#pragma unroll
+        for (int u = i; u < i + d; ++u)
+          if (u + d < N && u / (2 * run) == (u + d) / (2 * run)) {
+            const uint32_t x = a[u], y = a[u + d];
+            a[u] = max(x, y);
+            a[u + d] = min(x, y);
+          }
 }
 
 template <int L, int NE>
 __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
   constexpr int TEAMS = 64 / L, KS = 64 / L;  // tokens a wave; outputs (and groups) a lane
-  __shared__ uint32_t table[kWaves][TEAMS][L * NE];
+  __shared__ __attribute__((aligned(16))) uint32_t table[kWaves][TEAMS][L * NE];  // keys
+  __shared__ uint2 taken[kWaves][TEAMS][64];                                      // the choice: key; lane, rank
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, team = lane / L, l = lane % L;
   const int64_t token = ((int64_t)blockIdx.x * kWaves + wave) * TEAMS + team;
   const int64_t t = token < p.T ? token : p.T - 1;  // the last waves repeat the last token
@@ -164,20 +189,42 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
     if (!any) sum = 1.0;
   }
   if (p.bias != nullptr) {
-    const double scale = 1.0 / sum;
+    float bias[NE];
+    if (p.vector_bias) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      // (Masked logits give a score of 0 here and their own key below.)
-      const double x = (double)v[i];
-      const double s = softmax ? exp2_of(fmax((x - top) * kLog2e, -2000.0)) * scale
-                               : fast_reciprocal(1.0 + exp2_of(fmin(fmax(x * -kLog2e, -2000.0), 1000.0)));
-      const float c = (float)(s + (double)p.bias[e0 + i < E ? e0 + i : 0]);
+      for (int i = 0; i < NE; i += 4) {
+        const f32x4 q = *(const f32x4*)(p.bias + (e0 + i < E ? e0 + i : 0));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) bias[i + u] = q[u];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) bias[i] = p.bias[e0 + i < E ? e0 + i : 0];
+    }
+    // (Masked logits give a score of 0 here and their own key.)
+    auto take = [&](int i, double s) {
+      const float c = (float)(s + (double)bias[i]);
       v[i] = v[i] > -__builtin_inff() && c == c ? c : -__builtin_inff();
+    };
+    if (softmax) {
+      const double scale = 1.0 / sum;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) take(i, exp2_of(fmax(((double)v[i] - top) * kLog2e, -2000.0)) * scale);
+    } else {
+      // Past +-690 the score is 1, or vanishes in f32.
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        take(i, fast_reciprocal(1.0 + exp2_of((double)__builtin_amdgcn_fmed3f(v[i], -690.f, 690.f) * -kLog2e)));
     }
   }
 #pragma unroll
   for (int i = 0; i < NE; ++i) key[i] = e0 + i < E ? key_of(v[i]) : kNone;
 
+  // A lane's keys in falling order: the choice takes them from the front. Where each
+  // comes from is looked up at the end, in the table.
+  uint32_t sorted[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) sorted[i] = key[i];
   if (p.groups > 1) {
     const int size = E / p.groups;
     auto score_of = [&](uint32_t b1, uint32_t b2) {
@@ -189,12 +236,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
     if (size >= NE && size % NE == 0 && ((size / NE) & (size / NE - 1)) == 0) {
       // Groups of 1, 2, 4, ... whole lanes: the two highest by lane, then across them.
       const int lanes = size / NE;
-      uint32_t b1 = kMasked, b2 = kMasked;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        b2 = max(b2, min(b1, key[i]));
-        b1 = max(b1, key[i]);
-      }
+      sort_falling(sorted);
+      uint32_t b1 = max(kMasked, sorted[0]), b2 = max(kMasked, sorted[1]);
       for (int off = 1; off < lanes; off <<= 1) {
         const uint32_t o1 = (uint32_t)__shfl_xor((int)b1, off, 64), o2 = (uint32_t)__shfl_xor((int)b2, off, 64);
         b2 = max(min(b1, o1), max(b2, o2));
@@ -213,7 +256,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
       }
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (e0 + i < E && !kept) key[i] = kMasked;
+        if (e0 < E && !kept) key[i] = sorted[i] = kMasked;
     } else {
       uint32_t* tab = table[wave][team];
 #pragma unroll
@@ -256,32 +299,33 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
       for (int i = 0; i < NE; ++i)
         if (e0 + i < E && !((kept >> ((e0 + i) / size)) & 1)) key[i] = kMasked;
       __syncthreads();  // the table is written again below
+#pragma unroll
+      for (int i = 0; i < NE; ++i) sorted[i] = key[i];
+      sort_falling(sorted);
     }
+  } else {
+    sort_falling(sorted);
   }
 
-  // The choice: output j in the table.
-  uint32_t* out = table[wave][team];
-  uint32_t best = kNone;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) best = max(best, key[i]);
+  // The choice: output j is the rank-th of its lane's experts with that key.
+  uint2* out = taken[wave][team];
+  uint32_t before = kNone, rank = 0;
   for (int j = 0; j < k; ++j) {
-    const uint32_t b = team_max<L>(best);
-    const uint64_t has = __ballot(best == b) >> (team * L);
+    const uint32_t b = team_max<L>(sorted[0]);
+    const uint64_t has = __ballot(sorted[0] == b) >> (team * L);
     if (l == (int)__builtin_ctzll(has)) {
-      int at = 0;
-      bool found = false;
-      best = kNone;
+      rank = b == before ? rank + 1 : 0;
+      before = b;
+      out[j] = uint2{b, (uint32_t)l | rank << 8};
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const bool hit = key[i] == b && !found;
-        key[i] = hit ? kNone : key[i];
-        at = hit ? i : at;
-        found = found || hit;
-        best = max(best, key[i]);
-      }
-      out[j] = (uint32_t)(e0 + at) | (b > kMasked ? 0u : 0x80000000u);
+      for (int i = 0; i + 1 < NE; ++i) sorted[i] = sorted[i + 1];
+      sorted[NE - 1] = kNone;
     }
   }
+  uint32_t* tab = table[wave][team];
+#pragma unroll
+  for (int i = 0; i < NE; i += 4)
+    *(i32x4*)(tab + e0 + i) = i32x4{(int)key[i], (int)key[i + 1], (int)key[i + 2], (int)key[i + 3]};
   __syncthreads();
 
   // Output s L + l in this lane.
@@ -290,8 +334,21 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     const int j = s * L + l;
-    chosen[s] = j < k ? out[j] : 0x80000000u;
+    chosen[s] = 0x80000000u;
     w[s] = 0.0;
+    if (j < k) {
+      const uint2 o = out[j];
+      const int first = (int)(o.y & 0xFF) * NE;
+      uint32_t same = 0;  // the lane's experts with this key
+#pragma unroll
+      for (int i = NE - 4; i >= 0; i -= 4) {
+        const i32x4 q = *(const i32x4*)(tab + first + i);
+#pragma unroll
+        for (int u = 3; u >= 0; --u) same = 2 * same + ((uint32_t)q[u] == o.x ? 1u : 0u);
+      }
+      for (uint32_t n = o.y >> 8; n > 0; --n) same &= same - 1;
+      chosen[s] = (uint32_t)(first + __builtin_ctz(same)) | (o.x > kMasked ? 0u : 0x80000000u);
+    }
     if (!(chosen[s] >> 31)) {
       const double x = (double)logit(p, t, (int)chosen[s]);
       w[s] = softmax ? exp(x - top) / sum : 1.0 / (1.0 + exp(-x));
@@ -326,6 +383,7 @@ hipError_t launch(const RouteArgs& p, hipStream_t st) {
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
   RouteArgs p = a;
   const int es = p.f32 ? 4 : 2;
+  p.vector_bias = p.E % 4 == 0 && (uintptr_t)p.bias % 16 == 0;
   p.vector = p.E % 4 == 0 && (p.ld * es) % (4 * es) == 0 && (uintptr_t)p.logits % (uintptr_t)(4 * es) == 0;
   if (p.E <= 64) return launch<16, 4>(p, stream);
   if (p.E <= 128) return launch<16, 8>(p, stream);
