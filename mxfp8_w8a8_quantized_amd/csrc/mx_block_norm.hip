@@ -262,15 +262,15 @@ template <int RES, bool VF32, int MOD>
 __device__ __forceinline__ void make_y(const BlockNormArgs& p, const After<VF32, MOD>& a, int64_t row,
                                        const Held<RES>& h, int k, const Statistics& st, uint32_t (&out)[4]) {
   double g[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = st.rstd;
   if (p.weight != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] *= a.weight.at(i);
-  }
-  if (MOD != MOD_NONE && p.scale != nullptr) {
+    for (int i = 0; i < 8; ++i) {
+      g[i] = st.rstd * a.weight.at(i);
+      if constexpr (MOD != MOD_NONE) g[i] *= 1.0 + a.scale.at(i);
+    }
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] *= 1.0 + a.scale.at(i);
+    for (int i = 0; i < 8; ++i) g[i] = MOD == MOD_NONE ? st.rstd : __builtin_fma(st.rstd, a.scale.at(i), st.rstd);
   }
   float d[8];
 #pragma unroll
