@@ -647,8 +647,9 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
  * q, s: the slab, or both NULL for none (then y is needed; act is ignored and K a
  * multiple of 32). Outputs must otherwise overlap nothing. Every buffer 16-byte
  * aligned, rows a multiple of 16 bytes apart; pitches, dtypes and row counts of
- * NULL pointers are ignored. eps >= 0 and finite, residual_scale finite. K as the
- * format requires, at most 65536, M at most 2^22 (else MX_ERR_UNSUPPORTED).
+ * NULL pointers are ignored. eps >= 0 and finite, residual_scale (used as given, in
+ * f64) finite and within f32's range. K as the format requires, at most 65536, M at
+ * most 2^22 (else MX_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef enum { MX_NORM_RMS = 0, MX_NORM_LAYER = 1 } mx_norm_kind;
 int mx_block_norm_slab(const void* x, int64_t ldx, const void* residual, int rdtype, int64_t ldr,

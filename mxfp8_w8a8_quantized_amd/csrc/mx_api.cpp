@@ -1295,7 +1295,8 @@ extern "C" int mx_block_norm_slab(const void* x, int64_t ldx, const void* residu
   if (K > mx::kNormMaxK) return fail(MX_ERR_UNSUPPORTED, "K = %lld exceeds the norm's 65536", (long long)K);
   if (M > mx::kNormMaxRows) return fail(MX_ERR_UNSUPPORTED, "M = %lld exceeds the norm's 2^22", (long long)M);
   if (!(eps >= 0.0 && std::isfinite(eps))) return fail(MX_ERR_INVALID_ARGUMENT, "eps = %g must be finite and >= 0", eps);
-  if (!std::isfinite((float)residual_scale)) return fail(MX_ERR_INVALID_ARGUMENT, "residual_scale must be finite");
+  if (!std::isfinite((float)residual_scale))
+    return fail(MX_ERR_INVALID_ARGUMENT, "residual_scale = %g must lie in f32's range", residual_scale);
   if (rdtype != MX_DT_BF16 && rdtype != MX_DT_F32) return fail(MX_ERR_INVALID_ARGUMENT, "unknown residual dtype %d", rdtype);
   const bool vectors = post_weight != nullptr || gate != nullptr || weight != nullptr || scale != nullptr || shift != nullptr;
   if (vectors && vdtype != MX_DT_BF16 && vdtype != MX_DT_F32)
@@ -1358,7 +1359,7 @@ extern "C" int mx_block_norm_slab(const void* x, int64_t ldx, const void* residu
   a.ldx = ldx;
   a.residual = residual;
   a.ldr = ldr;
-  a.residual_scale = (float)residual_scale;
+  a.residual_scale = residual_scale;
   a.eps = eps;
   a.post_weight = post_weight;
   a.gate = gate;

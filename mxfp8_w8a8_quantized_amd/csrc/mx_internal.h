@@ -193,8 +193,7 @@ struct BlockNormArgs {
   int64_t ldx;
   const void* residual;
   int64_t ldr;
-  double eps;
-  float residual_scale;
+  double eps, residual_scale;
   const void *post_weight, *gate, *weight, *scale, *shift;
   int64_t gate_period, ldg, mod_period, ldm;
   int64_t M, R, K;  // R = slab_rows(M)

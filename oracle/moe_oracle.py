@@ -155,7 +155,7 @@ def block_h_ref(x, residual, residual_scale=1.0, post=False, post_weight=None, g
                 n = n * post_weight
         if gate is not None:
             n = n * gate
-        r = np.float64(np.float32(residual_scale)) * np.asarray(residual, dtype=np.float64)
+        r = np.float64(residual_scale) * np.asarray(residual, dtype=np.float64)
         return r + n, np.abs(r) + np.abs(n)
 
 
