@@ -12,8 +12,7 @@
 // A choice next to a tie is decided by its last bits, so scores that decide are
 // computed in f64 (to 2^-42; see Exp2) and rounded once; without a bias the order
 // of the scores is that of the logits and no score of a loser is computed at all (but
-// for the sum of an unnormalised softmax, in f32). Weights are computed in f64 for the
-// k chosen.
+// for the sum of an unnormalised softmax). Weights are computed in f64 for the k chosen.
 //
 // A team of L = 16 lanes (64 from 257 experts on) takes a token, lane l experts l NE ..
 // + NE - 1, so a wave takes four tokens and its maxima need four DPP steps. A lane sorts
@@ -176,17 +175,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
     const float f = value_of(team_max<L>(m));
     const bool any = f > -__builtin_inff();
     top = any ? (double)f : 0.0;
-    if (p.bias != nullptr) {
+    if (p.bias != nullptr || !p.renorm) {
       sum = 0.0;
 #pragma unroll
       for (int i = 0; i < NE; ++i)
         sum += exp2_of(fmax(((double)v[i] - top) * kLog2e, -2000.0));
       sum = team_sum<L>(sum);
-    } else if (!p.renorm) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) s += __builtin_amdgcn_exp2f((v[i] - (float)top) * 1.4426950408889634f);
-      sum = (double)team_sum<L>(s);
     }
     if (!any) sum = 1.0;
   }
