@@ -367,11 +367,20 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs p) {
   }
 }
 
+// A launch has fewer than 2^32 threads: 2^26 tokens of 64 lanes each take two.
 template <int L, int NE>
-hipError_t launch(const RouteArgs& p, hipStream_t st) {
-  const int64_t per_block = (int64_t)kWaves * (64 / L);
-  hipLaunchKernelGGL((route_kernel<L, NE>), dim3((unsigned)((p.T + per_block - 1) / per_block)), dim3(64 * kWaves), 0, st, p);
-  return hipGetLastError();
+hipError_t launch(RouteArgs p, hipStream_t st) {
+  constexpr int64_t per_block = (int64_t)kWaves * (64 / L), most = (int64_t(1) << 23) * per_block;
+  for (int64_t left = p.T; left > 0; left -= p.T) {
+    p.T = left < most ? left : most;
+    hipLaunchKernelGGL((route_kernel<L, NE>), dim3((unsigned)((p.T + per_block - 1) / per_block)), dim3(64 * kWaves), 0, st, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.logits = (const uint8_t*)p.logits + p.T * p.ld * (p.f32 ? 4 : 2);
+    p.ids += p.T * p.k;
+    p.weights += p.T * p.k;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
