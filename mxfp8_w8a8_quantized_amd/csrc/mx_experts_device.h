@@ -111,16 +111,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // o is kept as f16 with a power of two for each 32 columns of a row: 2^-11 of a value at
 // most is lost (f32 would be 2^-24, and twice the bytes written here and read by the
-// sum; bf16 2^-8, as much as y's own rounding). The largest of the 32 is brought to
-// [2^14, 2^15); values under 2^-28 of it lose bits. `e` is its biased f32 exponent, in
-// 15 .. 254. A lane holds 16 of a fragment's 32 columns of a pair, lane ^ 32 the others.
+// sum; bf16 2^-8, as much as y's own rounding). The largest finite one of the 32 is
+// brought to [2^14, 2^15); values under 2^-28 of it lose bits. `e` is its biased f32
+// exponent, in 15 .. 254. A lane holds 16 of a fragment's 32 columns of a pair, lane ^ 32
+// the others.
 __device__ __forceinline__ uint32_t o_exponent(const f32x16& a) {
-  float m = 0.f;
+  auto both = [](uint32_t b) {
+    const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return max((uint32_t)sw[0], (uint32_t)sw[1]) >> 23;
+  };
+  float m = 0.f;  // (fmaxf passes over NaN)
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = fmaxf(m, __builtin_fabsf(a[i]));
-  const uint32_t b = __float_as_uint(m);
-  const auto sw = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return min(max(max((uint32_t)sw[0], (uint32_t)sw[1]) >> 23, 15u), 254u);
+  uint32_t e = both(__float_as_uint(m));
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(e == 255u) != 0, 0)) {  // an infinity: again without
+    uint32_t f = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t b = __float_as_uint(__builtin_fabsf(a[i]));
+      f = max(f, b < 0x7F800000u ? b : 0u);
+    }
+    e = both(f);
+  }
+  return min(max(e, 15u), 254u);
 }
 // The lane's 16 columns 8 q + 4 hi .. + 3 (q = 0 .. 3), two dwords for each q.
 __device__ __forceinline__ void o_pack(const f32x16& a, uint32_t e, uint32_t (&c)[8]) {
