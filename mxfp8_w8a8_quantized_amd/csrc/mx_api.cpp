@@ -1411,8 +1411,7 @@ int check_experts_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, i
   if (T * H >= (int64_t(1) << 31)) return fail(MX_ERR_UNSUPPORTED, "T H = %lld must be below 2^31", (long long)(T * H));
   // Every launch has fewer than 2^24 workgroups, of 256 threads.
   const int64_t tiles = mx::experts_max_tiles(T, k, E);
-  if (tiles * 2 * ((I + 127) / 128) >= kMaxSplitWorkgroups || tiles * ((H + 127) / 128) >= kMaxSplitWorkgroups ||
-      T * ((H + 1023) / 1024) >= kMaxSplitWorkgroups)
+  if (tiles * 2 * ((I + 127) / 128) >= kMaxSplitWorkgroups || tiles * ((H + 127) / 128) >= kMaxSplitWorkgroups)
     return fail(MX_ERR_UNSUPPORTED, "%lld pairs of %lld experts are too many for H = %lld, I = %lld", (long long)(T * k),
                 (long long)E, (long long)H, (long long)I);
   return MX_OK;
