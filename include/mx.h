@@ -635,8 +635,9 @@ int mx_rmsnorm_slab(const void* x, int64_t ldx, const void* residual, int rdtype
  *          (h - mean h) / sqrt(var h + eps)      (MX_NORM_LAYER, var over K)
  *   q, s = the MX quantization of y (act), as in mx_rmsnorm_slab
  * Means, sums and products are computed in f64; h and y are rounded to f32 and
- * that to bf16. A row holding NaN or Inf gives what the formula gives in floating
- * point.
+ * that to bf16. The variance of a bf16 h is mean h^2 - (mean h)^2, good to 2^-21 of
+ * itself at worst (65536 values that are all but equal). A row holding NaN or Inf
+ * gives what the formula gives in floating point.
  * x: bf16 [M][ldx]; residual: bf16 or f32 (rdtype) [M][ldr]; vectors of type
  * vdtype, each NULL for none: post_weight, weight [K]; gate [gate_rows][ldg],
  * scale and shift [mod_rows][ldm], whose row i serves rows i M / rows .. (i + 1) M
@@ -670,8 +671,9 @@ typedef enum { MX_ROUTE_SOFTMAX = 0, MX_ROUTE_SIGMOID = 1 } mx_route_scores;
 /* The k experts of every token, and their weights, from the router's logits:
  *   l = logits, NaN as -inf and +inf as the largest f32
  *   s = softmax(l) over the E experts, or 1 / (1 + exp(-l)); 0 where l = -inf
- *   c = l without a bias, f32(s + bias) with one (s in f64); -inf where l is
- *       (a masked expert) or where c is NaN
+ *   c = l without a bias, f32(s + bias) with one (s in f64, good to 2^-42 of it: a
+ *       sum that close to the middle of two f32 may be rounded to either); -inf
+ *       where l is (a masked expert) or where c is NaN
  * With groups > 1 (equal runs of E / groups experts) the top_groups best stay and
  * the others' c become -inf. A group's score is its highest c, with a bias the
  * f32 sum of its two highest (a second one of -inf adds nothing).

@@ -16,10 +16,12 @@
 // next rounded to few bits, where a sum off in its last f32 bit moves a code. What
 // bounds it is the memory (5.2 TB/s would take 521 us for 75348 x 5120, bf16
 // residual), with gate, post norm or modulation the 37 to 45 vector operations an
-// element, a quarter of them conversions to f64. Measured there: RMS norm 550 us, layer
-// norm 546, with gate and modulation 640 (4.2 TB/s), RMS norm behind a post norm 725;
-// f32 products take 673 with gate and modulation, and move one code in 1e4.
-// 4096 x 5120: 39 us; one row: 5 us.
+// element, a quarter of them conversions to f64. Measured there: RMS norm 555 us, layer
+// norm without a gain 547, with gate and modulation 634, and a gain besides 681 (4.0
+// TB/s), RMS norm behind a post norm 718; f32 products were no faster there, and move one
+// code in 1e4. 4096 x 5120: 38 us; one row: 6 us. Rows of more than 16384 elements have 16
+// chunks a wave and spill registers: 4096 x 20480 626 us (f32 residual 979), 114 (179) at
+// the copy's rate, where 4096 x 16384 takes 127.
 #include "mx_internal.h"
 #include "mx_norm_device.h"
 

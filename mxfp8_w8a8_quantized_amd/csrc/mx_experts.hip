@@ -566,11 +566,13 @@ hipError_t launch_product(const ProductParams& p, int64_t max_tiles, hipStream_t
   return hipGetLastError();
 }
 
-// Tiles of 256 weight rows where an expert has many pairs. Measured, 128-row tiles and
-// 256-row ones, in us: MXFP8 tokens, E = 32, H = 4096, I = 1408, k = 4: 64 pairs an
-// expert 119 and 112, 128 145 and 127, 512 401 and 371; E = 8, H = 5120, I = 2048: 64
-// 49 and 56, 128 64 and 62; E = 64, H = 2048, I = 768: 128 91 and 97. MXFP4, E = 32:
-// 128 130 and 115.
+// Tiles of 256 weight rows where an expert has many pairs, by the average over all E.
+// Measured, 128-row tiles and 256-row ones, in us: MXFP8 tokens, E = 32, H = 4096, I =
+// 1408, k = 4: 64 pairs an expert 119 and 112, 128 145 and 127, 512 401 and 371; E = 8, H
+// = 5120, I = 2048: 64 49 and 56, 128 64 and 62; E = 64, H = 2048, I = 768: 128 91 and 97.
+// MXFP4, E = 32: 128 130 and 115. So the average alone is a coarse rule: it leaves out how
+// the tiles fill the last round of workgroups, which loses 14% at the 64 pairs of E = 8
+// and 7% at the 128 of E = 64, and experts without a token count in it.
 bool large_tiles(const ExpertsArgs& a) { return a.T * a.k >= 64 * a.E; }
 
 // A few tokens, whose products read each expert's weights once in two launches. Measured

@@ -21,8 +21,11 @@
 // (3.2 PFLOP/s), down 309 (2.2). The up product without its stores takes 402 us, with
 // weights that stay in the L2 as well 365, without any loads 243. Five or six regions,
 // eight waves of 64 x 64, other groupings of the tiles, stores left in flight take the
-// same time: at 2.0 GHz of 2.4, loads and MFMAs share the power. 4001 tokens, E = 64, k =
-// 8, H = 4096 with MXFP8 tokens: up 485 (2.2), down 310 (1.7).
+// same time. MFMAs are busy 40% (up) and 25% (down) of the time at 2.0 to 2.3 GHz, where
+// mx_fp4_gemm.hip keeps them busy 68% at 1.6: they wait, for the gathered loads (64 or 128
+// bytes of a row, where the dense product reads 1 KB runs) and in an epilogue that no
+// MFMA overlaps. 4001 tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 485 (2.2),
+// down 310 (1.7).
 #include "mx_experts_device.h"
 
 namespace mx {

@@ -160,14 +160,15 @@ def block_h_ref(x, residual, residual_scale=1.0, post=False, post_weight=None, g
 
 
 def block_y_ref(h, kind="rms", weight=None, scale=None, shift=None, eps=1e-6):
-    """(y before its rounding, bound of the library's error before it) from h as
-    stored, float64.
+    """(y before its rounding, a bound that f32 arithmetic before it would keep) from h
+    as stored, float64.
 
-    The bound counts f32 roundings of 2^-24 of a term: a row's sum of squares 8 (its
-    f32 sums of 8; their sum is f64) and its differences from the mean 4, halved by
-    the root, rstd 1, products and the shift 6: under 2^-19 of the difference's term.
-    A mean is off by 8 2^-24 of the mean magnitude, in the difference and (again) in
-    the squares: under 2^-20 of it."""
+    The library computes in float64, so its own error is far smaller
+    (tests/test_gpu_block_norm_exact.py derives that bound). The one here counts f32
+    roundings of 2^-24 of a term: a row's sum of squares 8 (its f32 sums of 8; their sum
+    is f64) and its differences from the mean 4, halved by the root, rstd 1, products
+    and the shift 6: under 2^-19 of the difference's term. A mean is off by 8 2^-24 of
+    the mean magnitude, in the difference and (again) in the squares: under 2^-20 of it."""
     h = np.asarray(h, dtype=np.float64)
     with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
         m = np.mean(h, axis=-1, keepdims=True) if kind == "layer" else 0.0
