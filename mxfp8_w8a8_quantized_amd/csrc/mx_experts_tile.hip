@@ -22,9 +22,9 @@
 // weights that stay in the L2 as well 365, without any loads 243. Five or six regions,
 // eight waves of 64 x 64, other groupings of the tiles, stores left in flight take the
 // same time. MFMAs are busy 40% (up) and 25% (down) of the time at 2.0 to 2.3 GHz, where
-// mx_fp4_gemm.hip keeps them busy 68% at 1.6: they wait, for the gathered loads (64 or 128
-// bytes of a row, where the dense product reads 1 KB runs) and in an epilogue that no
-// MFMA overlaps. 4001 tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 485 (2.2),
+// mx_fp4_gemm.hip keeps them busy 68% at 1.6, so they wait. What differs from it: loads
+// gathered in pieces of 64 or 128 bytes where the dense product reads 1 KB runs, and an
+// epilogue that no MFMA overlaps. 4001 tokens, E = 64, k = 8, H = 4096 with MXFP8 tokens: up 485 (2.2),
 // down 310 (1.7).
 #include "mx_experts_device.h"
 
